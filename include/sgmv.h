@@ -355,6 +355,191 @@ int sgmv_copy_gather(int32_t n, void *const *dst, const void *const *src, const 
                      int32_t max_ctas, void *stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Speculative decoding over a paged KV cache: what a step of a multi-LoRA model
+ * runs between its projections.  (No counterpart on the pages, which leave
+ * attention and the cache to the serving engine.)
+ *
+ *   sgmv_rope            rotary positions of q and k, k and v appended to the cache
+ *   sgmv_tree_attention  attention of every sequence's drafted tokens over the cache
+ *   sgmv_tree_verify     which drafted tokens the target distribution accepts
+ *   sgmv_cache_commit    the accepted tokens' k and v moved to their final places
+ *
+ * Shared conventions.  The batch has T rows (tokens); sequence b owns the rows
+ * [tree_ptr[b], tree_ptr[b+1]), its "nodes" 0, 1, ....  parents[row] is the
+ * node's parent within its sequence: an earlier node, -1 for a node whose only
+ * ancestors are the tokens already in the cache, or -2 for a padding row.
+ * parents == NULL makes every sequence a chain (node i's parent is i - 1).  A
+ * sequence has at most SGMV_TREE_MAX_NODES nodes; empty sequences are allowed.
+ *
+ * The cache holds token position j of sequence b in page block_table[b][j /
+ * block_size], at offset j % block_size.  Positions 0 .. prefix_lens[b] - 1
+ * are the context; node i sits at position prefix_lens[b] + i.  k_cache and
+ * v_cache have the same strides (in elements; the last dimension is
+ * contiguous), any block_size >= 1, and may be views of one array in either
+ * order of pages, tokens and heads.  Nothing is assumed about slots that hold no token.
+ *
+ * Arguments travel in a struct, which is read before the call returns.  All
+ * pointers are device pointers unless stated; f16 / bf16 data must be 16-byte
+ * aligned and its strides multiples of 8 elements (SGMV_ERR_ALIGNMENT).
+ * Metadata is checked on the device: a sequence with bad tree_ptr or too many
+ * nodes is skipped (SGMV_ERR_BAD_SEGMENTS in the device error word), and a
+ * parent, page, slot, token or path entry out of range is left out
+ * (SGMV_ERR_BAD_INDEX).  Calls are asynchronous, allocate nothing, and read
+ * their inputs only after the previous kernel on the stream has finished.
+ */
+#define SGMV_TREE_MAX_NODES 256
+
+/*
+ * Rotary positions.  The first 2 * pairs columns of every head of q and k turn
+ * pairwise by the angle positions[t] * inv_freq[i]:
+ *   out_a = scale * (x_a cos - x_b sin),  out_b = scale * (x_a sin + x_b cos)
+ * with (a, b) = (i, i + pairs), or (2i, 2i + 1) if interleaved; the other
+ * columns are copied.  inverse != 0 turns by the negative angle: applied to
+ * the gradients of the outputs it gives the gradients of the inputs.  scale
+ * is the magnitude factor of long-context scalings (1 without).  The angle is
+ * reduced in 64-bit fixed point, so positions of any size are as accurate as
+ * small ones; sums are fp32 and rounded once.
+ *   q [T][Hq][D], k and v [T][Hk][D]  any token and head strides; q or k may
+ *     be NULL (with Hq or Hk = 0).  q_out / k_out may equal q / k (in place)
+ *     but must not overlap them otherwise.  k_out may be NULL when k_cache is given.
+ *   positions int32 [T]; inv_freq HOST double [pairs], 0 <= 2 pairs <= D
+ *   k_cache, v_cache, slots: all NULL, or the rotated k and the unchanged v of
+ *     row t are also written to slot slots[t] (page * block_size + offset;
+ *     -1 = not appended).  v_cache needs v.  Slots must be distinct.
+ * D a multiple of 8, at most 256 (SGMV_ERR_UNSUPPORTED beyond).
+ */
+typedef struct {
+    void *q_out;
+    const void *q;
+    void *k_out;
+    const void *k;
+    const void *v;
+    void *k_cache;
+    void *v_cache;
+    const int32_t *positions;
+    const int32_t *slots;
+    const double *inv_freq;
+    int64_t q_out_token, q_out_head, q_token, q_head;
+    int64_t k_out_token, k_out_head, k_token, k_head, v_token, v_head;
+    int64_t cache_block, cache_token, cache_head;
+    int32_t T, Hq, Hk, D, pairs, num_blocks, block_size, dtype, interleaved, inverse;
+    float scale;
+} sgmv_rope_args;
+int sgmv_rope(const sgmv_rope_args *args, void *stream);
+
+/*
+ * Inverse frequencies of rotary positions, on the host: inv_freq[i] =
+ * base^(-2i / (2 pairs)), i < pairs, then stretched for contexts of `factor`
+ * times the `trained` length: a pair that turns at least `fast` times over
+ * the trained length is kept, one that turns at most `slow` times is divided
+ * by factor, with a linear ramp between (slow < fast).  factor = 1 leaves them
+ * as they are; slow = fast = INFINITY divides every pair (linear position
+ * interpolation).
+ */
+int sgmv_rope_frequencies(double *inv_freq, int32_t pairs, double base, double factor,
+                          double trained, double slow, double fast);
+
+/*
+ * Attention of the drafted tokens over the cache:
+ *   out[t][h] = sum_j p_j v_j,  p = softmax_j(scale * q[t][h] . k_j)
+ * over the context of t's sequence, t's ancestors and t itself; k_j and v_j
+ * of head h / (Hq / Hkv).  What a row does not see has no influence on it,
+ * infinities and NaN included.  A row that sees nothing (padding) gets 0 and
+ * lse -inf.  The sequences' nodes must have been appended to the cache.
+ *   q, out [T][Hq][D]; lse fp32 [T][Hq] contiguous or NULL: log of the sum of
+ *     exp(scale * score); block_table int32 [B][max_blocks], row stride
+ *     table_row; prefix_lens int32 [B]; tree_ptr int32 [B+1]
+ *   scale: multiplied onto the scores (usually D^-1/2)
+ *   workspace: sgmv_tree_attention_workspace_bytes() bytes, 256-byte aligned.
+ *     It must be all zero before its first use; every call leaves it ready
+ *     for the next.  Calls that run at the same time need separate ones.
+ * Hq a multiple of Hkv, D a multiple of 8 up to 256.  Scores, softmax and
+ * sums are fp32; the weights p are rounded to the inputs' type for the
+ * tensor cores, the output once.  out must not overlap the inputs.  Rows in
+ * no sequence are not written.
+ */
+typedef struct {
+    void *out;
+    const void *q;
+    const void *k_cache;
+    const void *v_cache;
+    float *lse;
+    const int32_t *block_table;
+    const int32_t *prefix_lens;
+    const int32_t *tree_ptr;
+    const int32_t *parents;
+    void *workspace;
+    uint64_t workspace_bytes;
+    int64_t out_token, out_head, q_token, q_head;
+    int64_t cache_block, cache_token, cache_head, table_row;
+    int32_t T, B, Hq, Hkv, D, num_blocks, block_size, max_blocks, dtype;
+    float scale;
+} sgmv_tree_attention_args;
+size_t sgmv_tree_attention_workspace_bytes(int32_t T, int32_t B, int32_t Hq, int32_t Hkv,
+                                           int32_t D);
+int sgmv_tree_attention(const sgmv_tree_attention_args *args, void *stream);
+
+/*
+ * Verification of drafted tokens (speculative sampling on a tree), from given
+ * random numbers.  Node 0 of a sequence is its last token, already accepted;
+ * tokens[row] is each node's token; target[row] the model's distribution
+ * after the node, draft[row] the distribution its children were drawn from
+ * (independent draws), or draft == NULL for children proposed without one.
+ * From node 0 on, the children of the last accepted node are tried in order:
+ *   child c is accepted if  u_accept[c] * q(token) * W < w(token),
+ * else the rest of the distribution shrinks:  w = max(w - q W, 0), W = sum w
+ * (without a draft: q = 1 at the token, so w(token) = 0).  w starts as the
+ * target's weights with W = 1 at every accepted node.  When no child is left,
+ * `token` is drawn from w by inverting its running sum at u_sample[b]; if w
+ * is zero everywhere, from the target itself, and -1 if that is zero too.
+ * The accepted tokens and the drawn one follow the target's distribution.
+ * Weights are whole multiples of 2^-38 (probabilities are clamped to [0, 1];
+ * NaN counts as 0), so sums are exact and results do not depend on the order
+ * of summation; products are single fp32 multiplications.
+ *   target, draft fp32 [T][V], rows target_row / draft_row elements apart, 4-byte aligned
+ *   u_accept fp32 [T], u_sample fp32 [B], in [0, 1)
+ *   count int32 [B]: accepted nodes, node 0 among them (0 for an empty sequence)
+ *   path int32 [B][max_path]: their node numbers, -1 beyond; the walk stops
+ *     when it is full.  token int32 [B].
+ */
+typedef struct {
+    const float *target;
+    const float *draft;
+    const int32_t *tokens;
+    const int32_t *parents;
+    const int32_t *tree_ptr;
+    const float *u_accept;
+    const float *u_sample;
+    int32_t *count;
+    int32_t *path;
+    int32_t *token;
+    int64_t target_row, draft_row;
+    int32_t T, B, V, max_path;
+} sgmv_tree_verify_args;
+int sgmv_tree_verify(const sgmv_tree_verify_args *args, void *stream);
+
+/*
+ * Moves the accepted nodes' k and v to their final places in the cache, in
+ * place: position prefix_lens[b] + d takes what position prefix_lens[b] +
+ * path[b][d] held, for d < count[b].  path rows ascend (as
+ * sgmv_tree_verify writes them).  Afterwards the sequence's context is
+ * prefix_lens[b] + count[b] long.  layers > 1 moves the same tokens in that
+ * many caches, cache_layer elements apart.
+ */
+typedef struct {
+    void *k_cache;
+    void *v_cache;
+    const int32_t *block_table;
+    const int32_t *prefix_lens;
+    const int32_t *path;
+    const int32_t *count;
+    int64_t cache_layer, cache_block, cache_token, cache_head, table_row;
+    int32_t layers, B, Hkv, D, num_blocks, block_size, max_blocks, max_path, dtype;
+} sgmv_cache_commit_args;
+int sgmv_cache_commit(const sgmv_cache_commit_args *args, void *stream);
+
+/*
  * Diagnostics (no counterpart on the pages).
  *
  * sgmv_read_floor: the floor of a decode-sized SGMV launch on this GPU.  Reads

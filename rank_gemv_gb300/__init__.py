@@ -16,6 +16,8 @@ _BINDING_NAMES = {
     "sgmv_apply", "sgmv_apply_multi", "sgmv_apply_rows", "sgmv_apply_noalloc", "sgmv_load_adapter", "sgmv_copy_gather",
     "sgmv_get_device_error", "sgmv_last_launch_count", "sgmv_read_floor",
     "sgmv_debug_inject_wait_timeout", "sgmv_fused_workspace_bytes", "sgmv_fused_linear_lora",
+    "sgmv_rope", "sgmv_rope_frequencies", "sgmv_tree_attention",
+    "sgmv_tree_attention_workspace_bytes", "sgmv_tree_verify", "sgmv_cache_commit",
     "SgmvError", "load_library",
 }
 

@@ -11,6 +11,7 @@
 #include "sgmv_internal.h"
 #include "sgmv_fused.h"
 #include "sgmv_gather.h"
+#include "sgmv_spec.h"
 
 // Sticky device error word of this library (first reported status wins).
 __device__ int g_sgmv_error;
@@ -183,6 +184,10 @@ constexpr uint32_t kStreamSmemMax = 170u * 1024u;
 void sgmv::note_cuda_error(const char *what, cudaError_t e) { note(what, e); }
 
 int *sgmv::device_error_word() { return error_word(); }
+
+void sgmv::set_launch_count(int n) { g_launches = n; }
+
+int sgmv::device_sms() { return num_sms(); }
 
 // Launch shape of the streaming kernel for a batch of T rows in S segments
 // (the last max_len rows long at most), or false when the kernel does not

@@ -11,6 +11,7 @@ it raises: there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import struct
 from pathlib import Path
 
 import torch
@@ -27,6 +28,7 @@ STATUS = {0: "SGMV_OK", 1: "SGMV_ERR_INVALID_ARG", 2: "SGMV_ERR_UNSUPPORTED",
 # Every function include/sgmv.h declares, with its ctypes signature.
 _vp, _i32, _i32p = ctypes.c_void_p, ctypes.c_int32, ctypes.POINTER(ctypes.c_int32)
 _int, _f32, _sz = ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_f64, _cp = ctypes.c_double, ctypes.c_char_p  # _cp: a packed argument struct
 _vpp, _u64p = ctypes.POINTER(ctypes.c_void_p), ctypes.POINTER(ctypes.c_uint64)
 SIGNATURES = {
     "sgmv_status_string": (ctypes.c_char_p, [_int]),
@@ -55,6 +57,12 @@ SIGNATURES = {
     "sgmv_copy_gather": (_int, [_i32, _vpp, _vpp, _u64p, _i32, _vp]),
     "sgmv_read_floor": (_int, [_vp, _sz, _i32, _i32, _i32, _i32, _i32, _int, _int, _i32p, _i32p,
                                _vp]),
+    "sgmv_rope": (_int, [_cp, _vp]),
+    "sgmv_rope_frequencies": (_int, [_vp, _i32, _f64, _f64, _f64, _f64, _f64]),
+    "sgmv_tree_attention_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32, _i32]),
+    "sgmv_tree_attention": (_int, [_cp, _vp]),
+    "sgmv_tree_verify": (_int, [_cp, _vp]),
+    "sgmv_cache_commit": (_int, [_cp, _vp]),
     "sgmv_debug_inject_wait_timeout": (_int, [_int]),
     "sgmv_get_device_error": (_int, [_vp]),
 }
@@ -359,6 +367,200 @@ def sgmv_copy_gather(dsts, srcs, stream=None, max_ctas=0):
         s = (ctypes.c_void_p * n)(*[srcs[i].data_ptr() for i in part])
         b = (ctypes.c_uint64 * n)(*[srcs[i].nbytes for i in part])
         _check(lib.sgmv_copy_gather(n, d, s, b, int(max_ctas), st), "sgmv_copy_gather")
+
+
+# Argument structs of the speculative decoding calls (include/sgmv.h), packed
+# with native sizes and alignment (0q: padded to whole 8-byte words).
+_ROPE_ARGS = struct.Struct("@10P13q10if0q")
+_ATTENTION_ARGS = struct.Struct("@10PQ8q9if0q")
+_VERIFY_ARGS = struct.Struct("@10P2q4i0q")
+_COMMIT_ARGS = struct.Struct("@6P5q9i0q")
+
+
+def _heads(t, name, dtype, H=None, T=None):
+    """(pointer, token stride, head stride) of a [T, H, D] tensor."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.dim() != 3 or (H is not None and t.shape[1] != H) or (T is not None and t.shape[0] != T):
+        raise ValueError(f"{name} has the wrong shape")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 and t.shape[2] > 1:
+        raise TypeError(f"the last dimension of {name} must be contiguous")
+    return t.data_ptr(), s0, s1
+
+
+def _cache(k_cache, v_cache, dtype, layers=False):
+    """Checked strides and shape of a pair of caches [blocks, block_size, Hkv, D]
+    (with layers, [layers, blocks, block_size, Hkv, D] too)."""
+    shape, stride = k_cache.shape, k_cache.stride()
+    if v_cache.shape != shape or v_cache.stride() != stride:
+        raise ValueError("k_cache and v_cache differ in shape or strides")
+    if k_cache.dtype != dtype or v_cache.dtype != dtype:
+        raise TypeError(f"the caches must be {dtype}")
+    if len(shape) != 4 and not (layers and len(shape) == 5):
+        raise ValueError("the caches must be [blocks, block_size, heads, D]")
+    if stride[-1] != 1 and shape[-1] > 1:
+        raise TypeError("the last dimension of the caches must be contiguous")
+    return shape, stride
+
+
+def _list(t, name, n):
+    """Pointer of a contiguous int32 tensor of n entries (or of None)."""
+    if t is None:
+        return 0
+    if _meta(t, name).numel() != n:
+        raise ValueError(f"{name} must have {n} entries")
+    return t.data_ptr()
+
+
+def _table(block_table, B):
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B or (
+            block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise TypeError("block_table must be int32 [B, max_blocks] with contiguous rows")
+    return block_table.data_ptr(), block_table.shape[1], block_table.stride(0)
+
+
+def sgmv_rope_frequencies(pairs, base=10000.0, factor=1.0, trained=0.0, slow=float("inf"),
+                          fast=float("inf")):
+    """Inverse frequencies of `pairs` rotary pairs, stretched by `factor` (see
+    include/sgmv.h); a float64 CPU tensor to pass to sgmv_rope."""
+    out = torch.empty(pairs, dtype=torch.float64)
+    _check(load_library().sgmv_rope_frequencies(out.data_ptr(), pairs, base, factor, trained, slow,
+                                                fast), "sgmv_rope_frequencies")
+    return out
+
+
+def sgmv_rope(q, k, positions, inv_freq, interleaved=False, scale=1.0, inverse=False, q_out=None,
+              k_out=None, v=None, k_cache=None, v_cache=None, slots=None):
+    """Rotary positions of q [T, Hq, D] and k [T, Hk, D] (either may be None);
+    returns (q_out, k_out).
+
+    Without q_out q is rotated in place; without k_out k is rotated in place,
+    unless caches are given: then the rotated k and the unchanged v go to the
+    cache slots `slots` only (-1: not appended).  inv_freq: float64 CPU tensor
+    of the rotated pairs (sgmv_rope_frequencies); inverse=True turns back, the
+    gradient of the rotation."""
+    first = q if q is not None else k
+    T, _, D = first.shape
+    dtype = first.dtype
+    if inv_freq.dtype != torch.float64 or inv_freq.device.type != "cpu" or not inv_freq.is_contiguous():
+        raise TypeError("inv_freq must be a contiguous float64 CPU tensor")
+    qi = qo = ki = ko = vi = (0, 0, 0)
+    Hq = Hk = blocks = bs = 0
+    cs = (0, 0, 0, 0)
+    if q is not None:
+        Hq = q.shape[1]
+        q_out = q if q_out is None else q_out
+        qi, qo = _heads(q, "q", dtype), _heads(q_out, "q_out", dtype, Hq, T)
+        if q_out.shape[2] != D:
+            raise ValueError("q_out has the wrong shape")
+    if k is not None:
+        Hk = k.shape[1]
+        if k_out is None and k_cache is None:
+            k_out = k
+        ki = _heads(k, "k", dtype, None, T)
+        if k_out is not None:
+            ko = _heads(k_out, "k_out", dtype, Hk, T)
+        if k.shape[2] != D or (k_out is not None and k_out.shape[2] != D):
+            raise ValueError("q, k and k_out differ in head size")
+    if k_cache is not None:
+        shape, cs = _cache(k_cache, v_cache, dtype)
+        vi = _heads(v, "v", dtype, Hk, T)
+        blocks, bs = shape[0], shape[1]
+        if shape[2] != Hk or shape[3] != D or v.shape[2] != D:
+            raise ValueError("the caches or v do not fit k")
+    args = _ROPE_ARGS.pack(
+        qo[0], qi[0], ko[0], ki[0], vi[0], 0 if k_cache is None else k_cache.data_ptr(),
+        0 if v_cache is None else v_cache.data_ptr(), _list(positions, "positions", T),
+        _list(slots, "slots", T), inv_freq.data_ptr(), qo[1], qo[2], qi[1], qi[2], ko[1], ko[2],
+        ki[1], ki[2], vi[1], vi[2], cs[0], cs[1], cs[2], T, Hq, Hk, D, inv_freq.numel(), blocks, bs,
+        _DTYPES[dtype], interleaved, inverse, scale)
+    _check(load_library().sgmv_rope(args, _stream(first.device)), "sgmv_rope")
+    return q_out, k_out
+
+
+def sgmv_tree_attention_workspace_bytes(T: int, B: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(load_library().sgmv_tree_attention_workspace_bytes(T, B, Hq, Hkv, D))
+
+
+def sgmv_tree_attention(out, q, k_cache, v_cache, block_table, prefix_lens, tree_ptr, parents=None,
+                        scale=None, lse=None, workspace=None):
+    """Attention of the drafted rows q [T, Hq, D] over the paged cache [blocks,
+    block_size, Hkv, D], into out; returns out.
+
+    Row t of sequence b (tree_ptr[b] <= t < tree_ptr[b + 1]) sees the
+    prefix_lens[b] tokens of its context, its ancestors by `parents` (None: a
+    chain) and itself.  scale defaults to D ** -0.5; lse (fp32 [T, Hq]) receives
+    the log-sum-exp.  workspace: uint8 device tensor of
+    sgmv_tree_attention_workspace_bytes(T, B, Hq, Hkv, D) bytes, zeroed once
+    before its first use (a zeroed one is made when None)."""
+    T, Hq, D = q.shape
+    B = prefix_lens.numel()
+    dtype = q.dtype
+    qi, oo = _heads(q, "q", dtype), _heads(out, "out", dtype, Hq, T)
+    shape, cs = _cache(k_cache, v_cache, dtype)
+    if shape[3] != D or out.shape[2] != D:
+        raise ValueError("q, out and the caches differ in head size")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, Hq) or not lse.is_contiguous()):
+        raise TypeError("lse must be a contiguous float32 [T, Hq] tensor")
+    table, width, row = _table(block_table, B)
+    lib = load_library()
+    if workspace is None:
+        workspace = torch.zeros(lib.sgmv_tree_attention_workspace_bytes(T, B, Hq, shape[2], D),
+                                dtype=torch.uint8, device=q.device)
+    args = _ATTENTION_ARGS.pack(
+        oo[0], qi[0], k_cache.data_ptr(), v_cache.data_ptr(), 0 if lse is None else lse.data_ptr(),
+        table, _list(prefix_lens, "prefix_lens", B), _list(tree_ptr, "tree_ptr", B + 1),
+        _list(parents, "parents", T), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), oo[1], oo[2], qi[1], qi[2], cs[0], cs[1],
+        cs[2], row, T, B, Hq, shape[2], D, shape[0], shape[1], width, _DTYPES[dtype],
+        D ** -0.5 if scale is None else scale)
+    _check(lib.sgmv_tree_attention(args, _stream(q.device)), "sgmv_tree_attention")
+    return out
+
+
+def sgmv_tree_verify(target, draft, tokens, parents, tree_ptr, u_accept, u_sample, max_path, out=None):
+    """Verify drafted tokens against target [T, V] (fp32 probabilities after each
+    node) and draft [T, V] (what each node's children were drawn from, or None)
+    with the uniform numbers u_accept [T] and u_sample [B]; returns (count [B],
+    path [B, max_path], token [B]), int32 (`out`: such a tuple to write into)."""
+    T, V = target.shape
+    B = tree_ptr.numel() - 1
+    for t, name in ((target, "target"), (draft, "draft")):
+        if t is not None and (t.dtype != torch.float32 or t.shape != (T, V) or (V > 1 and t.stride(1) != 1)):
+            raise TypeError(f"{name} must be float32 [T, V] with contiguous rows")
+    for t, name, n in ((u_accept, "u_accept", T), (u_sample, "u_sample", B)):
+        if t.dtype != torch.float32 or not t.is_contiguous() or t.numel() != n:
+            raise TypeError(f"{name} must be a contiguous float32 tensor of {n} entries")
+    if out is None:
+        out = torch.empty(B * (max_path + 2), dtype=torch.int32, device=target.device)
+        out = out[:B], out[2 * B:].view(B, max_path), out[B:2 * B]
+    count, path, token = out
+    args = _VERIFY_ARGS.pack(
+        target.data_ptr(), 0 if draft is None else draft.data_ptr(), _list(tokens, "tokens", T),
+        _list(parents, "parents", T), _list(tree_ptr, "tree_ptr", B + 1), u_accept.data_ptr(),
+        u_sample.data_ptr(), _list(count, "count", B), _list(path, "path", B * max_path),
+        _list(token, "token", B), target.stride(0), 0 if draft is None else draft.stride(0), T, B, V,
+        max_path)
+    _check(load_library().sgmv_tree_verify(args, _stream(target.device)), "sgmv_tree_verify")
+    return out
+
+
+def sgmv_cache_commit(k_cache, v_cache, block_table, prefix_lens, path, count):
+    """Move the accepted nodes (path [B, max_path], count [B], as
+    sgmv_tree_verify returns them) to their final places in the caches
+    [blocks, block_size, Hkv, D] or [layers, blocks, block_size, Hkv, D], in place."""
+    dtype = k_cache.dtype
+    shape, cs = _cache(k_cache, v_cache, dtype, layers=True)
+    layers, layer_stride = (shape[0], cs[0]) if len(shape) == 5 else (1, 0)
+    blocks, bs, Hkv, D = shape[-4:]
+    B, width = path.shape
+    table, max_blocks, row = _table(block_table, B)
+    args = _COMMIT_ARGS.pack(
+        k_cache.data_ptr(), v_cache.data_ptr(), table, _list(prefix_lens, "prefix_lens", B),
+        _list(path, "path", B * width), _list(count, "count", B), layer_stride, cs[-4], cs[-3],
+        cs[-2], row, layers, B, Hkv, D, blocks, bs, max_blocks, width, _DTYPES[dtype])
+    _check(load_library().sgmv_cache_commit(args, _stream(k_cache.device)), "sgmv_cache_commit")
 
 
 def sgmv_read_floor(src, nbytes, T, L, H1, H2, r, in_dtype=torch.float16, y_dtype=None):
