@@ -127,11 +127,12 @@ __global__ void __launch_bounds__(kRowThreads)
 }  // namespace
 
 size_t tree_attention_workspace(int32_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D) {
-    return 256;
+    return D <= kMmaMaxD ? tree_mma_workspace(T, B, Hq / Hkv) : 256;
 }
 
 int tree_attention_launch(const sgmv_tree_attention_args &a, int nsm, int *err,
                           cudaStream_t stream) {
+    if (a.D <= kMmaMaxD) return tree_mma_launch(a, nsm, err, stream);
     const dim3 grid((unsigned)a.T, (unsigned)a.Hq, 1);
     return a.dtype == SGMV_F16
                ? spec_launch(sgmv_tree_row_kernel<__half>, grid, kRowThreads, 0, 1, stream, a, err)
