@@ -384,8 +384,8 @@ int sgmv_copy_gather(int32_t n, void *const *dst, const void *const *src, const 
  * aligned and its strides multiples of 8 elements (SGMV_ERR_ALIGNMENT).
  * Metadata is checked on the device: a sequence with bad tree_ptr or too many
  * nodes is skipped (SGMV_ERR_BAD_SEGMENTS in the device error word), and a
- * parent, page, slot, token or path entry out of range is left out
- * (SGMV_ERR_BAD_INDEX).  Calls are asynchronous, allocate nothing, and read
+ * parent, slot, token or path entry out of range is left out, a page out of
+ * range spoils its own sequence alone (SGMV_ERR_BAD_INDEX).  Calls are asynchronous, allocate nothing, and read
  * their inputs only after the previous kernel on the stream has finished.
  */
 #define SGMV_TREE_MAX_NODES 256

@@ -796,7 +796,7 @@ bool tmap_encode(CUtensorMap *m, bool bf16, int rank, const void *ptr, const cuu
                  const cuuint64_t *strides, const cuuint32_t *box, bool swizzle128) {
     EncodeTiledFn fn = tiled_encoder();
     if (!fn) return false;
-    const cuuint32_t es[3] = {1, 1, 1};
+    const cuuint32_t es[5] = {1, 1, 1, 1, 1};
     return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
               (cuuint32_t)rank, const_cast<void *>(ptr), dims, strides, box, es,
               CU_TENSOR_MAP_INTERLEAVE_NONE,

@@ -33,9 +33,11 @@
 // the rows that do see them.
 #include <math.h>
 
+#include <numeric>
 #include <type_traits>
 
 #include "sgmv_device.cuh"
+#include "sgmv_internal.h"
 #include "sgmv_spec.h"
 #include "sgmv_tcgen05.cuh"
 
@@ -74,6 +76,9 @@ template <int RT> struct Shape {
 };
 
 struct MmaParams {
+    // the caches as [page][head][token][D], boxes of `box` tokens by 64 columns
+    CUtensorMap map_k, map_v;
+    int32_t box;      // tokens per box: the largest divisor of 128 that divides a page; 0: cp.async
     sgmv_tree_attention_args a;
     float c;          // scale * log2(e)
     int32_t group;    // query heads per KV head
@@ -262,8 +267,10 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
 
     if (warp == kMmaWarp) {
         if (lane == 0) {
-            for (int i = 0; i < S::kStages; ++i) mbar_init(&full[i], kLoaders), mbar_init(&empty[i], 1);
-            for (int i = 0; i < S::kQ; ++i) mbar_init(&q_full[i], kLoaders), mbar_init(&q_empty[i], 1);
+            for (int i = 0; i < S::kStages; ++i)
+                mbar_init(&full[i], P.box ? 1 : kLoaders), mbar_init(&empty[i], 1);
+            for (int i = 0; i < S::kQ; ++i)
+                mbar_init(&q_full[i], P.box ? kLoaders - 32 : kLoaders), mbar_init(&q_empty[i], 1);
             for (int i = 0; i < 2; ++i) mbar_init(&s_full[i], 1), mbar_init(&s_empty[i], S::kSoft);
             mbar_init(&p_full, S::kSoft);
             mbar_init(&pv_done, 1);
@@ -276,9 +283,10 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
         tmem_alloc(&s_tmem, S::kTmem);
     }
     for (int i = tid; i < RT; i += S::kThreads) s_ref[i] = kUnset;
-    // columns past D are never loaded: zero in K and Q (0 . 0 in the scores)
-    if (a.D < 128)
-        for (uint32_t i = tid * 16u; i < S::kOffP; i += S::kThreads * 16u)
+    // columns past D that the products read are zero: in Q, and in K where TMA
+    // does not fill them
+    if (a.D % 64 != 0)
+        for (uint32_t i = (P.box ? S::kOffQ : 0u) + tid * 16u; i < S::kOffP; i += S::kThreads * 16u)
             sts128(sm + i, make_uint4(0, 0, 0, 0));
     fence_proxy_async();
     pdl_wait();
@@ -340,8 +348,87 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
         // ---- loaders: ring order K0, K1, V0, K2, V1, ..., V(last) -----------
         const int lt = tid - S::kSoft - 32;
         const int cpr = D / 8;                     // 16-byte chunks per row
+        const int dm = kLoaders / cpr, dc = kLoaders - dm * cpr;
+        constexpr int kBatch = 8, kOwn = (kTok + kLoaders - 1) / kLoaders;
         int64_t *const tab = reinterpret_cast<int64_t *>(sm + S::kOffTab);
+        const int halves = D > 64 ? 2 : 1;
         int pos = 0, g = 0, seg = 0;               // ring position, tile, segment
+        // the queries of segment seg's row tile, by `count` threads
+        auto load_q = [&](int i0, int count) {
+            const int qb = seg % S::kQ;
+            if (seg >= S::kQ) await(&q_empty[qb], (uint32_t)(seg / S::kQ - 1) & 1, lost);
+            uint8_t *const dst = sm + S::kOffQ + (uint32_t)qb * S::kQBytes;
+            const int R = cur.n * group;
+            for (int i = i0; i < RT * cpr; i += count) {
+                const int m = i / cpr, c = i - m * cpr, r = cur.rt * RT + m;
+                const int node = r / group, hq = cur.h * group + (r - node * group);
+                const bool in = r < R;
+                const T *src = static_cast<const T *>(a.q) +
+                               (in ? (int64_t)(cur.t0 + node) * a.q_token + (int64_t)hq * a.q_head + c * 8 : 0);
+                cp_async16(dst + (uint32_t)(c >> 3) * (RT * 128u) + sw128_offset(m, c & 7), src, in ? 16u : 0u);
+            }
+            cp_async_arrive(&q_full[qb]);
+            ++seg;
+        };
+        if (P.box && lt >= 32) {
+            while (cur.next(P)) load_q(lt - 32, kLoaders - 32);
+            asm volatile("cp.async.wait_all;" ::: "memory");
+        } else if (P.box) {
+            // TMA: lane = one box (tokens x 64 columns) of a tile
+            const int box = P.box, nbox = kTok / box, mine = lane % nbox, half = lane / nbox;
+            const bool busy = half < halves;
+            const uint32_t bytes = (uint32_t)halves * kHalf;
+            const uint32_t at = (uint32_t)half * kHalf + (uint32_t)(mine * box) * 128u;
+            Cur peek = cur;   // the tile whose page is looked up next
+            int peek_tile = 0, peek_end = 0;
+            int32_t next_page = 0;
+            int next_in = 0;
+            auto look = [&]() {
+                if (peek_tile == peek_end) {
+                    if (!peek.next(P)) return;
+                    peek_tile = peek.tile;
+                    peek_end = peek.end;
+                }
+                const int j = peek_tile * kTok + mine * box;
+                next_in = -1;
+                if (j < peek.total) {
+                    const int pg = j / a.block_size;
+                    next_in = j - pg * a.block_size;
+                    next_page = a.block_table[peek.b * a.table_row + pg];
+                }
+                ++peek_tile;
+            };
+            auto copy_boxes = [&](const CUtensorMap *map, int32_t page, int in, int head) {
+                const int st = pos % S::kStages;
+                if (pos >= S::kStages) await(&empty[st], (uint32_t)(pos / S::kStages - 1) & 1, lost);
+                if (lane == 0) mbar_arrive_expect_tx(&full[st], bytes);
+                __syncwarp();
+                if (busy) tma_load_4d(sm + (uint32_t)st * kStage + at, map, half * 64, in, head, page, &full[st]);
+                ++pos;
+            };
+            int32_t page = 0, old_page = 0;
+            int in = 0, old_in = 0, old_h = 0;
+            look();
+            while (cur.next(P)) {
+                for (int tile = cur.tile; tile < cur.end; ++tile, ++g) {
+                    // boxes past the end, and pages out of range, read as zeros
+                    page = next_page;
+                    in = next_in;
+                    if (in < 0 || page < 0 || page >= a.num_blocks) {
+                        if (in >= 0) set_error(P.err, kErrBadIndex);
+                        page = a.num_blocks;
+                        in = 0;
+                    }
+                    look();
+                    copy_boxes(&P.map_k, page, in, cur.h);
+                    if (g > 0) copy_boxes(&P.map_v, old_page, old_in, old_h);
+                    old_page = page;
+                    old_in = in;
+                    old_h = cur.h;
+                }
+            }
+            copy_boxes(&P.map_v, old_page, old_in, old_h);
+        } else {
         int64_t head_off = 0, prev_head = 0;
         auto copy_tile = [&](const void *cache, int64_t off, int tile) {
             const int st = pos % S::kStages;
@@ -349,63 +436,81 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
             const T *const base = static_cast<const T *>(cache) + off;
             const int64_t *const rows = tab + (tile & 3) * kTok;
             uint8_t *const dst = sm + (uint32_t)st * kStage;
+            // eight copies' row offsets are read before the first is used
             int m = lt / cpr, c = lt - m * cpr;
-            const int dm = kLoaders / cpr, dc = kLoaders - dm * cpr;
             while (m < kTok) {
-                const int64_t o = rows[m];
-                cp_async16(dst + (uint32_t)(c >> 3) * kHalf + sw128_offset(m, c & 7),
-                           o >= 0 ? base + o + c * 8 : base, o >= 0 ? 16u : 0u);
-                m += dm;
-                c += dc;
-                if (c >= cpr) c -= cpr, ++m;
+                int64_t o[kBatch];
+                uint32_t to[kBatch];
+                int cc[kBatch];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    o[i] = -2;
+                    if (m < kTok) {
+                        o[i] = rows[m];
+                        to[i] = (uint32_t)(c >> 3) * kHalf + sw128_offset(m, c & 7);
+                        cc[i] = c * 8;
+                    }
+                    m += dm;
+                    c += dc;
+                    if (c >= cpr) c -= cpr, ++m;
+                }
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i)
+                    if (o[i] != -2)
+                        cp_async16(dst + to[i], o[i] >= 0 ? base + o[i] + cc[i] : base, o[i] >= 0 ? 16u : 0u);
             }
             cp_async_arrive(&full[st]);
             ++pos;
         };
+        // the tile after the current one: its pages are looked up while the
+        // current one's copies are issued
+        Cur peek = cur;
+        int peek_tile = 0, peek_end = 0;
+        int32_t block[kOwn];
+        int in_page[kOwn];
+        auto look = [&]() {
+            if (peek_tile == peek_end) {
+                if (!peek.next(P)) return;
+                peek_tile = peek.tile;
+                peek_end = peek.end;
+            }
+#pragma unroll
+            for (int e = 0; e < kOwn; ++e) {
+                const int m = lt + e * kLoaders, j = peek_tile * kTok + m;
+                in_page[e] = -1;
+                if (m < kTok && j < peek.total) {
+                    const int pg = j / a.block_size;
+                    in_page[e] = j - pg * a.block_size;
+                    block[e] = a.block_table[peek.b * a.table_row + pg];
+                }
+            }
+            ++peek_tile;
+        };
+        look();
         while (cur.next(P)) {
             prev_head = head_off;
             head_off = (int64_t)cur.h * a.cache_head;
-            // the row tile's queries
-            const int qb = seg % S::kQ;
-            if (seg >= S::kQ) await(&q_empty[qb], (uint32_t)(seg / S::kQ - 1) & 1, lost);
-            {
-                uint8_t *const dst = sm + S::kOffQ + (uint32_t)qb * S::kQBytes;
-                const int R = cur.n * group;
-                for (int i = lt; i < RT * cpr; i += kLoaders) {
-                    const int m = i / cpr, c = i - m * cpr, r = cur.rt * RT + m;
-                    const int node = r / group, hq = cur.h * group + (r - node * group);
-                    const bool in = r < R;
-                    const T *src = static_cast<const T *>(a.q) + (in ? (int64_t)(cur.t0 + node) * a.q_token +
-                                                                           (int64_t)hq * a.q_head + c * 8
-                                                                     : 0);
-                    cp_async16(dst + (uint32_t)(c >> 3) * (RT * 128u) + sw128_offset(m, c & 7), src,
-                               in ? 16u : 0u);
-                }
-                cp_async_arrive(&q_full[qb]);
-            }
-            ++seg;
+            load_q(lt, kLoaders);
             for (int tile = cur.tile; tile < cur.end; ++tile, ++g) {
                 // where the tile's tokens are (elements from the cache's start)
-                for (int m = lt; m < kTok; m += kLoaders) {
-                    int64_t off = -1;
-                    const int j = tile * kTok + m;
-                    if (j < cur.total) {
-                        const int pg = j / a.block_size;
-                        const int32_t block = a.block_table[cur.b * a.table_row + pg];
-                        if (block >= 0 && block < a.num_blocks)
-                            off = (int64_t)block * a.cache_block + (int64_t)(j - pg * a.block_size) * a.cache_token;
-                        else
-                            set_error(P.err, kErrBadIndex);
-                    }
-                    tab[(g & 3) * kTok + m] = off;
+#pragma unroll
+                for (int e = 0; e < kOwn; ++e) {
+                    const int m = lt + e * kLoaders;
+                    const bool in = in_page[e] >= 0, good = in && block[e] >= 0 && block[e] < a.num_blocks;
+                    if (in && !good) set_error(P.err, kErrBadIndex);
+                    if (m < kTok)
+                        tab[(g & 3) * kTok + m] =
+                            good ? (int64_t)block[e] * a.cache_block + (int64_t)in_page[e] * a.cache_token : -1;
                 }
                 named_sync<1, kLoaders>();
+                look();
                 copy_tile(a.k_cache, head_off, g);
                 if (g > 0) copy_tile(a.v_cache, tile == cur.tile ? prev_head : head_off, g - 1);
             }
         }
         copy_tile(a.v_cache, head_off, g - 1);
         asm volatile("cp.async.wait_all;" ::: "memory");
+        }
     } else if (warp == kMmaWarp) {
         // ---- MMA issuer ------------------------------------------------------
         const uint32_t idesc_s = idesc_f16(kBf16, kTok, RT) & ~(1u << 16);   // both K-major
@@ -434,10 +539,12 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
                 tc_fence_after();
                 const uint32_t ka = ring + (uint32_t)st * kStage, q = qa + (uint32_t)qb * S::kQBytes;
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
+                for (int kk = 0; kk < 8; ++kk) {
+                    if (kk >= 4 && D <= 64) break;
                     mma_f16(tmem + (uint32_t)((g & 1) * RT),
                             sw128_desc(ka + (kk >> 2) * kHalf + (kk & 3) * 32, 16, 1024),
                             sw128_desc(q + (kk >> 2) * (RT * 128u) + (kk & 3) * 32, 16, 1024), idesc_s, kk != 0);
+                }
                 mma_commit(&empty[st]);
                 mma_commit(&s_full[g & 1]);
                 if (left == 0) mma_commit(&q_empty[qb]);
@@ -666,15 +773,21 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
                 tc_fence_before();
                 mbar_arrive(&s_empty[g & 1]);
                 if (edge) {
-                    // non-finite v of tree nodes: out of the tile, noted
+                    // non-finite v of tree nodes: out of the tile, noted; what TMA
+                    // brought from the last page past the end: zeroed
                     const int v0 = max(0, cur.prefix - tile * kTok), v1 = min(kTok, cur.total - tile * kTok);
+                    const int ve = P.box ? min(kTok, (v1 + P.box - 1) / P.box * P.box) : v1;
                     const int cpr = D / 8;
                     const int pv = g + 1 < N ? pos_v : pos_v - 1;
                     await(&full[pv % S::kStages], (uint32_t)(pv / S::kStages) & 1, lost);
                     uint8_t *const vt = sm + (uint32_t)(pv % S::kStages) * kStage;
-                    for (int i = tid; i < (v1 - v0) * cpr; i += S::kSoft) {
+                    for (int i = tid; i < (ve - v0) * cpr; i += S::kSoft) {
                         const int m = v0 + i / cpr, cc = i % cpr;
                         uint8_t *const at = vt + (uint32_t)(cc >> 3) * kHalf + sw128_offset(m, cc & 7);
+                        if (m >= v1) {
+                            sts128(at, make_uint4(0, 0, 0, 0));
+                            continue;
+                        }
                         uint4 u = lds128(at);
                         uint32_t *const x = reinterpret_cast<uint32_t *>(&u);
                         bool any = false;
@@ -886,6 +999,20 @@ int tree_mma_launch(const sgmv_tree_attention_args &a, int nsm, int *err, cudaSt
     p.ml = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + kCountBytes);
     p.part = p.ml + (size_t)kMaxCtas * 2 * rt * 2;
     p.err = err;
+    const bool bf16 = a.dtype == SGMV_BF16;
+    p.box = std::gcd(a.block_size, kTok);
+    if (p.box >= 8) {
+        const cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)a.block_size, (cuuint64_t)a.Hkv,
+                                    (cuuint64_t)a.num_blocks};
+        const cuuint64_t strides[3] = {(cuuint64_t)a.cache_token * 2u, (cuuint64_t)a.cache_head * 2u,
+                                       (cuuint64_t)a.cache_block * 2u};
+        const cuuint32_t box[4] = {64, (cuuint32_t)p.box, 1, 1};
+        if (!tmap_encode(&p.map_k, bf16, 4, a.k_cache, dims, strides, box, true) ||
+            !tmap_encode(&p.map_v, bf16, 4, a.v_cache, dims, strides, box, true))
+            p.box = 0;  // strides that a tensor map cannot hold
+    } else {
+        p.box = 0;
+    }
     const bool h = a.dtype == SGMV_F16;
     using B16 = __nv_bfloat16;
     switch (rt) {
