@@ -54,17 +54,15 @@ constexpr float kSlack = 8.f;            // ... <= 2^(kBias + kSlack), finite in
 constexpr int kMaxCtas = 152;
 
 template <int RT> struct Shape {
-    static constexpr int kGroups = RT > 64 ? 2 : 1;       // softmax warpgroups
+    static constexpr int kGroups = RT > 32 ? RT / 32 : 1;  // softmax warpgroups
     static constexpr int kRows = RT / kGroups;            // rows per warpgroup
     static constexpr int kSoft = 128 * kGroups;           // softmax threads
     static constexpr int kThreads = kSoft + 32 + kLoaders;
-    static constexpr int kChunk = kRows < 32 ? kRows : 32;  // rows read from tensor memory at once
-    static constexpr int kChunks = kRows / kChunk;
     static constexpr int kQ = RT > 64 ? 1 : 2;            // Q buffers
     static constexpr int kStages = RT > 64 ? 4 : 5;
     static constexpr int kWords = RT < 32 ? 1 : RT / 32;  // words of one bit per row
     static constexpr uint32_t kQBytes = RT * 256u;
-    static constexpr uint32_t kPBytes = (uint32_t)kGroups * kHalf;
+    static constexpr uint32_t kPBytes = (RT > 64 ? 2 : 1) * kHalf;
     static constexpr uint32_t kTmem = RT <= 16 ? 64 : RT <= 32 ? 128 : RT <= 64 ? 256 : 512;
     // dynamic shared memory
     static constexpr uint32_t kOffQ = kStages * kStage;
@@ -78,7 +76,8 @@ template <int RT> struct Shape {
 struct MmaParams {
     // the caches as [page][head][token][D], boxes of `box` tokens by 64 columns
     CUtensorMap map_k, map_v;
-    int32_t box;      // tokens per box: the largest divisor of 128 that divides a page; 0: cp.async
+    int32_t box;      // tokens per box; 0: cp.async
+    int32_t tok;      // tokens per tile: 128, or the boxes that fit in 128
     sgmv_tree_attention_args a;
     float c;          // scale * log2(e)
     int32_t group;    // query heads per KV head
@@ -110,13 +109,13 @@ template <int RT> struct Cursor {
     __device__ __forceinline__ static uint32_t work(const MmaParams &P, int b) {
         int t0, n, prefix;
         if (!sequence(P, b, t0, n, prefix) || n == 0) return 0;
-        return (uint32_t)((prefix + n + kTok - 1) / kTok) * (uint32_t)((n * P.group + RT - 1) / RT) *
+        return (uint32_t)((prefix + n + P.tok - 1) / P.tok) * (uint32_t)((n * P.group + RT - 1) / RT) *
                (uint32_t)P.a.Hkv;
     }
     __device__ __forceinline__ void enter(const MmaParams &P) {
         sequence(P, b, t0, n, prefix);
         total = prefix + n;
-        tiles = (total + kTok - 1) / kTok;
+        tiles = (total + P.tok - 1) / P.tok;
         nrt = (n * P.group + RT - 1) / RT;
         items = (uint32_t)P.a.Hkv * (uint32_t)nrt;
     }
@@ -171,6 +170,30 @@ __device__ __forceinline__ float exp2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// One lane of the (whole) warp, always the same.
+__device__ __forceinline__ uint32_t elect() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(r));
+    return r;
+}
+// As mma_f16 and mma_commit, by the lane whose `on` is set: a predicate in
+// place of a branch keeps the operands in uniform registers.
+__device__ __forceinline__ void mma_on(uint32_t on, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                       uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(on)
+        : "memory");
+}
+__device__ __forceinline__ void commit_on(uint32_t on, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(
+            smem_addr(bar)),
+        "r"(on)
+        : "memory");
 }
 // floats as integers of the same order
 __device__ __forceinline__ int ordered(float f) {
@@ -254,7 +277,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
     const sgmv_tree_attention_args &a = P.a;
     extern __shared__ __align__(1024) uint8_t dsm[];
     __shared__ __align__(8) uint64_t full[S::kStages], empty[S::kStages], q_full[S::kQ], q_empty[S::kQ];
-    __shared__ __align__(8) uint64_t s_full[2], s_empty[2], p_full, pv_done, drained;
+    __shared__ __align__(8) uint64_t p_full, drained;
     __shared__ uint32_t s_tmem;
     __shared__ int s_lost, s_poison, s_last;
     __shared__ int s_b;
@@ -268,12 +291,9 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
     if (warp == kMmaWarp) {
         if (lane == 0) {
             for (int i = 0; i < S::kStages; ++i)
-                mbar_init(&full[i], P.box ? 1 : kLoaders), mbar_init(&empty[i], 1);
-            for (int i = 0; i < S::kQ; ++i)
-                mbar_init(&q_full[i], P.box ? kLoaders - 32 : kLoaders), mbar_init(&q_empty[i], 1);
-            for (int i = 0; i < 2; ++i) mbar_init(&s_full[i], 1), mbar_init(&s_empty[i], S::kSoft);
+                mbar_init(&full[i], P.box ? kLoaders / 32 : kLoaders), mbar_init(&empty[i], 1);
+            for (int i = 0; i < S::kQ; ++i) mbar_init(&q_full[i], kLoaders), mbar_init(&q_empty[i], 1);
             mbar_init(&p_full, S::kSoft);
-            mbar_init(&pv_done, 1);
             mbar_init(&drained, 1);
             mbar_init_fence();
             s_lost = 0;
@@ -284,7 +304,10 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
     }
     for (int i = tid; i < RT; i += S::kThreads) s_ref[i] = kUnset;
     // columns past D that the products read are zero: in Q, and in K where TMA
-    // does not fill them
+    // does not fill them; so are the rows past a short tile
+    if (P.tok < kTok)
+        for (uint32_t i = tid * 16u; i < S::kOffQ; i += S::kThreads * 16u)
+            sts128(sm + i, make_uint4(0, 0, 0, 0));
     if (a.D % 64 != 0)
         for (uint32_t i = (P.box ? S::kOffQ : 0u) + tid * 16u; i < S::kOffP; i += S::kThreads * 16u)
             sts128(sm + i, make_uint4(0, 0, 0, 0));
@@ -370,14 +393,12 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
             cp_async_arrive(&q_full[qb]);
             ++seg;
         };
-        if (P.box && lt >= 32) {
-            while (cur.next(P)) load_q(lt - 32, kLoaders - 32);
-            asm volatile("cp.async.wait_all;" ::: "memory");
-        } else if (P.box) {
-            // TMA: lane = one box (tokens x 64 columns) of a tile
-            const int box = P.box, nbox = kTok / box, mine = lane % nbox, half = lane / nbox;
+        if (P.box) {
+            // TMA: a box (tokens x 64 columns) per lane, dealt to the three warps
+            const int box = P.box, nbox = P.tok / box, op = lane * (kLoaders / 32) + lt / 32;
+            const int mine = op % nbox, half = op / nbox;
             const bool busy = half < halves;
-            const uint32_t bytes = (uint32_t)halves * kHalf;
+            const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, busy)) * (uint32_t)box * 128u;
             const uint32_t at = (uint32_t)half * kHalf + (uint32_t)(mine * box) * 128u;
             Cur peek = cur;   // the tile whose page is looked up next
             int peek_tile = 0, peek_end = 0;
@@ -389,7 +410,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
                     peek_tile = peek.tile;
                     peek_end = peek.end;
                 }
-                const int j = peek_tile * kTok + mine * box;
+                const int j = peek_tile * P.tok + mine * box;
                 next_in = -1;
                 if (j < peek.total) {
                     const int pg = j / a.block_size;
@@ -410,6 +431,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
             int in = 0, old_in = 0, old_h = 0;
             look();
             while (cur.next(P)) {
+                load_q(lt, kLoaders);
                 for (int tile = cur.tile; tile < cur.end; ++tile, ++g) {
                     // boxes past the end, and pages out of range, read as zeros
                     page = next_page;
@@ -428,6 +450,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
                 }
             }
             copy_boxes(&P.map_v, old_page, old_in, old_h);
+            asm volatile("cp.async.wait_all;" ::: "memory");
         } else {
         int64_t head_off = 0, prev_head = 0;
         auto copy_tile = [&](const void *cache, int64_t off, int tile) {
@@ -515,11 +538,22 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
         // ---- MMA issuer ------------------------------------------------------
         const uint32_t idesc_s = idesc_f16(kBf16, kTok, RT) & ~(1u << 16);   // both K-major
         const uint32_t idesc_o = idesc_f16(kBf16, kTok, RT) | (1u << 15);    // both MN-major
-        const uint32_t ring = smem_addr(sm), qa = ring + S::kOffQ, pa = ring + S::kOffP;
+        const uint32_t ring = smem_addr(sm), on = elect();
+        // descriptors of the first stage and buffers; offsets add to them (bytes / 16)
+        const uint64_t k_desc = sw128_desc(ring, 16, 1024), v_desc = sw128_desc(ring, kHalf, 1024);
+        const uint64_t q_desc = sw128_desc(ring + S::kOffQ, 16, 1024);
+        const uint64_t p_desc = sw128_desc(ring + S::kOffP, kHalf, 1024);
         const int N = (int)(w1 - w0);
-        int pos = 0, seg = -1;       // ring position of the next operand
+        const bool wide = D > 64;
+        int st = 0, seg = -1;        // ring stage of the next operand
+        uint32_t ph = 0;             // and its phase
+        auto advance = [&]() {
+            if (++st == S::kStages) st = 0, ph ^= 1;
+        };
         Cur ahead = cur;             // segment of the next score product
         int left = 0;                // its tiles not yet issued
+        // Score product of tile g.  Its accumulator was last read for tile
+        // g - 2, before that tile's P was complete.
         auto scores = [&](int g) {
             bool first = false;
             if (left == 0) {
@@ -530,58 +564,49 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
             }
             const int qb = seg % S::kQ;
             if (first) await(&q_full[qb], (uint32_t)(seg / S::kQ) & 1, lost);
-            const int st = pos % S::kStages;
-            await(&full[st], (uint32_t)(pos / S::kStages) & 1, lost);
-            if (g >= 2) await(&s_empty[g & 1], (uint32_t)(g / 2 - 1) & 1, lost);
+            await(&full[st], ph, lost);
             --left;
-            if (lane == 0) {
-                fence_proxy_async();  // cp.async (generic proxy) data -> tensor core (async proxy)
-                tc_fence_after();
-                const uint32_t ka = ring + (uint32_t)st * kStage, q = qa + (uint32_t)qb * S::kQBytes;
+            // cp.async (generic proxy) data -> tensor core (async proxy)
+            if (first || !P.box) fence_proxy_async();
+            tc_fence_after();
+            const uint64_t kd = k_desc + (uint32_t)st * (kStage >> 4);
+            const uint64_t qd = q_desc + (uint32_t)qb * (S::kQBytes >> 4);
+            const uint32_t d = tmem + (uint32_t)((g & 1) * RT);
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk) {
-                    if (kk >= 4 && D <= 64) break;
-                    mma_f16(tmem + (uint32_t)((g & 1) * RT),
-                            sw128_desc(ka + (kk >> 2) * kHalf + (kk & 3) * 32, 16, 1024),
-                            sw128_desc(q + (kk >> 2) * (RT * 128u) + (kk & 3) * 32, 16, 1024), idesc_s, kk != 0);
-                }
-                mma_commit(&empty[st]);
-                mma_commit(&s_full[g & 1]);
-                if (left == 0) mma_commit(&q_empty[qb]);
+            for (int kk = 0; kk < 4; ++kk) mma_on(on, d, kd + kk * 2, qd + kk * 2, idesc_s, kk != 0);
+            if (wide) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_on(on, d, kd + (kHalf >> 4) + kk * 2, qd + RT * 8u + kk * 2, idesc_s, 1);
             }
-            __syncwarp();
-            ++pos;
+            commit_on(on, &empty[st]);  // also tells the softmax that the scores are there
+            if (left == 0) commit_on(on, &q_empty[qb]);
+            advance();
         };
         scores(0);
         cur.next(P);
         int tile = cur.tile;
         for (int g = 0; g < N; ++g) {
             if (g + 1 < N) scores(g + 1);
-            const int st = pos % S::kStages;
-            await(&full[st], (uint32_t)(pos / S::kStages) & 1, lost);
+            await(&full[st], ph, lost);
             await(&p_full, (uint32_t)g & 1, lost);
             if (tile == cur.end) {
                 cur.next(P);
                 tile = cur.tile;
             }
-            if (lane == 0) {
-                fence_proxy_async();
-                tc_fence_after();
-                const uint32_t va = ring + (uint32_t)st * kStage;
+            if (!P.box) fence_proxy_async();
+            tc_fence_after();
+            const uint64_t vd = v_desc + (uint32_t)st * (kStage >> 4);
+            const uint32_t more = tile != cur.tile;
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    mma_f16(tmem + 2 * RT, sw128_desc(va + kk * 2048, kHalf, 1024),
-                            sw128_desc(pa + kk * 2048, kHalf, 1024), idesc_o, (tile != cur.tile) || kk != 0);
-                mma_commit(&empty[st]);
-                mma_commit(&pv_done);
-            }
-            __syncwarp();
-            ++pos;
+            for (int kk = 0; kk < 8; ++kk)
+                mma_on(on, tmem + 2 * RT, vd + kk * 128, p_desc + kk * 128, idesc_o, kk ? 1u : more);
+            commit_on(on, &empty[st]);  // also tells the softmax that P has been read
+            advance();
             ++tile;
         }
         // nothing of this kernel's is in flight when tensor memory is returned
-        if (lane == 0) mma_commit(&drained);
-        __syncwarp();
+        commit_on(on, &drained);
         await(&drained, 0, lost);
     } else {
         // ---- softmax and output: thread = token, then = head column ------------
@@ -590,17 +615,25 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
         const uint32_t t_s = tmem + lanes + (uint32_t)r0, t_o = tmem + lanes + 2 * RT + (uint32_t)r0;
         uint32_t *const see = reinterpret_cast<uint32_t *>(sm + S::kOffSee);
         int64_t *const row_out = reinterpret_cast<int64_t *>(sm + S::kOffRow);
-        uint8_t *const prow = sm + S::kOffP + (uint32_t)wg * kHalf;
+        uint8_t *const prow = sm + S::kOffP + (uint32_t)(wg >> 1) * kHalf;
+        const int pchunk = (wg & 1) * 4;
         const float c = P.c;
         float l[S::kRows];
         int see_b = -1, see_rt = -1;
-        int g = 0, pos_v = 2;  // tile; ring position of its V
         const int N = (int)(w1 - w0);
+        int g = 0;  // tile
+        // K of tile g is the ring's operand 2g - 1 (0 for the first), V is 2g + 2
+        // (2g + 1 for the last).  The commit that frees an operand's stage is
+        // the softmax's signal that the product is done; it waits for each
+        // before the stage can be freed again.
+        auto v_pos = [&](int g) { return g + 1 < N ? 2 * g + 2 : 2 * g + 1; };
+        auto done = [&](int pos) {
+            await(&empty[pos % S::kStages], (uint32_t)(pos / S::kStages) & 1, lost);
+            tc_fence_after();
+        };
         for (int seg = 0; cur.next(P); ++seg) {
             const int R = min(RT, cur.n * group - cur.rt * RT);  // rows in use
-#pragma unroll
-            for (int r = 0; r < S::kRows; ++r) l[r] = 0.f;
-            if (cur.end * kTok > cur.prefix && (see_b != cur.b || see_rt != cur.rt)) {
+            if (cur.end * P.tok > cur.prefix && (see_b != cur.b || see_rt != cur.rt)) {
                 // see[j]: the rows that see tree node j.  Ancestors by pointer
                 // doubling in the (idle) P buffer; invalid parents count as padding.
                 see_b = cur.b;
@@ -613,10 +646,10 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
                     if (p < -2 || p >= i) set_error(P.err, kErrBadIndex);
                     return p < -1 || p >= i ? -2 : p;
                 };
-                named_sync<4, S::kSoft>();
+                named_sync<6, S::kSoft>();
                 for (int i = tid; i < n; i += S::kSoft) up[i] = parent(i);
-                named_sync<4, S::kSoft>();
-                constexpr int kPer = SGMV_TREE_MAX_NODES / S::kSoft;
+                named_sync<6, S::kSoft>();
+                constexpr int kPer = (SGMV_TREE_MAX_NODES + S::kSoft - 1) / S::kSoft;
                 uint32_t word[kPer][8];
                 int to[kPer];
 #pragma unroll
@@ -629,11 +662,11 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
 #pragma unroll
                     for (int k = 0; k < 8; ++k) anc[i * 8 + k] = p != -2 && (i >> 5) == k ? 1u << (i & 31) : 0u;
                 }
-                named_sync<4, S::kSoft>();
+                named_sync<6, S::kSoft>();
 #pragma unroll
                 for (int e = 0; e < kPer; ++e)
                     if (tid + e * S::kSoft < n) up[tid + e * S::kSoft] = to[e];
-                named_sync<4, S::kSoft>();
+                named_sync<6, S::kSoft>();
                 for (int reach = 1; reach < n; reach <<= 1) {
 #pragma unroll
                     for (int e = 0; e < kPer; ++e) {
@@ -645,7 +678,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
                         for (int k = 0; k < 8; ++k)
                             word[e][k] = anc[i * 8 + k] | (p >= 0 ? anc[p * 8 + k] : 0u);
                     }
-                    named_sync<4, S::kSoft>();
+                    named_sync<6, S::kSoft>();
 #pragma unroll
                     for (int e = 0; e < kPer; ++e) {
                         const int i = tid + e * S::kSoft;
@@ -654,7 +687,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
 #pragma unroll
                         for (int k = 0; k < 8; ++k) anc[i * 8 + k] = word[e][k];
                     }
-                    named_sync<4, S::kSoft>();
+                    named_sync<6, S::kSoft>();
                 }
                 for (int i = tid; i < n * S::kWords; i += S::kSoft) {
                     const int j = i / S::kWords, k = i - j * S::kWords;
@@ -668,29 +701,26 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
                     }
                     see[i] = bits;
                 }
-                named_sync<4, S::kSoft>();
+                named_sync<6, S::kSoft>();
             }
+#pragma unroll
+            for (int r = 0; r < S::kRows; ++r) l[r] = 0.f;
             for (int tile = cur.tile; tile < cur.end; ++tile, ++g) {
-                await(&s_full[g & 1], (uint32_t)(g / 2) & 1, lost);
-                tc_fence_after();
+                done(g > 0 ? 2 * g - 1 : 0);
                 const uint32_t ts = t_s + (uint32_t)((g & 1) * RT);
                 // which rows see this token: all, none, or a node's
-                const int j = tile * kTok + tok;
-                const bool edge = (tile + 1) * kTok > cur.prefix;
-                uint32_t vis[(S::kRows + 31) / 32];
+                const int j = tile * P.tok + tok;
+                const bool tree = (tile + 1) * P.tok > cur.prefix, edge = tree || P.tok < kTok;
+                uint32_t vis = 0xffffffffu;
+                if (edge && (tok >= P.tok || j >= cur.prefix))
+                    vis = tok < P.tok && j < cur.total ? see[(j - cur.prefix) * S::kWords + wg] : 0u;
+                float s[S::kRows];
+                // the masked exponents
+                auto exponents = [&]() {
+                    tmem_load(ts, s);
 #pragma unroll
-                for (int k = 0; k < (S::kRows + 31) / 32; ++k) {
-                    vis[k] = 0xffffffffu;
-                    if (edge && j >= cur.prefix)
-                        vis[k] = j < cur.total ? see[(j - cur.prefix) * S::kWords + r0 / 32 + k] : 0u;
-                }
-                float s[S::kChunk];
-                // masked exponents of one chunk; v: over the slack
-                auto exponents = [&](int ch) {
-                    tmem_load(ts + (uint32_t)(ch * S::kChunk), s);
-#pragma unroll
-                    for (int i = 0; i < S::kChunk; i += 4) {
-                        const uint4 u = lds128(&s_ref[r0 + ch * S::kChunk + i]);
+                    for (int i = 0; i < S::kRows; i += 4) {
+                        const uint4 u = lds128(&s_ref[r0 + i]);
                         s[i] = fmaf(s[i], c, -__uint_as_float(u.x));
                         s[i + 1] = fmaf(s[i + 1], c, -__uint_as_float(u.y));
                         s[i + 2] = fmaf(s[i + 2], c, -__uint_as_float(u.z));
@@ -698,32 +728,25 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
                     }
                     if (edge) {
 #pragma unroll
-                        for (int i = 0; i < S::kChunk; ++i)
-                            if (!(vis[ch] >> i & 1u)) s[i] = -INFINITY;
+                        for (int i = 0; i < S::kRows; ++i)
+                            if (!(vis >> i & 1u)) s[i] = -INFINITY;
                     }
                 };
+                exponents();
                 float top = -INFINITY;
 #pragma unroll
-                for (int ch = 0; ch < S::kChunks; ++ch) {
-                    exponents(ch);
-#pragma unroll
-                    for (int i = 0; i < S::kChunk; ++i) top = fmaxf(top, s[i]);
-                }
-                const bool moved = group_any(wg, top > kBias + kSlack);
-                if (moved) {
+                for (int i = 0; i < S::kRows; ++i) top = fmaxf(top, s[i]);
+                if (group_any(wg, top > kBias + kSlack)) {
                     // new references: the larger of the old and this tile's maximum
+                    tmem_load(ts, s);
+                    int mine = 0;
 #pragma unroll
-                    for (int ch = 0; ch < S::kChunks; ++ch) {
-                        tmem_load(ts + (uint32_t)(ch * S::kChunk), s);
-                        int mine = 0;
-#pragma unroll
-                        for (int i = 0; i < S::kChunk; ++i) {
-                            const float y = !edge || (vis[ch] >> i & 1u) ? s[i] * c : -INFINITY;
-                            const int m = __reduce_max_sync(0xffffffffu, ordered(y));
-                            if (lane == i) mine = m;
-                        }
-                        if (lane < S::kChunk) s_red[warp & 3][r0 + ch * S::kChunk + lane] = unordered(mine);
+                    for (int i = 0; i < S::kRows; ++i) {
+                        const float y = !edge || (vis >> i & 1u) ? s[i] * c : -INFINITY;
+                        const int m = __reduce_max_sync(0xffffffffu, ordered(y));
+                        if (lane == i) mine = m;
                     }
+                    if (lane < S::kRows) s_red[warp & 3][r0 + lane] = unordered(mine);
                     group_bar(wg);
                     if (tok < S::kRows) {
                         const int r = r0 + tok;
@@ -742,43 +765,33 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
 #pragma unroll
                     for (int r = 0; r < S::kRows; ++r) l[r] *= s_fac[r0 + r];
                     if (tile != cur.tile) {
-                        await(&pv_done, (uint32_t)(g - 1) & 1, lost);
-                        tc_fence_after();
+                        done(v_pos(g - 1));
+                        tmem_load(t_o, s);
 #pragma unroll
-                        for (int ch = 0; ch < S::kChunks; ++ch) {
-                            tmem_load(t_o + (uint32_t)(ch * S::kChunk), s);
-#pragma unroll
-                            for (int i = 0; i < S::kChunk; ++i) s[i] *= s_fac[r0 + ch * S::kChunk + i];
-                            tmem_store(t_o + (uint32_t)(ch * S::kChunk), s);
-                        }
+                        for (int i = 0; i < S::kRows; ++i) s[i] *= s_fac[r0 + i];
+                        tmem_store(t_o, s);
                     }
+                    exponents();
+                }
+                T p[S::kRows];  // rounded to the tensor cores' operand type
+#pragma unroll
+                for (int i = 0; i < S::kRows; ++i) {
+                    const float e = exp2_approx(s[i]);
+                    l[i] += e;
+                    p[i] = from_f<T>(e);
                 }
                 // the previous tile's P has been read
-                if (g > 0) await(&pv_done, (uint32_t)(g - 1) & 1, lost);
+                if (g > 0) done(v_pos(g - 1));
 #pragma unroll
-                for (int ch = 0; ch < S::kChunks; ++ch) {
-                    if (S::kChunks > 1 || moved) exponents(ch);
-                    T p[S::kChunk];
-#pragma unroll
-                    for (int i = 0; i < S::kChunk; ++i) {
-                        const float e = exp2_approx(s[i]);
-                        l[ch * S::kChunk + i] += e;
-                        p[i] = from_f<T>(e);  // the tensor cores' operand type
-                    }
-#pragma unroll
-                    for (int q = 0; q < S::kChunk / 8; ++q)
-                        sts128(prow + sw128_offset(tok, ch * (S::kChunk / 8) + q),
-                               reinterpret_cast<const uint4 *>(p)[q]);
-                }
-                tc_fence_before();
-                mbar_arrive(&s_empty[g & 1]);
-                if (edge) {
+                for (int q = 0; q < S::kRows / 8; ++q)
+                    sts128(prow + sw128_offset(tok, pchunk + q), reinterpret_cast<const uint4 *>(p)[q]);
+                if (tree) {
                     // non-finite v of tree nodes: out of the tile, noted; what TMA
                     // brought from the last page past the end: zeroed
-                    const int v0 = max(0, cur.prefix - tile * kTok), v1 = min(kTok, cur.total - tile * kTok);
-                    const int ve = P.box ? min(kTok, (v1 + P.box - 1) / P.box * P.box) : v1;
+                    const int v0 = max(0, cur.prefix - tile * P.tok), v1 = min(P.tok, cur.total - tile * P.tok);
+                    const int ve = P.box ? (v1 + P.box - 1) / P.box * P.box : v1;
                     const int cpr = D / 8;
-                    const int pv = g + 1 < N ? pos_v : pos_v - 1;
+                    const int pv = v_pos(g);
                     await(&full[pv % S::kStages], (uint32_t)(pv / S::kStages) & 1, lost);
                     uint8_t *const vt = sm + (uint32_t)(pv % S::kStages) * kStage;
                     for (int i = tid; i < (ve - v0) * cpr; i += S::kSoft) {
@@ -805,10 +818,8 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
                 fence_proxy_async();
                 tc_fence_before();
                 mbar_arrive(&p_full);
-                pos_v += 2;
             }
-            await(&pv_done, (uint32_t)(g - 1) & 1, lost);
-            tc_fence_after();
+            done(v_pos(g - 1));
 
             // ---- the segment's sums and rows' places -----------------------------
             {
@@ -816,10 +827,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
 #pragma unroll
                 for (int r = 0; r < S::kRows; ++r) v[r] = l[r];
                 const int r = warp_sums(v, lane);
-                constexpr int per = S::kRows / 32 ? S::kRows / 32 : 1;
-#pragma unroll
-                for (int i = 0; i < per; ++i)
-                    if (S::kRows >= 32 || (lane & 1) == 0) s_red[warp & 3][r0 + r + i] = v[i];
+                if (S::kRows == 32 || (lane & 1) == 0) s_red[warp & 3][r0 + r] = v[0];
             }
             group_bar(wg);
             const bool whole = cur.tile == 0 && cur.end == cur.item_tiles;
@@ -853,13 +861,11 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
             group_bar(wg);
             const bool poison = *(volatile int *)&s_poison == seg, ok = !*lost;
             const int d = tok;
-#pragma unroll
-            for (int ch = 0; ch < S::kChunks; ++ch) {
-                float v[S::kChunk];
-                tmem_load(t_o + (uint32_t)(ch * S::kChunk), v);
-                const int rc = r0 + ch * S::kChunk;
+            {
+                float v[S::kRows];
+                tmem_load(t_o, v);
                 if (poison && d < D) {
-                    for (int jn = max(0, cur.tile * kTok - cur.prefix); jn < min(cur.n, cur.end * kTok - cur.prefix); ++jn) {
+                    for (int jn = max(0, cur.tile * P.tok - cur.prefix); jn < min(cur.n, cur.end * P.tok - cur.prefix); ++jn) {
                         const int j = cur.prefix + jn, pg = j / a.block_size;
                         const int32_t block = a.block_table[cur.b * a.table_row + pg];
                         if (block < 0 || block >= a.num_blocks) continue;
@@ -867,18 +873,18 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
                                                                      (int64_t)(j - pg * a.block_size) * a.cache_token +
                                                                      (int64_t)cur.h * a.cache_head + d];
                         if (!bad16<T>(*reinterpret_cast<const unsigned short *>(&x))) continue;
-                        const uint32_t bits = see[jn * S::kWords + rc / 32] >> (rc % 32);
+                        const uint32_t bits = see[jn * S::kWords + wg];
 #pragma unroll
-                        for (int i = 0; i < S::kChunk; ++i)
+                        for (int i = 0; i < S::kRows; ++i)
                             if (bits >> i & 1u) v[i] += to_f<T>(x);
                     }
                 }
                 if (whole) {
                     if (d < D && ok) {
 #pragma unroll
-                        for (int i = 0; i < S::kChunk; ++i) {
-                            const int64_t to = row_out[rc + i];
-                            const float f = s_fac[rc + i];
+                        for (int i = 0; i < S::kRows; ++i) {
+                            const int64_t to = row_out[r0 + i];
+                            const float f = s_fac[r0 + i];
                             if (to >= 0)
                                 static_cast<T *>(a.out)[to + d] = from_f<T>(f == 0.f ? 0.f : v[i] * f);
                             else if (to < -1)
@@ -886,24 +892,24 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
                         }
                     }
                 } else {
-                    float *const part = P.part + ((int64_t)slot * RT + rc) * 128 + d;
+                    float *const part = P.part + ((int64_t)slot * RT + r0) * 128 + d;
 #pragma unroll
-                    for (int i = 0; i < S::kChunk; ++i)
-                        if (rc + i < R) part[i * 128] = v[i];
+                    for (int i = 0; i < S::kRows; ++i)
+                        if (r0 + i < R) part[i * 128] = v[i];
                 }
             }
             if (!whole) {
                 // the last CTA of the item to finish joins its parts, in share order
                 const int first = (int)(cur.item0 / share), last = (int)((cur.item0 + cur.item_tiles - 1) / share);
                 __threadfence();
-                named_sync<4, S::kSoft>();
+                named_sync<6, S::kSoft>();
                 if (tid == 0) {
                     const int done = atomicAdd(&P.count[first], 1);
                     s_last = done == last - first;
                     if (done == last - first) P.count[first] = 0;  // ready for the next call
                     __threadfence();
                 }
-                named_sync<4, S::kSoft>();
+                named_sync<6, S::kSoft>();
                 if (s_last) {
                     auto at = [&](int k, int r) { return (int64_t)(2 * k + (k == first)) * RT + r; };
                     for (int r = tid; r < R; r += S::kSoft) {
@@ -928,7 +934,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
                                 none ? -INFINITY : (M + log2f(L)) * 0.693147180559945309f;
                         }
                     }
-                    named_sync<4, S::kSoft>();
+                    named_sync<6, S::kSoft>();
                     constexpr int kJoin = 8;  // rows whose parts are in flight together
                     for (int rc = wg * kJoin; rc < R && d < D; rc += kJoin * S::kGroups) {
                         float o[kJoin] = {};
@@ -954,7 +960,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
                 }
             }
             // every thread has read the rows' places, sums and the poison mark
-            named_sync<4, S::kSoft>();
+            named_sync<6, S::kSoft>();
         }
         if (tid == 0 && *lost) set_error(P.err, kErrTimeout);
     }
@@ -1000,7 +1006,15 @@ int tree_mma_launch(const sgmv_tree_attention_args &a, int nsm, int *err, cudaSt
     p.part = p.ml + (size_t)kMaxCtas * 2 * rt * 2;
     p.err = err;
     const bool bf16 = a.dtype == SGMV_BF16;
+    // Boxes are as high as pages allow: TMA's cost here is per box (at pages
+    // of 24 tokens, boxes of 8 filling every tile measured 115 us, boxes of 24 and tiles of
+    // 120 tokens XX us, on 128 sequences of up to 2100 tokens, 4 heads of 80)
     p.box = std::gcd(a.block_size, kTok);
+    p.tok = kTok;
+    if (a.block_size % 8 == 0 && a.block_size < kTok && a.block_size > p.box) {
+        p.box = a.block_size;
+        p.tok = kTok / p.box * p.box;
+    }
     if (p.box >= 8) {
         const cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)a.block_size, (cuuint64_t)a.Hkv,
                                     (cuuint64_t)a.num_blocks};
@@ -1009,7 +1023,7 @@ int tree_mma_launch(const sgmv_tree_attention_args &a, int nsm, int *err, cudaSt
         const cuuint32_t box[4] = {64, (cuuint32_t)p.box, 1, 1};
         if (!tmap_encode(&p.map_k, bf16, 4, a.k_cache, dims, strides, box, true) ||
             !tmap_encode(&p.map_v, bf16, 4, a.v_cache, dims, strides, box, true))
-            p.box = 0;  // strides that a tensor map cannot hold
+            p.box = 0, p.tok = kTok;  // strides that a tensor map cannot hold
     } else {
         p.box = 0;
     }
