@@ -125,7 +125,8 @@ int sgmv_tree_attention(const sgmv_tree_attention_args *args, void *stream) {
     int *err = device_error_word();
     if (!err) return SGMV_ERR_CUDA;
     return finish("tree attention kernel",
-                  tree_attention_launch(a, device_sms(), err, static_cast<cudaStream_t>(stream)), 1);
+                  tree_attention_launch(a, device_sms(), err, static_cast<cudaStream_t>(stream)),
+                  a.D <= kMmaMaxD ? 2 : 1);
 }
 
 int sgmv_tree_verify(const sgmv_tree_verify_args *args, void *stream) {

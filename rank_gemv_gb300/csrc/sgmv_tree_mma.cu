@@ -11,23 +11,28 @@
 //   O^T [columns x RT] += V^T . P^T      A = V tile (M-major),  B = P
 //
 // with S^T and O^T in tensor memory.  A softmax thread owns one token: it
-// reads its RT scores, makes p = 2^(c s - ref[row]) and writes them as one row
+// reads its scores, makes p = 2^(c s - ref[row]) and writes them as one row
 // of P.  ref[row] is the row's running maximum, moved only when a score
 // exceeds it by more than 2^kSlack (then O^T and the sums are scaled), so an
 // ordinary tile needs one vote and no reduction over tokens.
 //
 // Decomposition: the (sequence, head, row tile) items, each of ceil(length /
-// 128) token tiles, form one line that is cut into equal shares, one per CTA
-// (one CTA per SM).  A share that covers an item writes its output; items cut
-// across shares leave unnormalised O, sum and maximum in the workspace, and
-// the CTA that finishes last joins them in share order.
+// 128) token tiles, form one line of work for a persistent grid of one CTA
+// per SM.  A CTA takes its share of the line's first part, then claims small
+// shares of the rest as it finishes.  A share that covers an item writes its
+// output; items cut across shares leave unnormalised O, sums and references in
+// the workspace, and a second, small kernel joins them, in share order (so
+// results do not depend on who claimed what).  Joined by whichever CTA finished last,
+// behind a fence and a counter, each join cost 15 us of that CTA's time: its
+// chain of loads queued behind the stream of K and V.
 //
-// Warps: 4 (RT <= 64) or 8 softmax warps, then one that issues the MMAs, then
-// three that bring K, V (a ring of 32 KB stages) and Q in with cp.async, 16
-// bytes per lane, through the block table: any page size, and tokens past the
-// end become zeros.  The MMA warp runs one score product ahead of the softmax.
+// Warps: 4, 4, 8 or 16 for the softmax (32 rows each four); one that issues the
+// MMAs, a score product ahead of the softmax; one that walks the line, claims,
+// brings Q in and says which rows see which tree nodes; two that bring K and V
+// into a ring of 32 KB stages, through the block table: by TMA, or, for pages
+// that are no multiple of 8 tokens, with cp.async, 16 bytes per lane.
 //
-// Values of rows a query does not see never reach it: scores are masked after
+// Values that a row does not see never reach it: scores are masked after
 // the product, and non-finite v of tree nodes are taken out of the staged
 // tile (a masked weight of 0 times infinity would be NaN) and added back for
 // the rows that do see them.
@@ -44,33 +49,39 @@
 namespace sgmv {
 namespace {
 
-constexpr int kTok = 128;                // tokens per tile
+constexpr int kTok = 128;                // lanes: tokens per tile, at most
 constexpr uint32_t kHalf = kTok * 128u;  // bytes of 64 columns of a tile
 constexpr uint32_t kStage = 2 * kHalf;   // a K or V tile, 128 columns
-constexpr int kLoaders = 96;             // loading threads
+constexpr int kLoaders = 64;             // loading threads
+constexpr int kSegs = 4;                 // segments known ahead
 constexpr float kUnset = -3e38f;         // ref of a row that has seen nothing
 constexpr float kBias = 7.f;             // weights are 2^(kBias + score - ref) ...
 constexpr float kSlack = 8.f;            // ... <= 2^(kBias + kSlack), finite in f16
 constexpr int kMaxCtas = 152;
+constexpr int kSeqTable = 512;           // entries of the table that finds a tile's sequence
+constexpr int kMaxParts = 64;            // parts of an item (about)
 
 template <int RT> struct Shape {
     static constexpr int kGroups = RT > 32 ? RT / 32 : 1;  // softmax warpgroups
     static constexpr int kRows = RT / kGroups;            // rows per warpgroup
     static constexpr int kSoft = 128 * kGroups;           // softmax threads
-    static constexpr int kThreads = kSoft + 32 + kLoaders;
+    static constexpr int kThreads = kSoft + 64 + kLoaders;
     static constexpr int kQ = RT > 64 ? 1 : 2;            // Q buffers
     static constexpr int kStages = RT > 64 ? 4 : 5;
     static constexpr int kWords = RT < 32 ? 1 : RT / 32;  // words of one bit per row
     static constexpr uint32_t kQBytes = RT * 256u;
     static constexpr uint32_t kPBytes = (RT > 64 ? 2 : 1) * kHalf;
+    // shares claimed at run time, per CTA: their least tiles, and how many of them
+    static constexpr int kLeast = RT / 8, kClaims = RT <= 32 ? 8 : RT <= 64 ? 4 : 2;
+    static constexpr int kShares = kMaxCtas * (1 + kClaims);
     static constexpr uint32_t kTmem = RT <= 16 ? 64 : RT <= 32 ? 128 : RT <= 64 ? 256 : 512;
     // dynamic shared memory
     static constexpr uint32_t kOffQ = kStages * kStage;
     static constexpr uint32_t kOffP = kOffQ + kQ * kQBytes;
-    static constexpr uint32_t kOffTab = kOffP + kPBytes;                 // row offsets of 4 tiles
-    static constexpr uint32_t kOffSee = kOffTab + 4u * kTok * 8u;        // who sees each node
-    static constexpr uint32_t kOffRow = kOffSee + SGMV_TREE_MAX_NODES * kWords * 4u;  // rows' outputs
-    static constexpr uint32_t kBytes = kOffRow + RT * 8u + 1024u;        // + alignment
+    static constexpr uint32_t kOffTab = kOffP + kPBytes;            // cp.async: row offsets of 2 tiles
+    static constexpr uint32_t kOffSee = kOffTab + 2u * kTok * 8u;   // who sees each node, two trees
+    static constexpr uint32_t kOffRow = kOffSee + 2u * SGMV_TREE_MAX_NODES * kWords * 4u;  // rows' places
+    static constexpr uint32_t kBytes = kOffRow + kSegs * RT * 8u + 1024u;  // + alignment
 };
 
 struct MmaParams {
@@ -81,72 +92,74 @@ struct MmaParams {
     sgmv_tree_attention_args a;
     float c;          // scale * log2(e)
     int32_t group;    // query heads per KV head
-    int *count;       // [CTA]: partial items finished, by their first CTA
-    float *ml;        // [CTA][2][RT][2]: reference and sum of partial items
-    float *part;      // [CTA][2][RT][128]
+    int *claim;       // shares claimed (0 between calls); shares of this call
+    struct Cut *cut;  // [share]: the cut item that begins there
+    float *ml;        // [share][2][RT][2]: reference and sum of parts of items
+    float *part;      // [share][2][RT][128]
     int *err;
 };
 
-// A place in the line of work, advanced segment by segment (a segment: the
-// tiles of one item inside this CTA's share).
-template <int RT> struct Cursor {
-    int b, t0, n, prefix, total, tiles, nrt;
-    int64_t base, w, w1;  // first tile of sequence b; next tile; end of the share
-    uint32_t items;
-    // the current segment
-    int h, rt, tile, end, item_tiles;
-    int64_t item0;
+// An item whose parts are in the workspace; parts = 0: none.
+struct Cut {
+    int t0, n, h, rt, first, parts, pad0, pad1;
+};
 
-    __device__ __forceinline__ static bool sequence(const MmaParams &P, int b, int &t0, int &n,
-                                                    int &prefix) {
+// The tiles of one item inside one share.  Begins at the item's first tile:
+// slot 2 share + 1, else 2 share (the share's first).
+struct Segment {
+    int b, t0, n, prefix, total;     // sequence
+    int h, rt;                       // KV head, row tile
+    int tile, end;                   // tiles; end = 0: no more segments
+    int whole;                       // the whole item
+    int slot;                        // where a part goes
+    int see;                         // which tree table
+};
+
+// How the line of W tiles is cut.  Share i < ctas is CTA i's own, `own` tiles
+// each; the rest is cut into shares of `small` tiles that CTAs claim as they
+// finish: with equal shares alone, the SMs' unequal memory bandwidth left the
+// slowest CTA at 202 us and the average at 177 (32 trees over 4096 tokens).
+struct Plan {
+    int64_t W, own, split, small;    // split: where the claimed shares begin
+    int32_t ctas, shares, stride;
+    int64_t before[kSeqTable];       // tiles before every stride-th sequence
+
+    __device__ __forceinline__ int of(int64_t w) const {
+        return w < split ? (int)(w / own) : ctas + (int)((w - split) / small);
+    }
+    __device__ __forceinline__ void range(int id, int64_t &w, int64_t &w1) const {
+        w = id < ctas ? id * own : split + (id - ctas) * small;
+        w1 = w + (id < ctas ? own : small);
+        const int64_t end = id < ctas ? split : W;
+        w1 = w1 < end ? w1 : end;
+    }
+};
+
+// A sequence's part of the line.
+struct Sequence {
+    int b, t0, n, prefix, total, tiles, nrt;
+    uint32_t items;
+
+    // false: bad metadata
+    template <int RT> __device__ __forceinline__ bool enter(const MmaParams &P, int b_) {
         const sgmv_tree_attention_args &a = P.a;
+        b = b_;
         t0 = a.tree_ptr[b];
         n = a.tree_ptr[b + 1] - t0;
         prefix = a.prefix_lens[b];
-        return t0 >= 0 && n >= 0 && n <= SGMV_TREE_MAX_NODES && (int64_t)t0 + n <= a.T && prefix >= 0 &&
-               (int64_t)prefix + n <= (int64_t)a.max_blocks * a.block_size;
-    }
-    __device__ __forceinline__ static uint32_t work(const MmaParams &P, int b) {
-        int t0, n, prefix;
-        if (!sequence(P, b, t0, n, prefix) || n == 0) return 0;
-        return (uint32_t)((prefix + n + P.tok - 1) / P.tok) * (uint32_t)((n * P.group + RT - 1) / RT) *
-               (uint32_t)P.a.Hkv;
-    }
-    __device__ __forceinline__ void enter(const MmaParams &P) {
-        sequence(P, b, t0, n, prefix);
+        items = 0;
+        tiles = 1;
+        if (!(t0 >= 0 && n >= 0 && n <= SGMV_TREE_MAX_NODES && (int64_t)t0 + n <= a.T && prefix >= 0 &&
+              (int64_t)prefix + n <= (int64_t)a.max_blocks * a.block_size))
+            return false;
+        if (n == 0) return true;
         total = prefix + n;
         tiles = (total + P.tok - 1) / P.tok;
         nrt = (n * P.group + RT - 1) / RT;
         items = (uint32_t)P.a.Hkv * (uint32_t)nrt;
-    }
-    __device__ __forceinline__ void start(const MmaParams &P, int b_, int64_t base_, int64_t w_,
-                                          int64_t w1_) {
-        b = b_;
-        base = base_;
-        w = w_;
-        w1 = w1_;
-        enter(P);
-    }
-    // the segment at w; false at the end of the share
-    __device__ __forceinline__ bool next(const MmaParams &P) {
-        if (w >= w1) return false;
-        while (w >= base + (int64_t)items * tiles) {
-            base += (int64_t)items * tiles;
-            do ++b;
-            while (b < P.a.B - 1 && work(P, b) == 0);
-            enter(P);
-        }
-        const uint32_t rel = (uint32_t)(w - base), item = rel / (uint32_t)tiles;
-        h = (int)(item / (uint32_t)nrt);
-        rt = (int)(item - (uint32_t)h * (uint32_t)nrt);
-        tile = (int)(rel - item * (uint32_t)tiles);
-        item_tiles = tiles;
-        item0 = base + (int64_t)item * tiles;
-        const int64_t left = w1 - w;
-        end = left < tiles - tile ? tile + (int)left : tiles;
-        w += end - tile;
         return true;
     }
+    __device__ __forceinline__ int64_t work() const { return (int64_t)items * tiles; }
 };
 
 // Bounded wait of a whole warp.  When one runs out (or another role's did),
@@ -269,6 +282,18 @@ template <typename T> __device__ __forceinline__ bool bad16(uint32_t h) {
     return (h & e) == e;
 }
 
+// Row r of an item's row tile: its token (~token for a padding row) and query head.
+__device__ __forceinline__ int2 row_place(const MmaParams &P, int t0, int h, int i) {
+    const int node = i / P.group;
+    int t = t0 + node;
+    const int hq = h * P.group + (i - node * P.group);
+    if (P.a.parents) {
+        const int p = P.a.parents[t];
+        if (p < -1 || p >= node) t = ~t;
+    }
+    return make_int2(t, hq);
+}
+
 template <typename T, int RT>
 __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
     sgmv_tree_mma_kernel(const __grid_constant__ MmaParams P) {
@@ -277,27 +302,37 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
     const sgmv_tree_attention_args &a = P.a;
     extern __shared__ __align__(1024) uint8_t dsm[];
     __shared__ __align__(8) uint64_t full[S::kStages], empty[S::kStages], q_full[S::kQ], q_empty[S::kQ];
-    __shared__ __align__(8) uint64_t p_full, drained;
+    __shared__ __align__(8) uint64_t seg_full[kSegs], seg_empty[kSegs], aux_full[kSegs];
+    __shared__ __align__(8) uint64_t p_full, tab_ready, drained;
     __shared__ uint32_t s_tmem;
-    __shared__ int s_lost, s_poison, s_last;
-    __shared__ int s_b;
-    __shared__ int64_t s_base, s_sum[32];
+    __shared__ int s_lost, s_poison, s_longest, s_known, s_loading;
+    __shared__ int64_t s_sum[32];
+    __shared__ Plan plan;
+    __shared__ Segment s_seg[kSegs], s_cur;        // s_cur: the softmax warps' segment
+    __shared__ int16_t s_parent[SGMV_TREE_MAX_NODES];
     __shared__ __align__(16) float s_ref[RT], s_fac[RT];
     __shared__ float s_red[4][RT];
     uint8_t *const sm = align1024(dsm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    constexpr int kWarps = S::kThreads / 32, kMmaWarp = S::kSoft / 32;
+    constexpr int kWarps = S::kThreads / 32, kMmaWarp = S::kSoft / 32, kWalkWarp = kMmaWarp + 1;
 
     if (warp == kMmaWarp) {
         if (lane == 0) {
             for (int i = 0; i < S::kStages; ++i)
                 mbar_init(&full[i], P.box ? kLoaders / 32 : kLoaders), mbar_init(&empty[i], 1);
-            for (int i = 0; i < S::kQ; ++i) mbar_init(&q_full[i], kLoaders), mbar_init(&q_empty[i], 1);
+            for (int i = 0; i < S::kQ; ++i) mbar_init(&q_full[i], 32), mbar_init(&q_empty[i], 1);
+            for (int i = 0; i < kSegs; ++i) {
+                mbar_init(&seg_full[i], 1);
+                mbar_init(&seg_empty[i], 2 + kLoaders / 32);  // MMA, softmax, loaders
+                mbar_init(&aux_full[i], 32);
+            }
             mbar_init(&p_full, S::kSoft);
+            mbar_init(&tab_ready, kLoaders);
             mbar_init(&drained, 1);
             mbar_init_fence();
-            s_lost = 0;
+            s_lost = s_longest = s_known = s_loading = 0;
             s_poison = -1;
+            for (int i = 0; i < kSegs; ++i) s_seg[i].tile = s_seg[i].end = 0;
         }
         __syncwarp();
         tmem_alloc(&s_tmem, S::kTmem);
@@ -315,224 +350,343 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
     pdl_wait();
     pdl_trigger();
 
-    // ---- this CTA's share of the line -------------------------------------
-    using Cur = Cursor<RT>;
-    int64_t sum = 0;
-    for (int b = tid; b < a.B; b += S::kThreads) {
-        int t0, n, prefix;
-        if (!Cur::sequence(P, b, t0, n, prefix) && blockIdx.x == 0) set_error(P.err, kErrBadSegments);
-        sum += Cur::work(P, b);
+    // ---- the line of work -----------------------------------------------------
+    const int stride = (a.B + kSeqTable - 1) / kSeqTable;
+    int64_t W = 0;
+    int longest = 0;
+    __syncthreads();
+    for (int b0 = 0; b0 < a.B; b0 += S::kThreads) {
+        const int b = b0 + tid;
+        int64_t own = 0;
+        if (b < a.B) {
+            Sequence q;
+            if (!q.template enter<RT>(P, b) && blockIdx.x == 0) set_error(P.err, kErrBadSegments);
+            own = q.work();
+            if (own) longest = max(longest, q.tiles);
+        }
+        int64_t run = own;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t up = __shfl_up_sync(0xffffffffu, run, o);
+            if (lane >= o) run += up;
+        }
+        if (b0) __syncthreads();  // the last round's sums have been read
+        if (lane == 31) s_sum[warp] = run;
+        __syncthreads();
+        int64_t all = 0;
+        for (int i = 0; i < kWarps; ++i) {
+            if (i < warp) run += s_sum[i];
+            all += s_sum[i];
+        }
+        if (b < a.B && b % stride == 0) plan.before[b / stride] = W + run - own;
+        W += all;
     }
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) s_sum[warp] = sum;
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 0) atomicMax(&s_longest, longest);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    int64_t W = 0;
-    for (int i = 0; i < kWarps; ++i) W += s_sum[i];
-    const int64_t share = (W + gridDim.x - 1) / gridDim.x;
-    const int64_t w0 = share * blockIdx.x, w1 = w0 + share < W ? w0 + share : W;
     const uint32_t tmem = s_tmem;
-    if (w0 >= w1) {
-        __syncthreads();
+    const int ctas = (int)gridDim.x;
+    const int64_t even = W / ctas, least = (s_longest + kMaxParts - 1) / kMaxParts;
+    const bool claims = even >= 4 * S::kLeast && even >= 8 && even >= 4 * least;
+    if (tid == 0) {
+        plan.W = W;
+        plan.stride = stride;
+        plan.ctas = ctas;
+        if (claims) {
+            plan.own = even - even / 4;
+            plan.split = plan.own * ctas;
+            const int64_t small = (W - plan.split + (int64_t)ctas * S::kClaims - 1) / ((int64_t)ctas * S::kClaims);
+            plan.small = max(max(small, (int64_t)S::kLeast), least);
+            plan.shares = ctas + (int)((W - plan.split + plan.small - 1) / plan.small);
+        } else {
+            plan.own = max((W + ctas - 1) / ctas, max(least, (int64_t)1));
+            plan.split = W;
+            plan.small = 1;
+            plan.shares = (int)((W + plan.own - 1) / plan.own);
+        }
+        if (blockIdx.x == 0) P.claim[1] = plan.shares;
+    }
+    __syncthreads();
+    if (plan.own * blockIdx.x >= W) {
         if (warp == kMmaWarp) tmem_dealloc(tmem, S::kTmem);
         return;
     }
-    {
-        int64_t base = 0;
-        for (int b0 = 0; b0 < a.B; b0 += S::kThreads) {  // the sequence that holds tile w0
-            const int b = b0 + tid;
-            const int64_t own = b < a.B ? Cur::work(P, b) : 0;
-            int64_t run = own;
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t up = __shfl_up_sync(0xffffffffu, run, o);
-                if (lane >= o) run += up;
-            }
-            __syncthreads();
-            if (lane == 31) s_sum[warp] = run;
-            __syncthreads();
-            int64_t before = base, all = 0;
-            for (int i = 0; i < kWarps; ++i) {
-                if (i < warp) before += s_sum[i];
-                all += s_sum[i];
-            }
-            if (before + run - own <= w0 && w0 < before + run) s_b = b, s_base = before + run - own;
-            base += all;
-            if (w0 < base) break;
-        }
-        __syncthreads();
-    }
-    Cur cur;
-    cur.start(P, s_b, s_base, w0, w1);
     volatile int *const lost = &s_lost;
     const int D = a.D, group = P.group;
+    const int cpr = D / 8;  // 16-byte chunks per row
+    // a role's next segment: number i
+    auto wait_segment = [&](int i) -> const Segment & {
+        await(&seg_full[i % kSegs], (uint32_t)(i / kSegs) & 1, lost);
+        return s_seg[i % kSegs];
+    };
 
-    if (warp > kMmaWarp) {
-        // ---- loaders: ring order K0, K1, V0, K2, V1, ..., V(last) -----------
-        const int lt = tid - S::kSoft - 32;
-        const int cpr = D / 8;                     // 16-byte chunks per row
-        const int dm = kLoaders / cpr, dc = kLoaders - dm * cpr;
-        constexpr int kBatch = 8, kOwn = (kTok + kLoaders - 1) / kLoaders;
-        int64_t *const tab = reinterpret_cast<int64_t *>(sm + S::kOffTab);
-        const int halves = D > 64 ? 2 : 1;
-        int pos = 0, g = 0, seg = 0;               // ring position, tile, segment
-        // the queries of segment seg's row tile, by `count` threads
-        auto load_q = [&](int i0, int count) {
-            const int qb = seg % S::kQ;
-            if (seg >= S::kQ) await(&q_empty[qb], (uint32_t)(seg / S::kQ - 1) & 1, lost);
-            uint8_t *const dst = sm + S::kOffQ + (uint32_t)qb * S::kQBytes;
-            const int R = cur.n * group;
-            for (int i = i0; i < RT * cpr; i += count) {
-                const int m = i / cpr, c = i - m * cpr, r = cur.rt * RT + m;
-                const int node = r / group, hq = cur.h * group + (r - node * group);
-                const bool in = r < R;
-                const T *src = static_cast<const T *>(a.q) +
-                               (in ? (int64_t)(cur.t0 + node) * a.q_token + (int64_t)hq * a.q_head + c * 8 : 0);
-                cp_async16(dst + (uint32_t)(c >> 3) * (RT * 128u) + sw128_offset(m, c & 7), src, in ? 16u : 0u);
+    if (warp == kWalkWarp) {
+        // ---- the walk along the line ---------------------------------------------
+        int64_t base = 0, w = 0, w1 = 0;  // first tile of the sequence; next tile; end of the share
+        int id = (int)blockIdx.x, see = 0, see_b = -1, see_rt = -1, see_user[2] = {-1, -1};
+        Sequence q;
+        q.items = 0;
+        q.tiles = 1;
+        plan.range(id, w, w1);
+        bool seek = true;
+        for (int i = 0;; ++i) {
+            if (i >= kSegs) await(&seg_empty[i % kSegs], (uint32_t)(i / kSegs - 1) & 1, lost);
+            if (w >= w1) {
+                id = -1;
+                if (claims) {
+                    // not before the last known segment is being loaded
+                    const uint64_t t0 = global_ns();
+                    while (*(volatile int *)&s_loading < i && !*lost)
+                        if (global_ns() - t0 > kWaitLimitNs) *lost = 1;
+                    __syncwarp();
+                    if (lane == 0) {
+                        id = ctas + atomicAdd(&P.claim[0], 1);
+                        if (id >= plan.shares) id = -1;
+                    }
+                    id = __shfl_sync(0xffffffffu, id, 0);
+                }
+                if (id < 0) {
+                    if (lane == 0) {
+                        s_seg[i % kSegs].tile = s_seg[i % kSegs].end = 0;
+                        mbar_arrive(&seg_full[i % kSegs]);
+                    }
+                    break;
+                }
+                plan.range(id, w, w1);
+                seek = w >= base + q.work();
+            }
+            if (seek) {  // the table's last entry at or before w
+                int lo = 0, hi = (a.B - 1) / plan.stride;
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) >> 1;
+                    if (plan.before[mid] <= w) lo = mid;
+                    else hi = mid - 1;
+                }
+                base = plan.before[lo];
+                q.template enter<RT>(P, lo * plan.stride);
+                seek = false;
+            }
+            while (w >= base + q.work()) {
+                base += q.work();
+                q.template enter<RT>(P, q.b + 1);
+            }
+            const uint32_t rel = (uint32_t)(w - base), item = rel / (uint32_t)q.tiles;
+            const int h = (int)(item / (uint32_t)q.nrt), rt = (int)(item - (uint32_t)h * (uint32_t)q.nrt);
+            const int tile = (int)(rel - item * (uint32_t)q.tiles);
+            const int end = w1 - w < q.tiles - tile ? tile + (int)(w1 - w) : q.tiles;
+            const bool tree = end * P.tok > q.prefix, build = tree && (see_b != q.b || see_rt != rt);
+            if (build) see ^= 1;
+            if (lane == 0) {
+                Segment &s = s_seg[i % kSegs];
+                s.b = q.b;
+                s.t0 = q.t0;
+                s.n = q.n;
+                s.prefix = q.prefix;
+                s.total = q.total;
+                s.h = h;
+                s.rt = rt;
+                s.tile = tile;
+                s.end = end;
+                s.whole = tile == 0 && end == q.tiles;
+                s.slot = 2 * id + (tile == 0 ? 1 : 0);
+                s.see = see;
+                if (w + (end - tile) == w1) {  // the share's last: the only item that it may begin and not end
+                    Cut cut = {};
+                    if (tile == 0 && !s.whole) {
+                        cut.t0 = q.t0;
+                        cut.n = q.n;
+                        cut.h = h;
+                        cut.rt = rt;
+                        cut.first = id;
+                        cut.parts = plan.of(w + q.tiles - 1) - id + 1;
+                    }
+                    P.cut[id] = cut;
+                }
+                *(volatile int *)&s_known = i + 1;
+                mbar_arrive(&seg_full[i % kSegs]);
+            }
+            __syncwarp();
+            w += end - tile;
+            // the row tile's queries
+            const int qb = i % S::kQ, R = min(RT, q.n * group - rt * RT);
+            if (i >= S::kQ) await(&q_empty[qb], (uint32_t)(i / S::kQ - 1) & 1, lost);
+            uint8_t *const qs = sm + S::kOffQ + (uint32_t)qb * S::kQBytes;
+            for (int e = lane; e < RT * cpr; e += 32) {
+                const int m = e / cpr, c = e - m * cpr, r = rt * RT + m, node = r / group;
+                const T *src = static_cast<const T *>(a.q);
+                if (m < R)
+                    src += (int64_t)(q.t0 + node) * a.q_token + (int64_t)(h * group + r - node * group) * a.q_head + c * 8;
+                cp_async16(qs + (uint32_t)(c >> 3) * (RT * 128u) + sw128_offset(m, c & 7), src, m < R ? 16u : 0u);
             }
             cp_async_arrive(&q_full[qb]);
-            ++seg;
+            // the rows' places
+            int2 *const place = reinterpret_cast<int2 *>(sm + S::kOffRow) + (i % kSegs) * RT;
+            for (int r = lane; r < R; r += 32) place[r] = row_place(P, q.t0, h, rt * RT + r);
+            if (build) {
+                // see[j]: the rows that see tree node j.  Every node of this row
+                // tile marks itself and its ancestors with its rows' bits.
+                see_b = q.b;
+                see_rt = rt;
+                // the table's last user is done (those kSegs back were waited for)
+                const int u = see_user[see];
+                if (u >= 0 && i - u < kSegs) await(&seg_empty[u % kSegs], (uint32_t)(u / kSegs) & 1, lost);
+                uint32_t *const tab = reinterpret_cast<uint32_t *>(sm + S::kOffSee) +
+                                      see * SGMV_TREE_MAX_NODES * S::kWords;
+                for (int e = lane; e < q.n * S::kWords; e += 32) tab[e] = 0;
+                for (int j = lane; j < q.n; j += 32) {
+                    const int p = a.parents ? a.parents[q.t0 + j] : j - 1;
+                    if (p < -2 || p >= j) set_error(P.err, kErrBadIndex);
+                    s_parent[j] = (int16_t)(p < -1 || p >= j ? -2 : p);  // -2: padding
+                }
+                __syncwarp();
+                const int node0 = rt * RT / group, node1 = (rt * RT + R - 1) / group;
+                for (int node = node0 + lane; node <= node1; node += 32) {
+                    const int lo = max(0, node * group - rt * RT), hi = min(R, (node + 1) * group - rt * RT);
+                    for (int j = node; j >= 0 && s_parent[j] != -2; j = s_parent[j])
+                        for (int k = lo >> 5; k <= (hi - 1) >> 5; ++k) {
+                            const int l0 = max(lo - 32 * k, 0), l1 = min(hi - 32 * k, 32);
+                            atomicOr(&tab[j * S::kWords + k], (0xffffffffu >> (32 - (l1 - l0))) << l0);
+                        }
+                }
+                __syncwarp();
+            }
+            if (tree) see_user[see] = i;
+            mbar_arrive(&aux_full[i % kSegs]);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp > kWalkWarp) {
+        // ---- K and V: ring order K0, V0, K1, V1, ... ------------------------------
+        const int lt = tid - S::kSoft - 64, halves = D > 64 ? 2 : 1;
+        int pos = 0, st = 0;
+        uint32_t ph = 1;  // parity of the stage's release that is waited for
+        auto claim_stage = [&]() {
+            if (pos >= S::kStages) await(&empty[st], ph, lost);
+            ++pos;
+        };
+        auto advance = [&]() {
+            if (++st == S::kStages) st = 0, ph ^= 1;
         };
         if (P.box) {
-            // TMA: a box (tokens x 64 columns) per lane, dealt to the three warps
+            // TMA: a box (tokens x 64 columns) per lane, dealt to the two warps
             const int box = P.box, nbox = P.tok / box, op = lane * (kLoaders / 32) + lt / 32;
             const int mine = op % nbox, half = op / nbox;
             const bool busy = half < halves;
             const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, busy)) * (uint32_t)box * 128u;
             const uint32_t at = (uint32_t)half * kHalf + (uint32_t)(mine * box) * 128u;
-            Cur peek = cur;   // the tile whose page is looked up next
-            int peek_tile = 0, peek_end = 0;
-            int32_t next_page = 0;
-            int next_in = 0;
-            auto look = [&]() {
-                if (peek_tile == peek_end) {
-                    if (!peek.next(P)) return;
-                    peek_tile = peek.tile;
-                    peek_end = peek.end;
-                }
-                const int j = peek_tile * P.tok + mine * box;
-                next_in = -1;
-                if (j < peek.total) {
+            int32_t page = 0;
+            int in = -1;
+            // page and place of this lane's box of a tile
+            auto look = [&](const Segment &s, int tile) {
+                const int j = tile * P.tok + mine * box;
+                in = -1;
+                if (j < s.total) {
                     const int pg = j / a.block_size;
-                    next_in = j - pg * a.block_size;
-                    next_page = a.block_table[peek.b * a.table_row + pg];
+                    in = j - pg * a.block_size;
+                    page = a.block_table[s.b * a.table_row + pg];
                 }
-                ++peek_tile;
             };
-            auto copy_boxes = [&](const CUtensorMap *map, int32_t page, int in, int head) {
-                const int st = pos % S::kStages;
-                if (pos >= S::kStages) await(&empty[st], (uint32_t)(pos / S::kStages - 1) & 1, lost);
+            auto copy_boxes = [&](const CUtensorMap *map, int32_t pg, int row, int head) {
+                claim_stage();
                 if (lane == 0) mbar_arrive_expect_tx(&full[st], bytes);
                 __syncwarp();
-                if (busy) tma_load_4d(sm + (uint32_t)st * kStage + at, map, half * 64, in, head, page, &full[st]);
-                ++pos;
+                if (busy) tma_load_4d(sm + (uint32_t)st * kStage + at, map, half * 64, row, head, pg, &full[st]);
+                advance();
             };
-            int32_t page = 0, old_page = 0;
-            int in = 0, old_in = 0, old_h = 0;
-            look();
-            while (cur.next(P)) {
-                load_q(lt, kLoaders);
-                for (int tile = cur.tile; tile < cur.end; ++tile, ++g) {
+            bool looked = false;
+            for (int i = 0;; ++i) {
+                const Segment s = wait_segment(i);
+                if (s.end == 0) break;
+                if (lt == 0) *(volatile int *)&s_loading = i + 1;
+                if (!looked) look(s, s.tile);
+                for (int tile = s.tile; tile < s.end; ++tile) {
                     // boxes past the end, and pages out of range, read as zeros
-                    page = next_page;
-                    in = next_in;
-                    if (in < 0 || page < 0 || page >= a.num_blocks) {
-                        if (in >= 0) set_error(P.err, kErrBadIndex);
-                        page = a.num_blocks;
-                        in = 0;
+                    int32_t pg = page;
+                    int row = in;
+                    if (row < 0 || pg < 0 || pg >= a.num_blocks) {
+                        if (row >= 0) set_error(P.err, kErrBadIndex);
+                        pg = a.num_blocks;
+                        row = 0;
                     }
-                    look();
-                    copy_boxes(&P.map_k, page, in, cur.h);
-                    if (g > 0) copy_boxes(&P.map_v, old_page, old_in, old_h);
-                    old_page = page;
-                    old_in = in;
-                    old_h = cur.h;
+                    // the next tile's page is looked up meanwhile
+                    looked = false;
+                    if (tile + 1 < s.end) {
+                        look(s, tile + 1);
+                    } else if (__shfl_sync(0xffffffffu, *(volatile int *)&s_known, 0) > i + 1) {
+                        const Segment &next = wait_segment(i + 1);
+                        look(next, next.tile);
+                        looked = true;
+                    }
+                    copy_boxes(&P.map_k, pg, row, s.h);
+                    copy_boxes(&P.map_v, pg, row, s.h);
                 }
+                if (lane == 0) mbar_arrive(&seg_empty[i % kSegs]);
+                __syncwarp();
             }
-            copy_boxes(&P.map_v, old_page, old_in, old_h);
-            asm volatile("cp.async.wait_all;" ::: "memory");
         } else {
-        int64_t head_off = 0, prev_head = 0;
-        auto copy_tile = [&](const void *cache, int64_t off, int tile) {
-            const int st = pos % S::kStages;
-            if (pos >= S::kStages) await(&empty[st], (uint32_t)(pos / S::kStages - 1) & 1, lost);
-            const T *const base = static_cast<const T *>(cache) + off;
-            const int64_t *const rows = tab + (tile & 3) * kTok;
-            uint8_t *const dst = sm + (uint32_t)st * kStage;
-            // eight copies' row offsets are read before the first is used
-            int m = lt / cpr, c = lt - m * cpr;
-            while (m < kTok) {
-                int64_t o[kBatch];
-                uint32_t to[kBatch];
-                int cc[kBatch];
+            int64_t *const tab = reinterpret_cast<int64_t *>(sm + S::kOffTab);
+            const int dm = kLoaders / cpr, dc = kLoaders - dm * cpr;
+            constexpr int kBatch = 8;
+            int g = 0;
+            auto copy_tile = [&](const void *cache, int64_t off) {
+                claim_stage();
+                const T *const from = static_cast<const T *>(cache) + off;
+                const int64_t *const rows = tab + (g & 1) * kTok;
+                uint8_t *const dst = sm + (uint32_t)st * kStage;
+                // eight copies' row offsets are read before the first is used
+                int m = lt / cpr, c = lt - m * cpr;
+                while (m < kTok) {
+                    int64_t o[kBatch];
+                    uint32_t to[kBatch];
+                    int cc[kBatch];
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    o[i] = -2;
-                    if (m < kTok) {
-                        o[i] = rows[m];
-                        to[i] = (uint32_t)(c >> 3) * kHalf + sw128_offset(m, c & 7);
-                        cc[i] = c * 8;
+                    for (int i = 0; i < kBatch; ++i) {
+                        o[i] = -2;
+                        if (m < kTok) {
+                            o[i] = rows[m];
+                            to[i] = (uint32_t)(c >> 3) * kHalf + sw128_offset(m, c & 7);
+                            cc[i] = c * 8;
+                        }
+                        m += dm;
+                        c += dc;
+                        if (c >= cpr) c -= cpr, ++m;
                     }
-                    m += dm;
-                    c += dc;
-                    if (c >= cpr) c -= cpr, ++m;
-                }
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i)
-                    if (o[i] != -2)
-                        cp_async16(dst + to[i], o[i] >= 0 ? base + o[i] + cc[i] : base, o[i] >= 0 ? 16u : 0u);
-            }
-            cp_async_arrive(&full[st]);
-            ++pos;
-        };
-        // the tile after the current one: its pages are looked up while the
-        // current one's copies are issued
-        Cur peek = cur;
-        int peek_tile = 0, peek_end = 0;
-        int32_t block[kOwn];
-        int in_page[kOwn];
-        auto look = [&]() {
-            if (peek_tile == peek_end) {
-                if (!peek.next(P)) return;
-                peek_tile = peek.tile;
-                peek_end = peek.end;
-            }
-#pragma unroll
-            for (int e = 0; e < kOwn; ++e) {
-                const int m = lt + e * kLoaders, j = peek_tile * kTok + m;
-                in_page[e] = -1;
-                if (m < kTok && j < peek.total) {
-                    const int pg = j / a.block_size;
-                    in_page[e] = j - pg * a.block_size;
-                    block[e] = a.block_table[peek.b * a.table_row + pg];
+                    for (int i = 0; i < kBatch; ++i)
+                        if (o[i] != -2)
+                            cp_async16(dst + to[i], o[i] >= 0 ? from + o[i] + cc[i] : from, o[i] >= 0 ? 16u : 0u);
                 }
-            }
-            ++peek_tile;
-        };
-        look();
-        while (cur.next(P)) {
-            prev_head = head_off;
-            head_off = (int64_t)cur.h * a.cache_head;
-            load_q(lt, kLoaders);
-            for (int tile = cur.tile; tile < cur.end; ++tile, ++g) {
-                // where the tile's tokens are (elements from the cache's start)
-#pragma unroll
-                for (int e = 0; e < kOwn; ++e) {
-                    const int m = lt + e * kLoaders;
-                    const bool in = in_page[e] >= 0, good = in && block[e] >= 0 && block[e] < a.num_blocks;
-                    if (in && !good) set_error(P.err, kErrBadIndex);
-                    if (m < kTok)
-                        tab[(g & 3) * kTok + m] =
-                            good ? (int64_t)block[e] * a.cache_block + (int64_t)in_page[e] * a.cache_token : -1;
+                cp_async_arrive(&full[st]);
+                advance();
+            };
+            for (int i = 0;; ++i) {
+                const Segment s = wait_segment(i);
+                if (s.end == 0) break;
+                if (lt == 0) *(volatile int *)&s_loading = i + 1;
+                for (int tile = s.tile; tile < s.end; ++tile, ++g) {
+                    // where the tile's tokens are (elements from the cache's start)
+                    for (int m = lt; m < kTok; m += kLoaders) {
+                        int64_t off = -1;
+                        const int j = tile * kTok + m;
+                        if (j < s.total) {
+                            const int pg = j / a.block_size;
+                            const int32_t block = a.block_table[s.b * a.table_row + pg];
+                            if (block >= 0 && block < a.num_blocks)
+                                off = (int64_t)block * a.cache_block + (int64_t)(j - pg * a.block_size) * a.cache_token;
+                            else
+                                set_error(P.err, kErrBadIndex);
+                        }
+                        tab[(g & 1) * kTok + m] = off;
+                    }
+                    mbar_arrive(&tab_ready);  // (an mbarrier: its wait is bounded)
+                    await(&tab_ready, (uint32_t)g & 1, lost);
+                    copy_tile(a.k_cache, (int64_t)s.h * a.cache_head);
+                    copy_tile(a.v_cache, (int64_t)s.h * a.cache_head);
                 }
-                named_sync<1, kLoaders>();
-                look();
-                copy_tile(a.k_cache, head_off, g);
-                if (g > 0) copy_tile(a.v_cache, tile == cur.tile ? prev_head : head_off, g - 1);
+                if (lane == 0) mbar_arrive(&seg_empty[i % kSegs]);
+                __syncwarp();
             }
-        }
-        copy_tile(a.v_cache, head_off, g - 1);
-        asm volatile("cp.async.wait_all;" ::: "memory");
+            asm volatile("cp.async.wait_all;" ::: "memory");
         }
     } else if (warp == kMmaWarp) {
         // ---- MMA issuer ------------------------------------------------------
@@ -543,33 +697,37 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
         const uint64_t k_desc = sw128_desc(ring, 16, 1024), v_desc = sw128_desc(ring, kHalf, 1024);
         const uint64_t q_desc = sw128_desc(ring + S::kOffQ, 16, 1024);
         const uint64_t p_desc = sw128_desc(ring + S::kOffP, kHalf, 1024);
-        const int N = (int)(w1 - w0);
         const bool wide = D > 64;
-        int st = 0, seg = -1;        // ring stage of the next operand
-        uint32_t ph = 0;             // and its phase
-        auto advance = [&]() {
-            if (++st == S::kStages) st = 0, ph ^= 1;
+        int k_st = 0, v_st = 1 % S::kStages;  // ring stages of the next K and V
+        uint32_t k_ph = 0, v_ph = 0;
+        auto skip = [&](int &st, uint32_t &ph) {  // two operands on
+            st += 2;
+            if (st >= S::kStages) st -= S::kStages, ph ^= 1;
         };
-        Cur ahead = cur;             // segment of the next score product
-        int left = 0;                // its tiles not yet issued
+        int ahead = -1, left = 0;             // segment of the next score product, its tiles not yet issued
+        bool none = false;                    // no more of them
         // Score product of tile g.  Its accumulator was last read for tile
         // g - 2, before that tile's P was complete.
         auto scores = [&](int g) {
+            if (none) return;
             bool first = false;
             if (left == 0) {
-                ahead.next(P);
-                left = ahead.end - ahead.tile;
-                ++seg;
+                const Segment &s = wait_segment(++ahead);
+                left = s.end - s.tile;
+                if (s.end == 0) {
+                    none = true;
+                    return;
+                }
                 first = true;
             }
-            const int qb = seg % S::kQ;
-            if (first) await(&q_full[qb], (uint32_t)(seg / S::kQ) & 1, lost);
-            await(&full[st], ph, lost);
+            const int qb = ahead % S::kQ;
+            if (first) await(&q_full[qb], (uint32_t)(ahead / S::kQ) & 1, lost);
+            await(&full[k_st], k_ph, lost);
             --left;
             // cp.async (generic proxy) data -> tensor core (async proxy)
             if (first || !P.box) fence_proxy_async();
             tc_fence_after();
-            const uint64_t kd = k_desc + (uint32_t)st * (kStage >> 4);
+            const uint64_t kd = k_desc + (uint32_t)k_st * (kStage >> 4);
             const uint64_t qd = q_desc + (uint32_t)qb * (S::kQBytes >> 4);
             const uint32_t d = tmem + (uint32_t)((g & 1) * RT);
 #pragma unroll
@@ -579,141 +737,82 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
                 for (int kk = 0; kk < 4; ++kk)
                     mma_on(on, d, kd + (kHalf >> 4) + kk * 2, qd + RT * 8u + kk * 2, idesc_s, 1);
             }
-            commit_on(on, &empty[st]);  // also tells the softmax that the scores are there
+            commit_on(on, &empty[k_st]);  // also tells the softmax that the scores are there
             if (left == 0) commit_on(on, &q_empty[qb]);
-            advance();
+            skip(k_st, k_ph);
         };
         scores(0);
-        cur.next(P);
-        int tile = cur.tile;
-        for (int g = 0; g < N; ++g) {
-            if (g + 1 < N) scores(g + 1);
-            await(&full[st], ph, lost);
-            await(&p_full, (uint32_t)g & 1, lost);
-            if (tile == cur.end) {
-                cur.next(P);
-                tile = cur.tile;
-            }
-            if (!P.box) fence_proxy_async();
-            tc_fence_after();
-            const uint64_t vd = v_desc + (uint32_t)st * (kStage >> 4);
-            const uint32_t more = tile != cur.tile;
+        int g = 0;
+        for (int i = 0;; ++i) {
+            const Segment &s = wait_segment(i);
+            const int tiles = s.end - s.tile;
+            if (s.end == 0) break;
+            for (int t = 0; t < tiles; ++t, ++g) {
+                scores(g + 1);  // nothing at the end
+                await(&full[v_st], v_ph, lost);
+                await(&p_full, (uint32_t)g & 1, lost);
+                if (!P.box) fence_proxy_async();
+                tc_fence_after();
+                const uint64_t vd = v_desc + (uint32_t)v_st * (kStage >> 4);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-                mma_on(on, tmem + 2 * RT, vd + kk * 128, p_desc + kk * 128, idesc_o, kk ? 1u : more);
-            commit_on(on, &empty[st]);  // also tells the softmax that P has been read
-            advance();
-            ++tile;
+                for (int kk = 0; kk < 8; ++kk)
+                    mma_on(on, tmem + 2 * RT, vd + kk * 128, p_desc + kk * 128, idesc_o, kk ? 1u : (uint32_t)t);
+                commit_on(on, &empty[v_st]);  // also tells the softmax that P has been read
+                skip(v_st, v_ph);
+            }
+            if (lane == 0) mbar_arrive(&seg_empty[i % kSegs]);
+            __syncwarp();
         }
         // nothing of this kernel's is in flight when tensor memory is returned
         commit_on(on, &drained);
         await(&drained, 0, lost);
     } else {
         // ---- softmax and output: thread = token, then = head column ------------
-        const int wg = warp >> 2, tok = tid & 127, r0 = wg * S::kRows;
+        const int wg = warp >> 2, tok = tid & 127, r0 = wg * S::kRows, d = tok;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t t_s = tmem + lanes + (uint32_t)r0, t_o = tmem + lanes + 2 * RT + (uint32_t)r0;
-        uint32_t *const see = reinterpret_cast<uint32_t *>(sm + S::kOffSee);
-        int64_t *const row_out = reinterpret_cast<int64_t *>(sm + S::kOffRow);
         uint8_t *const prow = sm + S::kOffP + (uint32_t)(wg >> 1) * kHalf;
         const int pchunk = (wg & 1) * 4;
         const float c = P.c;
         float l[S::kRows];
-        int see_b = -1, see_rt = -1;
-        const int N = (int)(w1 - w0);
-        int g = 0;  // tile
-        // K of tile g is the ring's operand 2g - 1 (0 for the first), V is 2g + 2
-        // (2g + 1 for the last).  The commit that frees an operand's stage is
-        // the softmax's signal that the product is done; it waits for each
-        // before the stage can be freed again.
-        auto v_pos = [&](int g) { return g + 1 < N ? 2 * g + 2 : 2 * g + 1; };
+        volatile Segment &cur = s_cur;
+        int g = 0;              // tile
+        // K of tile g is the ring's operand 2g, V is 2g + 1.  The commit that
+        // frees an operand's stage is the softmax's signal that the product is
+        // done; it waits for each before the stage can be freed again.
         auto done = [&](int pos) {
             await(&empty[pos % S::kStages], (uint32_t)(pos / S::kStages) & 1, lost);
             tc_fence_after();
         };
-        for (int seg = 0; cur.next(P); ++seg) {
-            const int R = min(RT, cur.n * group - cur.rt * RT);  // rows in use
-            if (cur.end * P.tok > cur.prefix && (see_b != cur.b || see_rt != cur.rt)) {
-                // see[j]: the rows that see tree node j.  Ancestors by pointer
-                // doubling in the (idle) P buffer; invalid parents count as padding.
-                see_b = cur.b;
-                see_rt = cur.rt;
-                const int n = cur.n;
-                uint32_t *const anc = reinterpret_cast<uint32_t *>(sm + S::kOffP);  // [n][8]
-                int *const up = reinterpret_cast<int *>(anc + SGMV_TREE_MAX_NODES * 8);
-                auto parent = [&](int i) {
-                    const int p = a.parents ? a.parents[cur.t0 + i] : i - 1;
-                    if (p < -2 || p >= i) set_error(P.err, kErrBadIndex);
-                    return p < -1 || p >= i ? -2 : p;
-                };
-                named_sync<6, S::kSoft>();
-                for (int i = tid; i < n; i += S::kSoft) up[i] = parent(i);
-                named_sync<6, S::kSoft>();
-                constexpr int kPer = (SGMV_TREE_MAX_NODES + S::kSoft - 1) / S::kSoft;
-                uint32_t word[kPer][8];
-                int to[kPer];
-#pragma unroll
-                for (int e = 0; e < kPer; ++e) {
-                    const int i = tid + e * S::kSoft;
-                    to[e] = -1;
-                    if (i >= n) continue;
-                    const int p = up[i];
-                    to[e] = p >= 0 && up[p] != -2 ? p : -1;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) anc[i * 8 + k] = p != -2 && (i >> 5) == k ? 1u << (i & 31) : 0u;
-                }
-                named_sync<6, S::kSoft>();
-#pragma unroll
-                for (int e = 0; e < kPer; ++e)
-                    if (tid + e * S::kSoft < n) up[tid + e * S::kSoft] = to[e];
-                named_sync<6, S::kSoft>();
-                for (int reach = 1; reach < n; reach <<= 1) {
-#pragma unroll
-                    for (int e = 0; e < kPer; ++e) {
-                        const int i = tid + e * S::kSoft;
-                        if (i >= n) continue;
-                        const int p = up[i];
-                        to[e] = p >= 0 ? up[p] : -1;
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            word[e][k] = anc[i * 8 + k] | (p >= 0 ? anc[p * 8 + k] : 0u);
-                    }
-                    named_sync<6, S::kSoft>();
-#pragma unroll
-                    for (int e = 0; e < kPer; ++e) {
-                        const int i = tid + e * S::kSoft;
-                        if (i >= n) continue;
-                        up[i] = to[e];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) anc[i * 8 + k] = word[e][k];
-                    }
-                    named_sync<6, S::kSoft>();
-                }
-                for (int i = tid; i < n * S::kWords; i += S::kSoft) {
-                    const int j = i / S::kWords, k = i - j * S::kWords;
-                    uint32_t bits = 0;
-                    for (int e = 0; e < (RT < 32 ? RT : 32); ++e) {
-                        const int m = k * 32 + e;
-                        if (m < R) {
-                            const int node = (cur.rt * RT + m) / group;
-                            bits |= (anc[node * 8 + (j >> 5)] >> (j & 31) & 1u) << e;
-                        }
-                    }
-                    see[i] = bits;
-                }
-                named_sync<6, S::kSoft>();
+        for (int seg = 0;; ++seg) {
+            named_sync<6, S::kSoft>();  // every thread is done with the last segment
+            if (warp == 0) {
+                if (lane == 0 && seg > 0) mbar_arrive(&seg_empty[(seg - 1) % kSegs]);
+                const Segment &s = wait_segment(seg);
+                if (lane == 0) s_cur = s;
             }
+            named_sync<6, S::kSoft>();
+            const int prefix = cur.prefix, end = cur.end, first = cur.tile;
+            if (end == 0) break;
+            const int R = min(RT, cur.n * group - cur.rt * RT);  // rows in use
+            const uint32_t *const see = reinterpret_cast<const uint32_t *>(sm + S::kOffSee) +
+                                        cur.see * SGMV_TREE_MAX_NODES * S::kWords + wg;
+            bool aux = false;  // the walk's tables for this segment are known to be there
 #pragma unroll
             for (int r = 0; r < S::kRows; ++r) l[r] = 0.f;
-            for (int tile = cur.tile; tile < cur.end; ++tile, ++g) {
-                done(g > 0 ? 2 * g - 1 : 0);
+            for (int tile = first; tile < end; ++tile, ++g) {
+                done(2 * g);
+                if (!aux && (tile + 1) * P.tok > prefix) {
+                    await(&aux_full[seg % kSegs], (uint32_t)(seg / kSegs) & 1, lost);
+                    aux = true;
+                }
                 const uint32_t ts = t_s + (uint32_t)((g & 1) * RT);
                 // which rows see this token: all, none, or a node's
                 const int j = tile * P.tok + tok;
-                const bool tree = (tile + 1) * P.tok > cur.prefix, edge = tree || P.tok < kTok;
+                const bool tree = (tile + 1) * P.tok > prefix, edge = tree || P.tok < kTok;
                 uint32_t vis = 0xffffffffu;
-                if (edge && (tok >= P.tok || j >= cur.prefix))
-                    vis = tok < P.tok && j < cur.total ? see[(j - cur.prefix) * S::kWords + wg] : 0u;
+                if (edge && (tok >= P.tok || j >= prefix))
+                    vis = tok < P.tok && j < cur.total ? see[(j - prefix) * S::kWords] : 0u;
                 float s[S::kRows];
                 // the masked exponents
                 auto exponents = [&]() {
@@ -764,8 +863,8 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
                     group_bar(wg);
 #pragma unroll
                     for (int r = 0; r < S::kRows; ++r) l[r] *= s_fac[r0 + r];
-                    if (tile != cur.tile) {
-                        done(v_pos(g - 1));
+                    if (tile != first) {
+                        done(2 * g - 1);
                         tmem_load(t_o, s);
 #pragma unroll
                         for (int i = 0; i < S::kRows; ++i) s[i] *= s_fac[r0 + i];
@@ -781,7 +880,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
                     p[i] = from_f<T>(e);
                 }
                 // the previous tile's P has been read
-                if (g > 0) done(v_pos(g - 1));
+                if (g > 0) done(2 * g - 1);
 #pragma unroll
                 for (int q = 0; q < S::kRows / 8; ++q)
                     sts128(prow + sw128_offset(tok, pchunk + q), reinterpret_cast<const uint4 *>(p)[q]);
@@ -791,7 +890,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
                     const int v0 = max(0, cur.prefix - tile * P.tok), v1 = min(P.tok, cur.total - tile * P.tok);
                     const int ve = P.box ? (v1 + P.box - 1) / P.box * P.box : v1;
                     const int cpr = D / 8;
-                    const int pv = v_pos(g);
+                    const int pv = 2 * g + 1;
                     await(&full[pv % S::kStages], (uint32_t)(pv / S::kStages) & 1, lost);
                     uint8_t *const vt = sm + (uint32_t)(pv % S::kStages) * kStage;
                     for (int i = tid; i < (ve - v0) * cpr; i += S::kSoft) {
@@ -819,9 +918,9 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
                 tc_fence_before();
                 mbar_arrive(&p_full);
             }
-            done(v_pos(g - 1));
+            if (!aux) await(&aux_full[seg % kSegs], (uint32_t)(seg / kSegs) & 1, lost);
 
-            // ---- the segment's sums and rows' places -----------------------------
+            // ---- the segment's sums, then its rows -------------------------------
             {
                 float v[S::kRows];
 #pragma unroll
@@ -830,50 +929,40 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
                 if (S::kRows == 32 || (lane & 1) == 0) s_red[warp & 3][r0 + r] = v[0];
             }
             group_bar(wg);
-            const bool whole = cur.tile == 0 && cur.end == cur.item_tiles;
-            const int slot = 2 * (int)blockIdx.x + (cur.tile == 0 ? 1 : 0);
+            const bool whole = cur.whole != 0;
+            const int slot = cur.slot;
+            const int2 *const place = reinterpret_cast<const int2 *>(sm + S::kOffRow) + (seg % kSegs) * RT;
             if (tok < S::kRows) {
                 const int r = r0 + tok;
                 const float L = s_red[0][r] + s_red[1][r] + s_red[2][r] + s_red[3][r], ref = s_ref[r];
-                int64_t to = -1;
-                if (r < R) {
-                    const int i = cur.rt * RT + r, node = i / group, hq = cur.h * group + (i - node * group);
-                    const int64_t t = cur.t0 + node;
-                    to = t * a.out_token + (int64_t)hq * a.out_head;
-                    bool pad = false;
-                    if (a.parents) {
-                        const int p = a.parents[t];
-                        pad = p < -1 || p >= node;
-                    }
-                    s_fac[r] = pad || L == 0.f ? 0.f : 1.f / L;
-                    if (pad) to = ~to - 1;  // below -1: written as zeros
-                    if (whole && a.lse)
-                        a.lse[t * a.Hq + hq] = pad || L == 0.f ? -INFINITY : (ref + log2f(L)) * 0.693147180559945309f;
-                }
-                row_out[r] = to;
                 if (!whole) {
-                    float *const ml = P.ml + ((int64_t)slot * RT + r) * 2;
-                    ml[0] = ref;
-                    ml[1] = L;
+                    *reinterpret_cast<float2 *>(P.ml + ((int64_t)slot * RT + r) * 2) = make_float2(ref, L);
+                } else if (r < R) {
+                    const int2 to = place[r];
+                    const bool none = to.x < 0 || L == 0.f;
+                    s_fac[r] = none ? 0.f : 1.f / L;
+                    if (a.lse)
+                        a.lse[(int64_t)(to.x < 0 ? ~to.x : to.x) * a.Hq + to.y] =
+                            none ? -INFINITY : (ref + log2f(L)) * 0.693147180559945309f;
                 }
                 s_ref[r] = kUnset;
             }
+            done(2 * g - 1);
             group_bar(wg);
-            const bool poison = *(volatile int *)&s_poison == seg, ok = !*lost;
-            const int d = tok;
             {
+                const bool poison = *(volatile int *)&s_poison == seg, ok = !*lost;
                 float v[S::kRows];
                 tmem_load(t_o, v);
                 if (poison && d < D) {
-                    for (int jn = max(0, cur.tile * P.tok - cur.prefix); jn < min(cur.n, cur.end * P.tok - cur.prefix); ++jn) {
-                        const int j = cur.prefix + jn, pg = j / a.block_size;
+                    for (int jn = max(0, first * P.tok - prefix); jn < min(cur.n, end * P.tok - prefix); ++jn) {
+                        const int j = prefix + jn, pg = j / a.block_size;
                         const int32_t block = a.block_table[cur.b * a.table_row + pg];
                         if (block < 0 || block >= a.num_blocks) continue;
                         const T x = static_cast<const T *>(a.v_cache)[(int64_t)block * a.cache_block +
                                                                      (int64_t)(j - pg * a.block_size) * a.cache_token +
                                                                      (int64_t)cur.h * a.cache_head + d];
                         if (!bad16<T>(*reinterpret_cast<const unsigned short *>(&x))) continue;
-                        const uint32_t bits = see[jn * S::kWords + wg];
+                        const uint32_t bits = see[jn * S::kWords];
 #pragma unroll
                         for (int i = 0; i < S::kRows; ++i)
                             if (bits >> i & 1u) v[i] += to_f<T>(x);
@@ -881,14 +970,15 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
                 }
                 if (whole) {
                     if (d < D && ok) {
+                        T *const out = static_cast<T *>(a.out) + d;
 #pragma unroll
                         for (int i = 0; i < S::kRows; ++i) {
-                            const int64_t to = row_out[r0 + i];
-                            const float f = s_fac[r0 + i];
-                            if (to >= 0)
-                                static_cast<T *>(a.out)[to + d] = from_f<T>(f == 0.f ? 0.f : v[i] * f);
-                            else if (to < -1)
-                                static_cast<T *>(a.out)[~(to + 1) + d] = from_f<T>(0.f);
+                            if (r0 + i < R) {
+                                const int2 to = place[r0 + i];
+                                const float f = s_fac[r0 + i];
+                                out[(int64_t)(to.x < 0 ? ~to.x : to.x) * a.out_token + (int64_t)to.y * a.out_head] =
+                                    from_f<T>(f == 0.f ? 0.f : v[i] * f);
+                            }
                         }
                     }
                 } else {
@@ -898,75 +988,60 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
                         if (r0 + i < R) part[i * 128] = v[i];
                 }
             }
-            if (!whole) {
-                // the last CTA of the item to finish joins its parts, in share order
-                const int first = (int)(cur.item0 / share), last = (int)((cur.item0 + cur.item_tiles - 1) / share);
-                __threadfence();
-                named_sync<6, S::kSoft>();
-                if (tid == 0) {
-                    const int done = atomicAdd(&P.count[first], 1);
-                    s_last = done == last - first;
-                    if (done == last - first) P.count[first] = 0;  // ready for the next call
-                    __threadfence();
-                }
-                named_sync<6, S::kSoft>();
-                if (s_last) {
-                    auto at = [&](int k, int r) { return (int64_t)(2 * k + (k == first)) * RT + r; };
-                    for (int r = tid; r < R; r += S::kSoft) {
-                        float M = kUnset, L = 0.f;
-                        bool nan = false;
-                        for (int k = first; k <= last; ++k) {
-                            const float m = __ldcg(P.ml + at(k, r) * 2);
-                            nan |= m != m;
-                            M = fmaxf(M, m);
-                        }
-                        if (nan) M = NAN;
-                        for (int k = first; k <= last; ++k) {
-                            const float m = __ldcg(P.ml + at(k, r) * 2), x = __ldcg(P.ml + at(k, r) * 2 + 1);
-                            if (m != kUnset) L += exp2_approx(m - M) * x;
-                        }
-                        const bool none = row_out[r] < -1 || L == 0.f;
-                        s_red[0][r] = M;
-                        s_red[1][r] = none ? 0.f : 1.f / L;
-                        if (a.lse && ok) {
-                            const int i = cur.rt * RT + r, node = i / group;
-                            a.lse[(int64_t)(cur.t0 + node) * a.Hq + cur.h * group + (i - node * group)] =
-                                none ? -INFINITY : (M + log2f(L)) * 0.693147180559945309f;
-                        }
-                    }
-                    named_sync<6, S::kSoft>();
-                    constexpr int kJoin = 8;  // rows whose parts are in flight together
-                    for (int rc = wg * kJoin; rc < R && d < D; rc += kJoin * S::kGroups) {
-                        float o[kJoin] = {};
-#pragma unroll 2
-                        for (int k = first; k <= last; ++k) {
-#pragma unroll
-                            for (int i = 0; i < kJoin; ++i) {
-                                if (rc + i >= R) continue;
-                                const float m = __ldcg(P.ml + at(k, rc + i) * 2);
-                                const float x = __ldcg(P.part + at(k, rc + i) * 128 + d);
-                                if (m != kUnset) o[i] += exp2_approx(m - s_red[0][rc + i]) * x;
-                            }
-                        }
-#pragma unroll
-                        for (int i = 0; i < kJoin; ++i) {
-                            if (rc + i >= R || !ok) continue;
-                            const int64_t to = row_out[rc + i];
-                            const float f = s_red[1][rc + i];
-                            static_cast<T *>(a.out)[(to < -1 ? ~(to + 1) : to) + d] =
-                                from_f<T>(f == 0.f ? 0.f : o[i] * f);
-                        }
-                    }
-                }
-            }
-            // every thread has read the rows' places, sums and the poison mark
-            named_sync<6, S::kSoft>();
         }
         if (tid == 0 && *lost) set_error(P.err, kErrTimeout);
     }
     tc_fence_before();
     __syncthreads();
     if (warp == kMmaWarp) tmem_dealloc(tmem, S::kTmem);
+}
+
+// Joins the parts of cut items: one CTA per share (the item that begins there)
+// and 16 rows, a thread per head column and 8 rows.
+constexpr int kJoinRows = 16;
+template <typename T, int RT>
+__global__ void __launch_bounds__(256) sgmv_tree_join_kernel(const __grid_constant__ MmaParams P) {
+    const sgmv_tree_attention_args &a = P.a;
+    pdl_wait();
+    pdl_trigger();
+    const int id = blockIdx.x;
+    if (id == 0 && blockIdx.y == 0 && threadIdx.x == 0) P.claim[0] = 0;  // ready for the next call
+    if (id >= P.claim[1]) return;
+    const Cut cut = P.cut[id];
+    const int R = min(RT, cut.n * P.group - cut.rt * RT), d = threadIdx.x & 127;
+    const int r0 = blockIdx.y * kJoinRows + (threadIdx.x >> 7) * (kJoinRows / 2);
+    if (cut.parts == 0 || r0 >= R) return;
+    constexpr int N = kJoinRows / 2;
+    float M[N], L[N], o[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) M[i] = kUnset, L[i] = 0.f, o[i] = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < cut.parts; ++k) {
+        const int64_t at = (int64_t)(2 * (id + k) + (k == 0)) * RT + r0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            // rows past R of the last tile hold what earlier calls left: not used
+            const float2 ml = *reinterpret_cast<const float2 *>(P.ml + (at + i) * 2);
+            const float x = P.part[(at + i) * 128 + d];
+            const float m = fmaxf(M[i], ml.x);
+            const float was = exp2_approx(M[i] - m), now = ml.x == kUnset ? 0.f : exp2_approx(ml.x - m);
+            M[i] = m;
+            L[i] = L[i] * was + (now == 0.f ? 0.f : now * ml.y);
+            o[i] = o[i] * was + (now == 0.f ? 0.f : now * x);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if (r0 + i >= R) break;
+        const int2 to = row_place(P, cut.t0, cut.h, cut.rt * RT + r0 + i);
+        const int64_t t = to.x < 0 ? ~to.x : to.x;
+        const bool none = to.x < 0 || L[i] == 0.f;
+        if (d < a.D)
+            static_cast<T *>(a.out)[t * a.out_token + (int64_t)to.y * a.out_head + d] =
+                from_f<T>(none ? 0.f : o[i] / L[i]);
+        if (a.lse && d == 0)
+            a.lse[t * a.Hq + to.y] = none ? -INFINITY : (M[i] + log2f(L[i])) * 0.693147180559945309f;
+    }
 }
 
 template <typename T, int RT>
@@ -976,8 +1051,10 @@ int launch(const MmaParams &p, int ctas, cudaStream_t stream) {
                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)Shape<RT>::kBytes);
     if (e != cudaSuccess) return (int)e;
-    return spec_launch(sgmv_tree_mma_kernel<T, RT>, dim3((unsigned)ctas), Shape<RT>::kThreads,
-                       Shape<RT>::kBytes, 1, stream, p);
+    const int r = spec_launch(sgmv_tree_mma_kernel<T, RT>, dim3((unsigned)ctas), Shape<RT>::kThreads,
+                              Shape<RT>::kBytes, 1, stream, p);
+    if (r != (int)cudaSuccess) return r;
+    return spec_launch(sgmv_tree_join_kernel<T, RT>, dim3(Shape<RT>::kShares, RT / kJoinRows), 256, 0, 1, stream, p);
 }
 
 // Rows per tile: what a sequence of average length fills.
@@ -986,12 +1063,20 @@ int row_tile(int32_t T, int32_t B, int32_t group) {
     return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
 }
 
-constexpr size_t kCountBytes = 1024;
+constexpr size_t kHeadBytes = 256;
+
+size_t shares_of(int rt) {
+    return rt == 16   ? Shape<16>::kShares
+           : rt == 32 ? Shape<32>::kShares
+           : rt == 64 ? Shape<64>::kShares
+                      : Shape<128>::kShares;
+}
 
 }  // namespace
 
 size_t tree_mma_workspace(int32_t T, int32_t B, int32_t group) {
-    return kCountBytes + (size_t)kMaxCtas * 2u * (size_t)row_tile(T, B, group) * 130u * 4u;
+    const int rt = row_tile(T, B, group);
+    return kHeadBytes + shares_of(rt) * (sizeof(Cut) + 2u * (size_t)rt * 130u * 4u);
 }
 
 int tree_mma_launch(const sgmv_tree_attention_args &a, int nsm, int *err, cudaStream_t stream) {
@@ -1001,9 +1086,10 @@ int tree_mma_launch(const sgmv_tree_attention_args &a, int nsm, int *err, cudaSt
     p.a = a;
     p.c = a.scale * 1.4426950408889634f;
     p.group = group;
-    p.count = static_cast<int *>(a.workspace);
-    p.ml = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + kCountBytes);
-    p.part = p.ml + (size_t)kMaxCtas * 2 * rt * 2;
+    p.claim = static_cast<int *>(a.workspace);
+    p.cut = reinterpret_cast<Cut *>(static_cast<uint8_t *>(a.workspace) + kHeadBytes);
+    p.ml = reinterpret_cast<float *>(p.cut + shares_of(rt));
+    p.part = p.ml + shares_of(rt) * 2 * rt * 2;
     p.err = err;
     const bool bf16 = a.dtype == SGMV_BF16;
     // Boxes are as high as pages allow: TMA's cost here is per box (at pages

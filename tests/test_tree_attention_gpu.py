@@ -132,6 +132,34 @@ def test_many_ragged_sequences(sgmv, dtype):
     b.check()
 
 
+@pytest.mark.parametrize("group,n,Hkv,prefix,B", [(1, 9, 32, 1000, 40), (1, 1, 40, 500, 64), (8, 4, 8, 2000, 60),
+                                                  (8, 8, 8, 4000, 40), (8, 20, 8, 9000, 17), (4, 3, 2, 60000, 5)])
+@pytest.mark.parametrize("bs", [16, 24])
+def test_much_work(sgmv, group, n, Hkv, prefix, B, bs):
+    """More work than every SM's own share: parts of items are claimed and joined."""
+    rng = np.random.default_rng(B)
+    lens = [prefix] + [int(x) for x in rng.integers(prefix // 3, prefix, B - 1)]
+    nodes = [n] + [int(x) for x in rng.integers(1, n + 1, B - 1)]
+    b = Batch(lens, nodes, group * Hkv, Hkv, 64, bs, torch.bfloat16, seed=B + n).dirty()
+    ws = torch.zeros(sgmv.sgmv_tree_attention_workspace_bytes(b.T, B, group * Hkv, Hkv, 64), dtype=torch.uint8,
+                     device="cuda")
+    b.run(sgmv, workspace=ws)
+    check_error_word(0)
+    first = b.out.clone()
+    for _ in range(3):
+        b.out.zero_()
+        b.run(sgmv, workspace=ws)
+        assert torch.equal(b.out, first)
+    check_error_word(0)
+    # a sample of the sequences against the reference
+    few = sorted({0, B // 2, B - 1})
+    rows = np.concatenate([np.arange(b.ptr[s], b.ptr[s + 1]) for s in few])
+    b.total, b.table, b.prefix = [b.total[s] for s in few], b.table[few], [b.prefix[s] for s in few]
+    b.parents = [b.parents[r] for r in rows]
+    b.q, b.out, b.lse, b.ptr = b.q[rows], b.out[rows], b.lse[rows], ref.ptr_of([nodes[s] for s in few])
+    b.check()
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("n", [1, 4, 31, 200])
 def test_chains_without_parents(sgmv, dtype, n):
