@@ -208,6 +208,22 @@ __device__ __forceinline__ void commit_on(uint32_t on, uint64_t *bar) {
         "r"(on)
         : "memory");
 }
+// Two fp32 operations in one instruction, each rounded as alone.
+__device__ __forceinline__ void fma_pair(float &x, float &y, float c, float a, float b) {
+    uint64_t v, w, k;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+    asm("mov.b64 %0, {%1, %1};" : "=l"(k) : "f"(c));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(w) : "f"(a), "f"(b));
+    asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(v) : "l"(k), "l"(w));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ void add_pair(float &x, float &y, float a, float b) {
+    uint64_t v, w;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(w) : "f"(a), "f"(b));
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(w));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
 // floats as integers of the same order
 __device__ __forceinline__ int ordered(float f) {
     const int i = __float_as_int(f);
@@ -310,7 +326,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
     __shared__ Plan plan;
     __shared__ Segment s_seg[kSegs], s_cur;        // s_cur: the softmax warps' segment
     __shared__ int16_t s_parent[SGMV_TREE_MAX_NODES];
-    __shared__ __align__(16) float s_ref[RT], s_fac[RT];
+    __shared__ __align__(16) float s_ref[RT], s_fac[RT];  // s_ref: -ref
     __shared__ float s_red[4][RT];
     uint8_t *const sm = align1024(dsm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -337,7 +353,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
         __syncwarp();
         tmem_alloc(&s_tmem, S::kTmem);
     }
-    for (int i = tid; i < RT; i += S::kThreads) s_ref[i] = kUnset;
+    for (int i = tid; i < RT; i += S::kThreads) s_ref[i] = -kUnset;
     // columns past D that the products read are zero: in Q, and in K where TMA
     // does not fill them; so are the rows past a short tile
     if (P.tok < kTok)
@@ -814,27 +830,30 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
                 if (edge && (tok >= P.tok || j >= prefix))
                     vis = tok < P.tok && j < cur.total ? see[(j - prefix) * S::kWords] : 0u;
                 float s[S::kRows];
-                // the masked exponents
-                auto exponents = [&]() {
+                // the weights, and their largest exponent; ref holds -ref
+                float top;
+                auto weights = [&]() {
                     tmem_load(ts, s);
 #pragma unroll
                     for (int i = 0; i < S::kRows; i += 4) {
                         const uint4 u = lds128(&s_ref[r0 + i]);
-                        s[i] = fmaf(s[i], c, -__uint_as_float(u.x));
-                        s[i + 1] = fmaf(s[i + 1], c, -__uint_as_float(u.y));
-                        s[i + 2] = fmaf(s[i + 2], c, -__uint_as_float(u.z));
-                        s[i + 3] = fmaf(s[i + 3], c, -__uint_as_float(u.w));
+                        fma_pair(s[i], s[i + 1], c, __uint_as_float(u.x), __uint_as_float(u.y));
+                        fma_pair(s[i + 2], s[i + 3], c, __uint_as_float(u.z), __uint_as_float(u.w));
                     }
                     if (edge) {
 #pragma unroll
                         for (int i = 0; i < S::kRows; ++i)
                             if (!(vis >> i & 1u)) s[i] = -INFINITY;
                     }
-                };
-                exponents();
-                float top = -INFINITY;
+                    top = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < S::kRows; ++i) top = fmaxf(top, s[i]);
+                    for (int i = 0; i < S::kRows; i += 2) {
+                        top = fmaxf(top, fmaxf(s[i], s[i + 1]));
+                        s[i] = exp2_approx(s[i]);
+                        s[i + 1] = exp2_approx(s[i + 1]);
+                    }
+                };
+                weights();
                 if (group_any(wg, top > kBias + kSlack)) {
                     // new references: the larger of the old and this tile's maximum
                     tmem_load(ts, s);
@@ -854,11 +873,11 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
                             const float x = s_red[w][r];
                             m = x > m || x != x ? x : m;
                         }
-                        const float old = s_ref[r];
+                        const float old = -s_ref[r];
                         float now = m - kBias;
                         now = now > old || now != now ? now : old;
                         s_fac[r] = old == kUnset ? 0.f : exp2_approx(old - now);
-                        s_ref[r] = now;
+                        s_ref[r] = -now;
                     }
                     group_bar(wg);
 #pragma unroll
@@ -870,14 +889,14 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
                         for (int i = 0; i < S::kRows; ++i) s[i] *= s_fac[r0 + i];
                         tmem_store(t_o, s);
                     }
-                    exponents();
+                    weights();
                 }
                 T p[S::kRows];  // rounded to the tensor cores' operand type
 #pragma unroll
-                for (int i = 0; i < S::kRows; ++i) {
-                    const float e = exp2_approx(s[i]);
-                    l[i] += e;
-                    p[i] = from_f<T>(e);
+                for (int i = 0; i < S::kRows; i += 2) {
+                    add_pair(l[i], l[i + 1], s[i], s[i + 1]);
+                    p[i] = from_f<T>(s[i]);
+                    p[i + 1] = from_f<T>(s[i + 1]);
                 }
                 // the previous tile's P has been read
                 if (g > 0) done(2 * g - 1);
@@ -934,7 +953,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
             const int2 *const place = reinterpret_cast<const int2 *>(sm + S::kOffRow) + (seg % kSegs) * RT;
             if (tok < S::kRows) {
                 const int r = r0 + tok;
-                const float L = s_red[0][r] + s_red[1][r] + s_red[2][r] + s_red[3][r], ref = s_ref[r];
+                const float L = s_red[0][r] + s_red[1][r] + s_red[2][r] + s_red[3][r], ref = -s_ref[r];
                 if (!whole) {
                     *reinterpret_cast<float2 *>(P.ml + ((int64_t)slot * RT + r) * 2) = make_float2(ref, L);
                 } else if (r < R) {
@@ -945,7 +964,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
                         a.lse[(int64_t)(to.x < 0 ? ~to.x : to.x) * a.Hq + to.y] =
                             none ? -INFINITY : (ref + log2f(L)) * 0.693147180559945309f;
                 }
-                s_ref[r] = kUnset;
+                s_ref[r] = -kUnset;
             }
             done(2 * g - 1);
             group_bar(wg);
@@ -996,51 +1015,49 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
     if (warp == kMmaWarp) tmem_dealloc(tmem, S::kTmem);
 }
 
-// Joins the parts of cut items: one CTA per share (the item that begins there)
-// and 16 rows, a thread per head column and 8 rows.
-constexpr int kJoinRows = 16;
+// Joins the parts of cut items: a warp per (share, row), the item being the one
+// that begins in the share; a lane owns four head columns.
+constexpr int kJoinThreads = 256;
 template <typename T, int RT>
-__global__ void __launch_bounds__(256) sgmv_tree_join_kernel(const __grid_constant__ MmaParams P) {
+__global__ void __launch_bounds__(kJoinThreads) sgmv_tree_join_kernel(const __grid_constant__ MmaParams P) {
     const sgmv_tree_attention_args &a = P.a;
     pdl_wait();
     pdl_trigger();
-    const int id = blockIdx.x;
-    if (id == 0 && blockIdx.y == 0 && threadIdx.x == 0) P.claim[0] = 0;  // ready for the next call
-    if (id >= P.claim[1]) return;
-    const Cut cut = P.cut[id];
-    const int R = min(RT, cut.n * P.group - cut.rt * RT), d = threadIdx.x & 127;
-    const int r0 = blockIdx.y * kJoinRows + (threadIdx.x >> 7) * (kJoinRows / 2);
-    if (cut.parts == 0 || r0 >= R) return;
-    constexpr int N = kJoinRows / 2;
-    float M[N], L[N], o[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) M[i] = kUnset, L[i] = 0.f, o[i] = 0.f;
+    const int warps = gridDim.x * (kJoinThreads / 32), lane = threadIdx.x & 31;
+    const int units = P.claim[1] * RT;
+    if (blockIdx.x == 0 && threadIdx.x == 0) P.claim[0] = 0;  // ready for the next call
+    for (int u = blockIdx.x * (kJoinThreads / 32) + threadIdx.x / 32; u < units; u += warps) {
+        const int id = u / RT, r = u % RT;
+        const Cut cut = P.cut[id];
+        if (cut.parts == 0 || cut.rt * RT + r >= cut.n * P.group) continue;
+        const int2 to = row_place(P, cut.t0, cut.h, cut.rt * RT + r);
+        float M = kUnset, L = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int k = 0; k < cut.parts; ++k) {
-        const int64_t at = (int64_t)(2 * (id + k) + (k == 0)) * RT + r0;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            // rows past R of the last tile hold what earlier calls left: not used
-            const float2 ml = *reinterpret_cast<const float2 *>(P.ml + (at + i) * 2);
-            const float x = P.part[(at + i) * 128 + d];
-            const float m = fmaxf(M[i], ml.x);
-            const float was = exp2_approx(M[i] - m), now = ml.x == kUnset ? 0.f : exp2_approx(ml.x - m);
-            M[i] = m;
-            L[i] = L[i] * was + (now == 0.f ? 0.f : now * ml.y);
-            o[i] = o[i] * was + (now == 0.f ? 0.f : now * x);
+        for (int k = 0; k < cut.parts; ++k) {
+            const int64_t at = (int64_t)(2 * (id + k) + (k == 0)) * RT + r;
+            const float2 ml = *reinterpret_cast<const float2 *>(P.ml + at * 2);
+            const float4 x = reinterpret_cast<const float4 *>(P.part + at * 128)[lane];
+            if (ml.x == kUnset) continue;  // the row saw nothing there
+            const float m = fmaxf(M, ml.x), was = exp2_approx(M - m), now = exp2_approx(ml.x - m);
+            M = m;
+            L = L * was + ml.y * now;
+            o.x = o.x * was + x.x * now;
+            o.y = o.y * was + x.y * now;
+            o.z = o.z * was + x.z * now;
+            o.w = o.w * was + x.w * now;
         }
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        if (r0 + i >= R) break;
-        const int2 to = row_place(P, cut.t0, cut.h, cut.rt * RT + r0 + i);
         const int64_t t = to.x < 0 ? ~to.x : to.x;
-        const bool none = to.x < 0 || L[i] == 0.f;
-        if (d < a.D)
-            static_cast<T *>(a.out)[t * a.out_token + (int64_t)to.y * a.out_head + d] =
-                from_f<T>(none ? 0.f : o[i] / L[i]);
-        if (a.lse && d == 0)
-            a.lse[t * a.Hq + to.y] = none ? -INFINITY : (M[i] + log2f(L[i])) * 0.693147180559945309f;
+        const bool none = to.x < 0 || L == 0.f;
+        const float f = none ? 0.f : 1.f / L;
+        if (lane * 4 < a.D) {
+            T v[4] = {from_f<T>(none ? 0.f : o.x * f), from_f<T>(none ? 0.f : o.y * f),
+                      from_f<T>(none ? 0.f : o.z * f), from_f<T>(none ? 0.f : o.w * f)};
+            *reinterpret_cast<uint2 *>(static_cast<T *>(a.out) + t * a.out_token + (int64_t)to.y * a.out_head + lane * 4) =
+                *reinterpret_cast<const uint2 *>(v);
+        }
+        if (a.lse && lane == 0)
+            a.lse[t * a.Hq + to.y] = none ? -INFINITY : (M + log2f(L)) * 0.693147180559945309f;
     }
 }
 
@@ -1054,7 +1071,7 @@ int launch(const MmaParams &p, int ctas, cudaStream_t stream) {
     const int r = spec_launch(sgmv_tree_mma_kernel<T, RT>, dim3((unsigned)ctas), Shape<RT>::kThreads,
                               Shape<RT>::kBytes, 1, stream, p);
     if (r != (int)cudaSuccess) return r;
-    return spec_launch(sgmv_tree_join_kernel<T, RT>, dim3(Shape<RT>::kShares, RT / kJoinRows), 256, 0, 1, stream, p);
+    return spec_launch(sgmv_tree_join_kernel<T, RT>, dim3((unsigned)(8 * ctas)), kJoinThreads, 0, 1, stream, p);
 }
 
 // Rows per tile: what a sequence of average length fills.
