@@ -1,12 +1,16 @@
 // sgmv_rope.cu -- rotary positions of q and k, and the append of k and v to
 // the paged cache.
 //
-// One CTA per token (several along y when there are few tokens): the sines
-// and cosines of the token's pairs are computed once, into shared memory, and
-// used by all of its heads.  The angle position * inv_freq is a fraction of a
-// turn in 64-bit fixed point, so the product wraps modulo one turn by itself
-// and keeps 32 bits of the fraction at any position; in fp32 the product
-// alone would lose 2^-24 of the angle, 0.008 rad at position 131072.
+// One CTA per token: the sines and cosines of the token's pairs are computed
+// once, into shared memory, and used by all of its heads.  The angle position *
+// inv_freq is a fraction of a turn in 64-bit fixed point, so the product wraps
+// modulo one turn by itself and keeps 32 bits of the fraction at any position;
+// in fp32 the product alone would lose 2^-24 of the angle, 0.008 rad at
+// position 131072.
+//
+// Bound by memory for many tokens and by the chain position -> sine -> store
+// for few: the first rows are requested before the angles are computed, four
+// 16- or 32-byte pieces per thread at once.
 #include "sgmv_device.cuh"
 #include "sgmv_spec.h"
 
@@ -14,25 +18,66 @@ namespace sgmv {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeBatch = 4;  // pieces in flight per thread
 
-struct RopePhases {
-    uint64_t f[kRopeMaxPairs];
+enum RopeMode : int {
+    kHalves = 0,       // pairs (i, i + pairs), pairs a multiple of 8: 16-byte vectors
+    kInterleaved = 1,  // pairs (2i, 2i + 1): 16-byte vectors
+    kScalar = 2,       // pairs (i, i + pairs) of any number: one pair or column at a time
 };
 
-// Work items of a token: units of 16 bytes (scalar half pairs: of one pair or
-// one copied element), q's heads first, then k's, then v's (copied).
-template <typename T>
-__global__ void __launch_bounds__(kRopeThreads)
-    sgmv_rope_kernel(const __grid_constant__ sgmv_rope_args a, const __grid_constant__ RopePhases ph,
-                     int *err) {
+struct RopeParams {
+    sgmv_rope_args a;
+    uint64_t turns[kRopeMaxPairs];  // turns per position of every pair, times 2^64
+    int32_t rot, uph;               // pieces that rotate, pieces in all, per head
+    uint32_t by_uph, by_vec;        // 2^32 / uph and 2^32 / (D / 8), rounded up; 0: divide by one
+};
+
+// u / n for u * n < 2^32, by = 2^32 / n rounded up (0 for n = 1)
+__device__ __forceinline__ int quotient(int u, uint32_t by) {
+    return by ? (int)__umulhi((uint32_t)u, by) : u;
+}
+
+// Pieces of a token: q's heads, then k's, then v's (copied, D / 8 per head).
+template <typename T, int MODE>
+__global__ void __launch_bounds__(kRopeThreads, 4)
+    sgmv_rope_kernel(const __grid_constant__ RopeParams P, int *err) {
+    const sgmv_rope_args &a = P.a;
     __shared__ float s_cos[kRopeMaxPairs], s_sin[kRopeMaxPairs];
-    const int tid = threadIdx.x, t = blockIdx.x;
+    const int tid = threadIdx.x, pairs = a.pairs, D = a.D, uph = P.uph, rot = P.rot;
+    const int64_t t = blockIdx.x;
     pdl_wait();
     pdl_trigger();
-    const int pairs = a.pairs, D = a.D;
-    const int32_t pos = a.positions[t];
+    const int32_t pos = a.positions[t], slot = a.k_cache ? a.slots[t] : -1;
+    const int nqk = (a.Hq + a.Hk) * uph;
+    const int units = nqk + (slot >= 0 ? a.Hk * (D / 8) : 0);
+
+    uint4 x[kRopeBatch], y[kRopeBatch];
+    auto load = [&](int u, uint4 &x, uint4 &y) {
+        if (u >= nqk) {
+            const int h = quotient(u - nqk, P.by_vec), c = (u - nqk - h * (D / 8)) * 8;
+            x = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.v) + t * a.v_token + h * a.v_head + c);
+            return;
+        }
+        const int h = quotient(u, P.by_uph), w = u - h * uph;
+        const T *src = h < a.Hq ? static_cast<const T *>(a.q) + t * a.q_token + h * a.q_head
+                                : static_cast<const T *>(a.k) + t * a.k_token + (h - a.Hq) * a.k_head;
+        if (MODE == kScalar) {
+            x.x = *reinterpret_cast<const uint16_t *>(src + (w < rot ? w : w + pairs));
+            if (w < rot) y.x = *reinterpret_cast<const uint16_t *>(src + w + pairs);
+        } else if (MODE == kHalves && w < rot) {
+            x = *reinterpret_cast<const uint4 *>(src + w * 8);
+            y = *reinterpret_cast<const uint4 *>(src + w * 8 + pairs);
+        } else {
+            x = *reinterpret_cast<const uint4 *>(src + (MODE == kHalves ? (w - rot) * 8 + 2 * pairs : w * 8));
+        }
+    };
+#pragma unroll
+    for (int e = 0; e < kRopeBatch; ++e)
+        if (tid + e * kRopeThreads < units) load(tid + e * kRopeThreads, x[e], y[e]);
+
     if (tid < pairs) {
-        const uint64_t turn = (uint64_t)(int64_t)pos * ph.f[tid];  // modulo one turn
+        const uint64_t turn = (uint64_t)(int64_t)pos * P.turns[tid];  // modulo one turn
         const float half_turns = (float)(int32_t)(turn >> 32) * 0x1p-31f;
         float sn, cs;
         sincospif(half_turns, &sn, &cs);
@@ -40,100 +85,106 @@ __global__ void __launch_bounds__(kRopeThreads)
         s_sin[tid] = (a.inverse ? -sn : sn) * a.scale;
     }
     int64_t slot_off = -1;
-    if (a.k_cache) {
-        const int32_t slot = a.slots[t];
-        if (slot >= 0 && (int64_t)slot < (int64_t)a.num_blocks * a.block_size)
-            slot_off = (int64_t)(slot / a.block_size) * a.cache_block +
-                       (int64_t)(slot % a.block_size) * a.cache_token;
-        else if (slot != -1 && tid == 0 && blockIdx.y == 0)
-            set_error(err, kErrBadIndex);
-    }
+    if (slot >= 0 && (int64_t)slot < (int64_t)a.num_blocks * a.block_size)
+        slot_off = (int64_t)(slot / a.block_size) * a.cache_block + (int64_t)(slot % a.block_size) * a.cache_token;
+    else if (slot != -1 && tid == 0)
+        set_error(err, kErrBadIndex);
     __syncthreads();
-    const int mode = a.interleaved ? 1 : pairs % 8 == 0 ? 0 : 2;
-    // units per rotated head: half pairs in 16-byte vectors, then the copied
-    // columns; interleaved: every 16-byte vector; scalar: pairs, then columns
-    const int rot = mode == 0 ? pairs / 8 : mode == 1 ? D / 8 : pairs;
-    const int uph = mode == 0 ? rot + (D - 2 * pairs) / 8 : mode == 1 ? rot : rot + (D - 2 * pairs);
-    const int nqk = (a.Hq + a.Hk) * uph;
-    const int nv = slot_off >= 0 ? a.Hk * (D / 8) : 0;
-    for (int u = blockIdx.y * kRopeThreads + tid; u < nqk + nv; u += gridDim.y * kRopeThreads) {
+
+    auto store = [&](int u, uint4 x, uint4 y) {
         if (u >= nqk) {
-            const int h = (u - nqk) / (D / 8), c = (u - nqk) % (D / 8) * 8;
-            const T *src = static_cast<const T *>(a.v) + t * a.v_token + h * a.v_head + c;
-            *reinterpret_cast<uint4 *>(static_cast<T *>(a.v_cache) + slot_off + h * a.cache_head + c) =
-                *reinterpret_cast<const uint4 *>(src);
-            continue;
+            const int h = quotient(u - nqk, P.by_vec), c = (u - nqk - h * (D / 8)) * 8;
+            if (slot_off >= 0)
+                *reinterpret_cast<uint4 *>(static_cast<T *>(a.v_cache) + slot_off + h * a.cache_head + c) = x;
+            return;
         }
-        int h = u / uph;
+        int h = quotient(u, P.by_uph);
         const int w = u - h * uph;
-        const T *src;
         T *dst, *dst2 = nullptr;
         if (h < a.Hq) {
-            src = static_cast<const T *>(a.q) + t * a.q_token + h * a.q_head;
             dst = static_cast<T *>(a.q_out) + t * a.q_out_token + h * a.q_out_head;
         } else {
             h -= a.Hq;
-            src = static_cast<const T *>(a.k) + t * a.k_token + h * a.k_head;
             dst = a.k_out ? static_cast<T *>(a.k_out) + t * a.k_out_token + h * a.k_out_head : nullptr;
             if (slot_off >= 0) dst2 = static_cast<T *>(a.k_cache) + slot_off + h * a.cache_head;
         }
-        if (mode == 2) {
-            if (w < pairs) {
-                const float x = to_f<T>(src[w]), y = to_f<T>(src[w + pairs]);
-                const T p = from_f<T>(x * s_cos[w] - y * s_sin[w]);
-                const T q = from_f<T>(x * s_sin[w] + y * s_cos[w]);
-                if (dst) dst[w] = p, dst[w + pairs] = q;
-                if (dst2) dst2[w] = p, dst2[w + pairs] = q;
+        if (MODE == kScalar) {
+            const T xs = *reinterpret_cast<const T *>(&x.x), ys = *reinterpret_cast<const T *>(&y.x);
+            if (w < rot) {
+                const float p = to_f<T>(xs), q = to_f<T>(ys);
+                const T r = from_f<T>(p * s_cos[w] - q * s_sin[w]), s = from_f<T>(p * s_sin[w] + q * s_cos[w]);
+                if (dst) dst[w] = r, dst[w + pairs] = s;
+                if (dst2) dst2[w] = r, dst2[w + pairs] = s;
             } else {
-                const int c = w + pairs;
-                const T p = src[c];
-                if (dst) dst[c] = p;
-                if (dst2) dst2[c] = p;
+                if (dst) dst[w + pairs] = xs;
+                if (dst2) dst2[w + pairs] = xs;
             }
-        } else if (mode == 0 && w < rot) {
-            const int c = w * 8;
-            float x[8], y[8], p[8], q[8];
-            load8<T>(src + c, x);
-            load8<T>(src + c + pairs, y);
+            return;
+        }
+        int c = w * 8;
+        if (MODE == kHalves && w < rot) {
+            T *xs = reinterpret_cast<T *>(&x), *ys = reinterpret_cast<T *>(&y);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                p[e] = x[e] * s_cos[c + e] - y[e] * s_sin[c + e];
-                q[e] = x[e] * s_sin[c + e] + y[e] * s_cos[c + e];
+                const float p = to_f<T>(xs[e]), q = to_f<T>(ys[e]);
+                xs[e] = from_f<T>(p * s_cos[c + e] - q * s_sin[c + e]);
+                ys[e] = from_f<T>(p * s_sin[c + e] + q * s_cos[c + e]);
             }
-            if (dst) store8<T>(dst + c, p), store8<T>(dst + c + pairs, q);
-            if (dst2) store8<T>(dst2 + c, p), store8<T>(dst2 + c + pairs, q);
+            if (dst) *reinterpret_cast<uint4 *>(dst + c + pairs) = y;
+            if (dst2) *reinterpret_cast<uint4 *>(dst2 + c + pairs) = y;
+        } else if (MODE == kHalves) {
+            c = (w - rot) * 8 + 2 * pairs;
         } else {
-            const int c = mode == 0 ? (w - rot) * 8 + 2 * pairs : w * 8;
-            uint4 r = *reinterpret_cast<const uint4 *>(src + c);
-            if (mode == 1 && c < 2 * pairs) {
-                T *x = reinterpret_cast<T *>(&r);
+            T *xs = reinterpret_cast<T *>(&x);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int i = c / 2 + e;
-                    if (i < pairs) {
-                        const float p = to_f<T>(x[2 * e]), q = to_f<T>(x[2 * e + 1]);
-                        x[2 * e] = from_f<T>(p * s_cos[i] - q * s_sin[i]);
-                        x[2 * e + 1] = from_f<T>(p * s_sin[i] + q * s_cos[i]);
-                    }
+            for (int e = 0; e < 4; ++e) {
+                const int i = w * 4 + e;
+                if (i < pairs) {
+                    const float p = to_f<T>(xs[2 * e]), q = to_f<T>(xs[2 * e + 1]);
+                    xs[2 * e] = from_f<T>(p * s_cos[i] - q * s_sin[i]);
+                    xs[2 * e + 1] = from_f<T>(p * s_sin[i] + q * s_cos[i]);
                 }
             }
-            if (dst) *reinterpret_cast<uint4 *>(dst + c) = r;
-            if (dst2) *reinterpret_cast<uint4 *>(dst2 + c) = r;
         }
+        if (dst) *reinterpret_cast<uint4 *>(dst + c) = x;
+        if (dst2) *reinterpret_cast<uint4 *>(dst2 + c) = x;
+    };
+    for (int u0 = 0;;) {
+#pragma unroll
+        for (int e = 0; e < kRopeBatch; ++e)
+            if (u0 + tid + e * kRopeThreads < units) store(u0 + tid + e * kRopeThreads, x[e], y[e]);
+        u0 += kRopeBatch * kRopeThreads;
+        if (u0 >= units) break;
+#pragma unroll
+        for (int e = 0; e < kRopeBatch; ++e)
+            if (u0 + tid + e * kRopeThreads < units) load(u0 + tid + e * kRopeThreads, x[e], y[e]);
+    }
+}
+
+uint32_t inverse_of(int n) { return n > 1 ? (uint32_t)(((1ull << 32) + n - 1) / n) : 0; }
+
+template <typename T> int launch(const RopeParams &p, int mode, int *err, cudaStream_t stream) {
+    const dim3 grid((unsigned)p.a.T);
+    switch (mode) {
+        case kHalves: return spec_launch(sgmv_rope_kernel<T, kHalves>, grid, kRopeThreads, 0, 1, stream, p, err);
+        case kInterleaved:
+            return spec_launch(sgmv_rope_kernel<T, kInterleaved>, grid, kRopeThreads, 0, 1, stream, p, err);
+        default: return spec_launch(sgmv_rope_kernel<T, kScalar>, grid, kRopeThreads, 0, 1, stream, p, err);
     }
 }
 
 }  // namespace
 
-int rope_launch(const sgmv_rope_args &a, const uint64_t *phase, int nsm, int *err,
-                cudaStream_t stream) {
-    RopePhases ph;
-    for (int i = 0; i < a.pairs; ++i) ph.f[i] = phase[i];
-    const dim3 grid((unsigned)a.T, 1, 1);
-    return a.dtype == SGMV_F16
-               ? spec_launch(sgmv_rope_kernel<__half>, grid, kRopeThreads, 0, 1, stream, a, ph, err)
-               : spec_launch(sgmv_rope_kernel<__nv_bfloat16>, grid, kRopeThreads, 0, 1, stream, a,
-                             ph, err);
+int rope_launch(const sgmv_rope_args &a, const uint64_t *turns, int *err, cudaStream_t stream) {
+    RopeParams p;
+    p.a = a;
+    for (int i = 0; i < a.pairs; ++i) p.turns[i] = turns[i];
+    const int mode = a.interleaved ? kInterleaved : a.pairs % 8 == 0 ? kHalves : kScalar, rest = a.D - 2 * a.pairs;
+    p.rot = mode == kHalves ? a.pairs / 8 : mode == kInterleaved ? a.D / 8 : a.pairs;
+    p.uph = mode == kHalves ? p.rot + rest / 8 : mode == kInterleaved ? p.rot : p.rot + rest;
+    p.by_uph = inverse_of(p.uph);
+    p.by_vec = inverse_of(a.D / 8);
+    return a.dtype == SGMV_F16 ? launch<__half>(p, mode, err, stream) : launch<__nv_bfloat16>(p, mode, err, stream);
 }
 
 }  // namespace sgmv

@@ -14,9 +14,8 @@ constexpr int kSpecMaxD = 256;               // widest head
 constexpr int kRopeMaxPairs = kSpecMaxD / 2;
 
 // Every launcher returns a cudaError_t value.
-// phase[i]: turns per position of pair i, as a fraction of 2^64.
-int rope_launch(const sgmv_rope_args &a, const uint64_t *phase, int nsm, int *err,
-                cudaStream_t stream);
+// turns[i]: turns per position of pair i, modulo one, times 2^64.
+int rope_launch(const sgmv_rope_args &a, const uint64_t *turns, int *err, cudaStream_t stream);
 int tree_attention_launch(const sgmv_tree_attention_args &a, int nsm, int *err,
                           cudaStream_t stream);
 // The tensor-core form, for D <= kMmaMaxD.
@@ -25,7 +24,7 @@ size_t tree_mma_workspace(int32_t T, int32_t B, int32_t group);
 int tree_mma_launch(const sgmv_tree_attention_args &a, int nsm, int *err, cudaStream_t stream);
 size_t tree_attention_workspace(int32_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D);
 int tree_verify_launch(const sgmv_tree_verify_args &a, int nsm, int *err, cudaStream_t stream);
-int cache_commit_launch(const sgmv_cache_commit_args &a, int nsm, int *err, cudaStream_t stream);
+int cache_commit_launch(const sgmv_cache_commit_args &a, int *err, cudaStream_t stream);
 
 // Records how many kernels the calling thread's last call launched.
 void set_launch_count(int n);

@@ -65,16 +65,16 @@ int sgmv_rope(const sgmv_rope_args *args, void *stream) {
                    !vectors(a.v_cache, a.cache_head, 0)))
         return SGMV_ERR_ALIGNMENT;
     // turns per position, modulo one turn, as a fraction of 2^64
-    uint64_t phase[kRopeMaxPairs];
+    uint64_t turns[kRopeMaxPairs];
     for (int i = 0; i < a.pairs; ++i) {
-        const double turns = a.inv_freq[i] / 6.283185307179586476925;
-        if (!(fabs(turns) < 1e15)) return SGMV_ERR_INVALID_ARG;
-        const double part = turns - floor(turns);  // [0, 1]
-        phase[i] = part < 1.0 ? (uint64_t)ldexp(part, 64) : 0;
+        const double f = a.inv_freq[i] / 6.283185307179586476925;
+        if (!(fabs(f) < 1e15)) return SGMV_ERR_INVALID_ARG;
+        const double part = f - floor(f);  // [0, 1]
+        turns[i] = part < 1.0 ? (uint64_t)ldexp(part, 64) : 0;
     }
     int *err = device_error_word();
     if (!err) return SGMV_ERR_CUDA;
-    return finish("rotary kernel", rope_launch(a, phase, device_sms(), err, static_cast<cudaStream_t>(stream)), 1);
+    return finish("rotary kernel", rope_launch(a, turns, err, static_cast<cudaStream_t>(stream)), 1);
 }
 
 int sgmv_rope_frequencies(double *inv_freq, int32_t pairs, double base, double factor,
@@ -165,7 +165,7 @@ int sgmv_cache_commit(const sgmv_cache_commit_args *args, void *stream) {
     int *err = device_error_word();
     if (!err) return SGMV_ERR_CUDA;
     return finish("commit kernel",
-                  cache_commit_launch(a, device_sms(), err, static_cast<cudaStream_t>(stream)), 1);
+                  cache_commit_launch(a, err, static_cast<cudaStream_t>(stream)), 1);
 }
 
 }  // extern "C"

@@ -4,10 +4,20 @@
 // Probabilities become whole multiples of 2^-38, so that a distribution's sum
 // is exact in 64 bits whatever the order of summation, and the drawn token is
 // the same for any division of the vocabulary among threads.  The products
-// q * W are single fp32 multiplications of each element.  An accepted child
-// costs two lookups; only a rejected one needs a pass over the vocabulary, for
-// the sum of what is left.  The rest of a distribution after k rejections
-// is recomputed from p, q and the k earlier sums instead of being stored.
+// q * W are single fp32 multiplications of each element.
+//
+// Every node's p and q at its own token are looked up first, all at once, so
+// the walk itself touches no memory; only a rejected child costs a pass over
+// the vocabulary, for the sum of what is left.  The rest of a distribution
+// after k rejections is recomputed from p, q and the k earlier sums instead of
+// being stored.  Without a draft a rejection only takes the token out, so one
+// pass per node is enough.
+//
+// A cluster of CTAs shares a sequence's vocabulary when there are few
+// sequences; all of its CTAs walk alike and exchange their sums through
+// distributed shared memory.
+#include <algorithm>
+
 #include "sgmv_device.cuh"
 #include "sgmv_spec.h"
 
@@ -16,149 +26,253 @@ namespace {
 
 constexpr int kVerifyThreads = 1024;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
+constexpr int kVerifyMaxCluster = 8;
+constexpr int kVerifyUnroll = 4;  // vectors in flight per thread and distribution
 constexpr int64_t kOne = 1ll << 38;
 
 __device__ __forceinline__ float prob(float p) { return fminf(fmaxf(p, 0.f), 1.f); }  // NaN -> 0
 __device__ __forceinline__ int64_t weight(float p) { return (int64_t)(prob(p) * 0x1p38f); }
 
 struct VerifyShared {
-    float W[SGMV_TREE_MAX_NODES];      // W before each rejection at this node
-    int32_t out[SGMV_TREE_MAX_NODES];  // rejected tokens (without a draft)
-    int64_t part[kVerifyWarps];
-    int64_t total;
-    int32_t token;
+    float p[SGMV_TREE_MAX_NODES], q[SGMV_TREE_MAX_NODES];  // at the node's token, after its parent
+    float u[SGMV_TREE_MAX_NODES];
+    int32_t token[SGMV_TREE_MAX_NODES];
+    int16_t parent[SGMV_TREE_MAX_NODES];  // -2: not to be tried
+    float W[SGMV_TREE_MAX_NODES];         // W before each rejection at this node
+    int32_t out[SGMV_TREE_MAX_NODES];     // rejected tokens (without a draft)
+    int64_t part[kVerifyWarps];           // sums of the warps' ranges
+    int64_t mine[2];                      // sum of this CTA's range, by pass
+    int64_t scan[kVerifyWarps];
 };
 
-// w(token j) after `k` rejections at a node with distributions p and q
-__device__ __forceinline__ int64_t rest(const float *p, const float *q, int j, int k,
-                                        const VerifyShared &s) {
-    int64_t w = weight(p[j]);
-    if (q) {
-        const float qj = k > 0 ? prob(q[j]) : 0.f;
-        for (int i = 0; i < k; ++i) {
-            w -= (int64_t)__fmul_rn(qj, s.W[i]);
-            w = w < 0 ? 0 : w;
-        }
-    } else {
-        for (int i = 0; i < k; ++i)
-            if (s.out[i] == j) w = 0;
+// The rest after k rejections of a token with p, q (with a draft).
+__device__ __forceinline__ int64_t shrink(float p, float q, int k, const float *W) {
+    int64_t w = weight(p);
+    const float qc = prob(q);
+    for (int i = 0; i < k; ++i) {
+        w -= (int64_t)__fmul_rn(qc, W[i]);
+        w = w < 0 ? 0 : w;
     }
     return w;
 }
 
-// One CTA per sequence.  Warp w holds vocabulary range [w c, (w + 1) c).
 __global__ void __launch_bounds__(kVerifyThreads)
     sgmv_verify_kernel(const __grid_constant__ sgmv_tree_verify_args a, int *err) {
     __shared__ VerifyShared s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int b = blockIdx.x;
+    const int cl = (int)cluster_size(), rank = (int)cluster_rank(), b = (int)blockIdx.x / cl;
     pdl_wait();
     pdl_trigger();
     const int t0 = a.tree_ptr[b], n = a.tree_ptr[b + 1] - t0;
     int32_t *path = a.path + (int64_t)b * a.max_path;
+    const bool writer = rank == 0 && tid == 0;
     const bool bad = t0 < 0 || n < 0 || n > SGMV_TREE_MAX_NODES || (int64_t)t0 + n > a.T;
-    if (bad && tid == 0) set_error(err, kErrBadSegments);
-    if (bad || n == 0) {
-        for (int i = tid; i < a.max_path; i += kVerifyThreads) path[i] = -1;
-        if (tid == 0) a.count[b] = 0, a.token[b] = -1;
+    if (bad && writer) set_error(err, kErrBadSegments);
+    if (bad || n == 0) {  // the whole cluster alike
+        if (rank == 0)
+            for (int i = tid; i < a.max_path; i += kVerifyThreads) path[i] = -1;
+        if (writer) a.count[b] = 0, a.token[b] = -1;
         return;
     }
-    const int chunk = (a.V + kVerifyWarps - 1) / kVerifyWarps;
-    const int v0 = min(a.V, warp * chunk), v1 = min(a.V, v0 + chunk);
-    // sums of the rest after k rejections: part[] per warp, total
-    auto sum_pass = [&](const float *p, const float *q, int k) {
+    for (int i = tid; i < n; i += kVerifyThreads) {
+        int par = a.parents ? a.parents[t0 + i] : i - 1;
+        const int tok = a.tokens[t0 + i];
+        if (par >= i || par < -2) {
+            if (rank == 0) set_error(err, kErrBadIndex);
+            par = -2;
+        }
+        if (i > 0 && par >= 0 && (tok < 0 || tok >= a.V)) {
+            if (rank == 0) set_error(err, kErrBadIndex);
+            par = -2;
+        }
+        s.parent[i] = (int16_t)(i > 0 && par >= 0 ? par : -2);
+        s.token[i] = tok;
+        if (i > 0 && par >= 0) {
+            s.p[i] = a.target[(int64_t)(t0 + par) * a.target_row + tok];
+            s.q[i] = a.draft ? a.draft[(int64_t)(t0 + par) * a.draft_row + tok] : 1.f;
+            s.u[i] = a.u_accept[t0 + i];
+        }
+    }
+    __syncthreads();
+    // This warp's range of the vocabulary, whole vectors long.
+    const int share = ((a.V + cl * kVerifyWarps - 1) / (cl * kVerifyWarps) + 3) / 4 * 4;
+    const int v0 = min(a.V, (rank * kVerifyWarps + warp) * share), v1 = min(a.V, v0 + share);
+    const bool vec = ((reinterpret_cast<uintptr_t>(a.target) | reinterpret_cast<uintptr_t>(a.draft)) & 15) == 0 &&
+                     a.target_row % 4 == 0 && (!a.draft || a.draft_row % 4 == 0);
+    int passes = 0;
+    // Sum of the rest after k rejections (k = 0 without a draft: of p itself).
+    // Leaves the warps' sums in part[], every CTA's in mine[], returns the total.
+    auto sum_pass = [&](const float *p, const float *q, int k) -> int64_t {
         int64_t sum = 0;
-        for (int j = v0 + lane; j < v1; j += 32) sum += rest(p, q, j, k, s);
+        int j = v0 + lane * 4;
+        if (vec) {
+            for (; j + 128 * (kVerifyUnroll - 1) + 4 <= v1; j += 128 * kVerifyUnroll) {
+                float4 x[kVerifyUnroll], y[kVerifyUnroll];
+#pragma unroll
+                for (int e = 0; e < kVerifyUnroll; ++e) {
+                    x[e] = *reinterpret_cast<const float4 *>(p + j + 128 * e);
+                    if (k > 0) y[e] = *reinterpret_cast<const float4 *>(q + j + 128 * e);
+                }
+#pragma unroll
+                for (int e = 0; e < kVerifyUnroll; ++e)
+                    sum += shrink(x[e].x, y[e].x, k, s.W) + shrink(x[e].y, y[e].y, k, s.W) +
+                           shrink(x[e].z, y[e].z, k, s.W) + shrink(x[e].w, y[e].w, k, s.W);
+            }
+        }
+        for (; j < v1; j += 128) {
+            float x[4] = {}, y[4] = {};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (j + e < v1) {
+                    x[e] = p[j + e];
+                    if (k > 0) y[e] = q[j + e];
+                }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum += shrink(x[e], y[e], k, s.W);
+        }
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        __syncthreads();  // earlier readers of part and total are done
         if (lane == 0) s.part[warp] = sum;
         __syncthreads();
-        if (tid == 0) {
-            int64_t t = 0;
-            for (int w = 0; w < kVerifyWarps; ++w) t += s.part[w];
-            s.total = t;
+        int64_t total = 0;
+        for (int w = 0; w < kVerifyWarps; ++w) total += s.part[w];
+        if (cl > 1) {
+            // two buffers: a CTA may be a pass ahead of those that still read
+            const int at = passes++ & 1;
+            if (tid == 0) s.mine[at] = total;
+            cluster_sync();
+            total = 0;
+            for (int r = 0; r < cl; ++r) {
+                const uint32_t addr = peer_addr(&s.mine[at], (uint32_t)r);
+                uint64_t v;
+                asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+                total += (int64_t)v;
+            }
+        } else {
+            passes++;
+            if (tid == 0) s.mine[0] = total;
         }
-        __syncthreads();
+        return total;
     };
     int cur = 0, count = 1, k = 0;  // last accepted node, nodes accepted, rejections at it
-    int64_t total = kOne;
+    int64_t total = kOne;           // W
+    bool summed = false;            // part[] and mine[] hold this node's rest
     const float *p = a.target + (int64_t)t0 * a.target_row;
     const float *q = a.draft ? a.draft + (int64_t)t0 * a.draft_row : nullptr;
-    if (tid == 0 && a.max_path > 0) path[0] = 0;
+    if (writer) path[0] = 0;
     for (int i = 1; i < n && count < a.max_path; ++i) {  // every thread walks alike
-        const int par = a.parents ? a.parents[t0 + i] : i - 1;
-        if (par >= i || par < -2) {
-            if (tid == 0) set_error(err, kErrBadIndex);
-            continue;
-        }
-        if (par != cur) continue;
-        const int tok = a.tokens[t0 + i];
-        if (tok < 0 || tok >= a.V) {
-            if (tid == 0) set_error(err, kErrBadIndex);
-            continue;
-        }
-        const float have = __ll2float_rn(rest(p, q, tok, k, s));
-        const float qt = q ? prob(q[tok]) : 1.f;
-        if (__fmul_rn(__fmul_rn(a.u_accept[t0 + i], qt), __ll2float_rn(total)) < have) {
-            if (tid == 0) path[count] = i;
+        if (s.parent[i] != cur) continue;
+        const int tok = s.token[i];
+        int64_t have = q ? shrink(s.p[i], s.q[i], k, s.W) : weight(s.p[i]);
+        if (!q)
+            for (int e = 0; e < k; ++e)
+                if (s.out[e] == tok) have = 0;
+        if (__fmul_rn(__fmul_rn(s.u[i], prob(s.q[i])), __ll2float_rn(total)) < __ll2float_rn(have)) {
+            if (writer) path[count] = i;
             ++count;
             cur = i;
             k = 0;
             total = kOne;
+            summed = false;
             p = a.target + (int64_t)(t0 + i) * a.target_row;
             if (q) q = a.draft + (int64_t)(t0 + i) * a.draft_row;
-            __syncthreads();  // s.W is rewritten by the next rejection
-        } else {
-            __syncthreads();
-            if (tid == 0) s.W[k] = __ll2float_rn(total), s.out[k] = tok;
-            __syncthreads();
+            continue;
+        }
+        __syncthreads();  // W, out and part[] are no longer read
+        if (q) {
+            if (tid == 0) s.W[k] = __ll2float_rn(total);
             ++k;
-            sum_pass(p, q, k);
-            total = s.total;
+            __syncthreads();
+            total = sum_pass(p, q, k);
+        } else {
+            if (!summed) total = sum_pass(p, nullptr, 0);
+            __syncthreads();
+            total -= have;
+            // the token's weight leaves its warp's and its CTA's sums
+            const int owner = tok / share;
+            if (tid == 0) {
+                s.out[k] = tok;
+                if (owner / kVerifyWarps == rank) s.part[owner % kVerifyWarps] -= have;
+            }
+            ++k;
+            __syncthreads();
         }
+        summed = true;
     }
-    for (int i = count + tid; i < a.max_path; i += kVerifyThreads) path[i] = -1;
-    // the rest's sums (of the last rejection, or of the target itself)
-    if (k == 0) sum_pass(p, q, 0);
-    if (s.total == 0 && k > 0) {
+    if (rank == 0)
+        for (int i = count + tid; i < a.max_path; i += kVerifyThreads) path[i] = -1;
+    if (writer) a.count[b] = count;
+    __syncthreads();
+    if (!summed) total = sum_pass(p, q, 0);
+    if (total == 0 && k > 0) {  // nothing left: the target's own
         k = 0;
-        sum_pass(p, q, 0);
+        __syncthreads();
+        total = sum_pass(p, q, 0);
     }
-    total = s.total;
-    if (tid == 0) a.count[b] = count;
-    if (total == 0) {
-        if (tid == 0) a.token[b] = -1;
-        return;
-    }
-    const int64_t unit = 1ll << 24;
-    const float u = a.u_sample[b];
-    int64_t m = (int64_t)__fmul_rn(u, 0x1p24f);
-    m = m < 0 ? 0 : m >= unit ? unit - 1 : m;
-    const int64_t mark = (total >> 24) * m + (((total & (unit - 1)) * m) >> 24);
-    // the warp whose range holds the mark finds the first token beyond it
-    int64_t before = 0;
-    for (int w = 0; w < warp; ++w) before += s.part[w];
-    if (before <= mark && mark < before + s.part[warp]) {
-        for (int j0 = v0; j0 < v1; j0 += 32) {
-            int64_t run = j0 + lane < v1 ? rest(p, q, j0 + lane, k, s) : 0;
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t up = __shfl_up_sync(0xffffffffu, run, o);
-                if (lane >= o) run += up;
+    if (total > 0) {
+        const int64_t unit = 1ll << 24;
+        int64_t m = (int64_t)__fmul_rn(a.u_sample[b], 0x1p24f);
+        m = m < 0 ? 0 : m >= unit ? unit - 1 : m;
+        const int64_t mark = (total >> 24) * m + (((total & (unit - 1)) * m) >> 24);
+        // where this CTA's range begins in the running sum
+        int64_t mine = 0, before = 0;
+        for (int w = 0; w < kVerifyWarps; ++w) mine += s.part[w];
+        if (cl > 1) {
+            const int at = passes & 1;
+            if (tid == 0) s.mine[at] = mine;
+            cluster_sync();
+            for (int r = 0; r < rank; ++r) {
+                const uint32_t addr = peer_addr(&s.mine[at], (uint32_t)r);
+                uint64_t v;
+                asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+                before += (int64_t)v;
             }
-            const unsigned over = __ballot_sync(0xffffffffu, before + run > mark);
-            if (over) {
-                if (lane == 0) a.token[b] = j0 + __ffs(over) - 1;
-                break;
-            }
-            before += __shfl_sync(0xffffffffu, run, 31);
         }
+        if (before <= mark && mark < before + mine) {  // the token is in this CTA's range
+            int w = 0;
+            while (mark >= before + s.part[w]) before += s.part[w++];
+            const int j0 = min(a.V, (rank * kVerifyWarps + w) * share), j1 = min(a.V, j0 + share);
+            // the first token of warp w's range whose running sum passes the mark
+            for (int jb = j0; jb < j1; jb += kVerifyThreads) {
+                const int j = jb + tid;
+                int64_t run = 0;
+                if (j < j1) {
+                    run = q ? shrink(p[j], k > 0 ? q[j] : 0.f, k, s.W) : weight(p[j]);
+                    if (!q)
+                        for (int e = 0; e < k; ++e)
+                            if (s.out[e] == j) run = 0;
+                }
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int64_t up = __shfl_up_sync(0xffffffffu, run, o);
+                    if (lane >= o) run += up;
+                }
+                if (lane == 31) s.scan[warp] = run;
+                __syncthreads();
+                int64_t all = 0, here = before;
+                for (int e = 0; e < kVerifyWarps; ++e) {
+                    if (e < warp) here += s.scan[e];
+                    all += s.scan[e];
+                }
+                const unsigned over = __ballot_sync(0xffffffffu, here + run > mark);
+                if (here <= mark && over && lane == 0) a.token[b] = jb + warp * 32 + __ffs(over) - 1;
+                before += all;
+                if (before > mark) break;
+                __syncthreads();
+            }
+        }
+    } else if (writer) {
+        a.token[b] = -1;
     }
+    if (cl > 1) cluster_sync();  // a peer may still read this CTA's shared memory
 }
 
 }  // namespace
 
 int tree_verify_launch(const sgmv_tree_verify_args &a, int nsm, int *err, cudaStream_t stream) {
-    return spec_launch(sgmv_verify_kernel, dim3((unsigned)a.B), kVerifyThreads, 0, 1, stream, a, err);
+    // CTAs per sequence: as many as keep two CTAs on every SM busy, each with 2048
+    // tokens of the vocabulary at least
+    int cl = 1;
+    while (cl < kVerifyMaxCluster && (int64_t)a.B * cl * 2 <= 2 * std::max(1, nsm) && a.V >= cl * 2 * 2048) cl *= 2;
+    return spec_launch(sgmv_verify_kernel, dim3((unsigned)a.B * (unsigned)cl), kVerifyThreads, 0, cl, stream, a, err);
 }
 
 }  // namespace sgmv

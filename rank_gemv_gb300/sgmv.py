@@ -112,7 +112,9 @@ _PTR_ARRAYS = [None] + [ctypes.c_void_p * n for n in range(1, 5)]
 
 
 def _stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
+    """Handle of the current stream (without a Stream object, which costs a microsecond)."""
+    index = device.index
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
 
 
 def _meta(t, name):
@@ -377,27 +379,27 @@ _VERIFY_ARGS = struct.Struct("@10P2q4i0q")
 _COMMIT_ARGS = struct.Struct("@6P5q9i0q")
 
 
-def _heads(t, name, dtype, H=None, T=None):
+def _heads(t, name, dtype, shape):
     """(pointer, token stride, head stride) of a [T, H, D] tensor."""
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}")
-    if t.dim() != 3 or (H is not None and t.shape[1] != H) or (T is not None and t.shape[0] != T):
-        raise ValueError(f"{name} has the wrong shape")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}")
     s0, s1, s2 = t.stride()
-    if s2 != 1 and t.shape[2] > 1:
+    if s2 != 1 and shape[2] > 1:
         raise TypeError(f"the last dimension of {name} must be contiguous")
     return t.data_ptr(), s0, s1
 
 
-def _cache(k_cache, v_cache, dtype, layers=False):
+def _cache(k_cache, v_cache, dtype, ndim):
     """Checked strides and shape of a pair of caches [blocks, block_size, Hkv, D]
-    (with layers, [layers, blocks, block_size, Hkv, D] too)."""
+    (ndim 5: [layers, blocks, block_size, Hkv, D])."""
     shape, stride = k_cache.shape, k_cache.stride()
     if v_cache.shape != shape or v_cache.stride() != stride:
         raise ValueError("k_cache and v_cache differ in shape or strides")
     if k_cache.dtype != dtype or v_cache.dtype != dtype:
         raise TypeError(f"the caches must be {dtype}")
-    if len(shape) != 4 and not (layers and len(shape) == 5):
+    if len(shape) != ndim:
         raise ValueError("the caches must be [blocks, block_size, heads, D]")
     if stride[-1] != 1 and shape[-1] > 1:
         raise TypeError("the last dimension of the caches must be contiguous")
@@ -441,37 +443,40 @@ def sgmv_rope(q, k, positions, inv_freq, interleaved=False, scale=1.0, inverse=F
     of the rotated pairs (sgmv_rope_frequencies); inverse=True turns back, the
     gradient of the rotation."""
     first = q if q is not None else k
-    T, _, D = first.shape
-    dtype = first.dtype
-    if inv_freq.dtype != torch.float64 or inv_freq.device.type != "cpu" or not inv_freq.is_contiguous():
+    shape, dtype = first.shape, first.dtype
+    if len(shape) != 3 or dtype not in _DTYPES:
+        raise TypeError("q and k must be [T, heads, D] tensors of f16 or bf16")
+    T, Hq, D = shape
+    if inv_freq.dtype != torch.float64 or inv_freq.is_cuda or not inv_freq.is_contiguous():
         raise TypeError("inv_freq must be a contiguous float64 CPU tensor")
     qi = qo = ki = ko = vi = (0, 0, 0)
-    Hq = Hk = blocks = bs = 0
+    Hk = blocks = bs = kc = vc = 0
     cs = (0, 0, 0, 0)
     if q is not None:
-        Hq = q.shape[1]
-        q_out = q if q_out is None else q_out
-        qi, qo = _heads(q, "q", dtype), _heads(q_out, "q_out", dtype, Hq, T)
-        if q_out.shape[2] != D:
-            raise ValueError("q_out has the wrong shape")
+        qi = _heads(q, "q", dtype, shape)
+        if q_out is None:
+            q_out, qo = q, qi
+        else:
+            qo = _heads(q_out, "q_out", dtype, shape)
+    else:
+        Hq = 0
     if k is not None:
         Hk = k.shape[1]
-        if k_out is None and k_cache is None:
-            k_out = k
-        ki = _heads(k, "k", dtype, None, T)
+        kshape = (T, Hk, D)
+        ki = _heads(k, "k", dtype, kshape)
         if k_out is not None:
-            ko = _heads(k_out, "k_out", dtype, Hk, T)
-        if k.shape[2] != D or (k_out is not None and k_out.shape[2] != D):
-            raise ValueError("q, k and k_out differ in head size")
+            ko = _heads(k_out, "k_out", dtype, kshape)
+        elif k_cache is None:
+            k_out, ko = k, ki
     if k_cache is not None:
-        shape, cs = _cache(k_cache, v_cache, dtype)
-        vi = _heads(v, "v", dtype, Hk, T)
-        blocks, bs = shape[0], shape[1]
-        if shape[2] != Hk or shape[3] != D or v.shape[2] != D:
-            raise ValueError("the caches or v do not fit k")
+        cshape, cs = _cache(k_cache, v_cache, dtype, 4)
+        vi = _heads(v, "v", dtype, kshape)
+        blocks, bs, ch, cd = cshape
+        if ch != Hk or cd != D:
+            raise ValueError("the caches do not fit k")
+        kc, vc = k_cache.data_ptr(), v_cache.data_ptr()
     args = _ROPE_ARGS.pack(
-        qo[0], qi[0], ko[0], ki[0], vi[0], 0 if k_cache is None else k_cache.data_ptr(),
-        0 if v_cache is None else v_cache.data_ptr(), _list(positions, "positions", T),
+        qo[0], qi[0], ko[0], ki[0], vi[0], kc, vc, _list(positions, "positions", T),
         _list(slots, "slots", T), inv_freq.data_ptr(), qo[1], qo[2], qi[1], qi[2], ko[1], ko[2],
         ki[1], ki[2], vi[1], vi[2], cs[0], cs[1], cs[2], T, Hq, Hk, D, inv_freq.numel(), blocks, bs,
         _DTYPES[dtype], interleaved, inverse, scale)
@@ -494,13 +499,15 @@ def sgmv_tree_attention(out, q, k_cache, v_cache, block_table, prefix_lens, tree
     the log-sum-exp.  workspace: uint8 device tensor of
     sgmv_tree_attention_workspace_bytes(T, B, Hq, Hkv, D) bytes, zeroed once
     before its first use (a zeroed one is made when None)."""
-    T, Hq, D = q.shape
+    qshape, dtype = q.shape, q.dtype
+    if len(qshape) != 3 or dtype not in _DTYPES:
+        raise TypeError("q must be a [T, heads, D] tensor of f16 or bf16")
+    T, Hq, D = qshape
     B = prefix_lens.numel()
-    dtype = q.dtype
-    qi, oo = _heads(q, "q", dtype), _heads(out, "out", dtype, Hq, T)
-    shape, cs = _cache(k_cache, v_cache, dtype)
-    if shape[3] != D or out.shape[2] != D:
-        raise ValueError("q, out and the caches differ in head size")
+    qi, oo = _heads(q, "q", dtype, qshape), _heads(out, "out", dtype, qshape)
+    shape, cs = _cache(k_cache, v_cache, dtype, 4)
+    if shape[3] != D:
+        raise ValueError("q and the caches differ in head size")
     if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, Hq) or not lse.is_contiguous()):
         raise TypeError("lse must be a contiguous float32 [T, Hq] tensor")
     table, width, row = _table(block_table, B)
@@ -533,8 +540,9 @@ def sgmv_tree_verify(target, draft, tokens, parents, tree_ptr, u_accept, u_sampl
         if t.dtype != torch.float32 or not t.is_contiguous() or t.numel() != n:
             raise TypeError(f"{name} must be a contiguous float32 tensor of {n} entries")
     if out is None:
-        out = torch.empty(B * (max_path + 2), dtype=torch.int32, device=target.device)
-        out = out[:B], out[2 * B:].view(B, max_path), out[B:2 * B]
+        dev = target.device
+        out = (torch.empty(B, dtype=torch.int32, device=dev), torch.empty(B, max_path, dtype=torch.int32, device=dev),
+               torch.empty(B, dtype=torch.int32, device=dev))
     count, path, token = out
     args = _VERIFY_ARGS.pack(
         target.data_ptr(), 0 if draft is None else draft.data_ptr(), _list(tokens, "tokens", T),
@@ -551,8 +559,11 @@ def sgmv_cache_commit(k_cache, v_cache, block_table, prefix_lens, path, count):
     sgmv_tree_verify returns them) to their final places in the caches
     [blocks, block_size, Hkv, D] or [layers, blocks, block_size, Hkv, D], in place."""
     dtype = k_cache.dtype
-    shape, cs = _cache(k_cache, v_cache, dtype, layers=True)
-    layers, layer_stride = (shape[0], cs[0]) if len(shape) == 5 else (1, 0)
+    if dtype not in _DTYPES:
+        raise TypeError("the caches must be f16 or bf16")
+    ndim = 5 if k_cache.dim() == 5 else 4
+    shape, cs = _cache(k_cache, v_cache, dtype, ndim)
+    layers, layer_stride = (shape[0], cs[0]) if ndim == 5 else (1, 0)
     blocks, bs, Hkv, D = shape[-4:]
     B, width = path.shape
     table, max_blocks, row = _table(block_table, B)
