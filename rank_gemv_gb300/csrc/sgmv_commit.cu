@@ -15,6 +15,7 @@ namespace {
 
 constexpr int kCommitThreads = 256;
 constexpr int kCommitBatch = 8;  // moves whose loads are in flight together
+static_assert(kCommitThreads >= SGMV_TREE_MAX_NODES, "one path entry per thread");
 
 // Grid: x = pieces of all layers of k and v, y = sequence.
 __global__ void __launch_bounds__(kCommitThreads)
@@ -31,8 +32,10 @@ __global__ void __launch_bounds__(kCommitThreads)
                            head * a.cache_head + (piece - head * (a.D / 8)) * 8;
     for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
         const int32_t *path = a.path + (int64_t)b * a.max_path, *table = a.block_table + b * a.table_row;
+        // the first entries of the path are read beside its length
+        const int early = tid < a.max_path ? path[tid] : 0, early_before = tid > 0 && tid < a.max_path ? path[tid - 1] : -1;
         const int64_t prefix = a.prefix_lens[b];
-        int n = a.count[b];
+        const int n = a.count[b];
         const bool report = tid == 0 && blockIdx.x == 0;
         if (n < 0 || n > a.max_path || n > SGMV_TREE_MAX_NODES || prefix < 0) {
             if (report) set_error(err, kErrBadIndex);
@@ -48,8 +51,8 @@ __global__ void __launch_bounds__(kCommitThreads)
         };
         if (tid == 0) s_first_bad = n;
         __syncthreads();
-        for (int d = tid; d < n; d += kCommitThreads) {
-            const int node = path[d], before = d > 0 ? path[d - 1] : -1;
+        if (const int d = tid; d < n) {
+            const int node = early, before = early_before;
             int64_t from = -1, to = -1;
             bool good = node > before && node < SGMV_TREE_MAX_NODES;  // an ascending path
             if (good && node != d) {

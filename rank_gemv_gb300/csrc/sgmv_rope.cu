@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4)
     pdl_trigger();
     const int32_t pos = a.positions[t], slot = a.k_cache ? a.slots[t] : -1;
     const int nqk = (a.Hq + a.Hk) * uph;
-    const int units = nqk + (slot >= 0 ? a.Hk * (D / 8) : 0);
+    const int units = nqk + (a.k_cache ? a.Hk * (D / 8) : 0);
 
     uint4 x[kRopeBatch], y[kRopeBatch];
     auto load = [&](int u, uint4 &x, uint4 &y) {

@@ -67,10 +67,10 @@ int sgmv_rope(const sgmv_rope_args *args, void *stream) {
     // turns per position, modulo one turn, as a fraction of 2^64
     uint64_t turns[kRopeMaxPairs];
     for (int i = 0; i < a.pairs; ++i) {
-        const double f = a.inv_freq[i] / 6.283185307179586476925;
+        const double f = a.inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
         if (!(fabs(f) < 1e15)) return SGMV_ERR_INVALID_ARG;
         const double part = f - floor(f);  // [0, 1]
-        turns[i] = part < 1.0 ? (uint64_t)ldexp(part, 64) : 0;
+        turns[i] = part < 1.0 ? (uint64_t)(part * 0x1p64) : 0;
     }
     int *err = device_error_word();
     if (!err) return SGMV_ERR_CUDA;
