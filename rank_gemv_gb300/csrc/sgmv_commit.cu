@@ -14,11 +14,11 @@ namespace sgmv {
 namespace {
 
 constexpr int kCommitThreads = 256;
-constexpr int kCommitBatch = 8;  // moves whose loads are in flight together
+constexpr int kCommitBatch = 4;  // moves whose loads are in flight together
 static_assert(kCommitThreads >= SGMV_TREE_MAX_NODES, "one path entry per thread");
 
 // Grid: x = pieces of all layers of k and v, y = sequence.
-__global__ void __launch_bounds__(kCommitThreads)
+__global__ void __launch_bounds__(kCommitThreads, 6)
     sgmv_commit_kernel(const __grid_constant__ sgmv_cache_commit_args a, int *err) {
     __shared__ int64_t s_from[SGMV_TREE_MAX_NODES], s_to[SGMV_TREE_MAX_NODES];
     __shared__ int s_first_bad;

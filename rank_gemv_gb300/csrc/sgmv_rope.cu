@@ -1,16 +1,18 @@
 // sgmv_rope.cu -- rotary positions of q and k, and the append of k and v to
 // the paged cache.
 //
-// One CTA per token: the sines and cosines of the token's pairs are computed
-// once, into shared memory, and used by all of its heads.  The angle position *
+// A CTA takes one token after another: the sines and cosines of the token's
+// pairs are computed once, into shared memory, and used by all of its heads.  The angle position *
 // inv_freq is a fraction of a turn in 64-bit fixed point, so the product wraps
 // modulo one turn by itself and keeps 32 bits of the fraction at any position;
 // in fp32 the product alone would lose 2^-24 of the angle, 0.008 rad at
 // position 131072.
 //
-// Bound by memory for many tokens and by the chain position -> sine -> store
-// for few: the first rows are requested before the angles are computed, four
-// 16- or 32-byte pieces per thread at once.
+// A thread keeps one place in the head and steps over the heads, so that its
+// sines and cosines stay in registers.  The rows are requested before the
+// angles are computed, two 16- or 32-byte pieces per thread at once.
+#include <algorithm>
+
 #include "sgmv_device.cuh"
 #include "sgmv_spec.h"
 
@@ -18,7 +20,8 @@ namespace sgmv {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeBatch = 4;  // pieces in flight per thread
+constexpr int kRopeCtas = 4;   // per SM
+constexpr int kRopeBatch = 2;  // pieces of q or k, and of v, in flight per thread
 
 enum RopeMode : int {
     kHalves = 0,       // pairs (i, i + pairs), pairs a multiple of 8: 16-byte vectors
@@ -30,59 +33,78 @@ struct RopeParams {
     sgmv_rope_args a;
     uint64_t turns[kRopeMaxPairs];  // turns per position of every pair, times 2^64
     int32_t rot, uph;               // pieces that rotate, pieces in all, per head
-    uint32_t by_uph, by_vec;        // 2^32 / uph and 2^32 / (D / 8), rounded up; 0: divide by one
 };
 
-// u / n for u * n < 2^32, by = 2^32 / n rounded up (0 for n = 1)
-__device__ __forceinline__ int quotient(int u, uint32_t by) {
-    return by ? (int)__umulhi((uint32_t)u, by) : u;
+// 16-bit pairs of a vector, widened and rounded
+template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// Pieces of a token: q's heads, then k's, then v's (copied, D / 8 per head).
+// Pieces of a head: the rotating ones, then the copied columns.  Piece w of
+// heads h0, h0 + step, ... (q's heads, then k's) is one thread's.
 template <typename T, int MODE>
-__global__ void __launch_bounds__(kRopeThreads, 4)
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
     sgmv_rope_kernel(const __grid_constant__ RopeParams P, int *err) {
     const sgmv_rope_args &a = P.a;
-    __shared__ float s_cos[kRopeMaxPairs], s_sin[kRopeMaxPairs];
-    const int tid = threadIdx.x, pairs = a.pairs, D = a.D, uph = P.uph, rot = P.rot;
-    const int64_t t = blockIdx.x;
+    constexpr int kAngles = MODE == kHalves ? 8 : MODE == kInterleaved ? 4 : 1;  // per piece
+    __shared__ __align__(16) float2 s_angles[2][kRopeMaxPairs];  // cosine, sine
+    const int tid = threadIdx.x, pairs = a.pairs, D = a.D, uph = P.uph;
     pdl_wait();
     pdl_trigger();
-    const int32_t pos = a.positions[t], slot = a.k_cache ? a.slots[t] : -1;
-    const int nqk = (a.Hq + a.Hk) * uph;
-    const int units = nqk + (a.k_cache ? a.Hk * (D / 8) : 0);
+    const int heads = a.Hq + a.Hk, step = kRopeThreads / uph, h0 = tid / uph, w = tid - h0 * uph;
+    const bool turns = w < P.rot && (MODE != kInterleaved || w * 4 < pairs);
+    // first column of the piece, and of its partners
+    const int c = MODE == kScalar ? (w < P.rot ? w : w + pairs)
+                                  : (MODE == kHalves && w >= P.rot ? (w - P.rot) * 8 + 2 * pairs : w * 8);
+    // v: whole vectors, copied
+    const int vph = D / 8, vstep = kRopeThreads / vph, vh0 = tid / vph, vc = (tid - vh0 * vph) * 8;
+    const uint64_t per_position = tid < pairs ? P.turns[tid] : 0;
+    int32_t next_pos = a.positions[blockIdx.x], next_slot = a.k_cache ? a.slots[blockIdx.x] : -1;
+    for (int64_t t = blockIdx.x, buf = 0; t < a.T; t += gridDim.x, buf ^= 1) {
+    const int32_t pos = next_pos, slot = next_slot;
+    if (t + gridDim.x < a.T) {
+        next_pos = a.positions[t + gridDim.x];
+        if (a.k_cache) next_slot = a.slots[t + gridDim.x];
+    }
+    float2 *const s_angle = s_angles[buf];
+    const T *const q = static_cast<const T *>(a.q) + t * a.q_token + c;
+    const T *const k = static_cast<const T *>(a.k) + t * a.k_token + c;
+    const T *const vs = static_cast<const T *>(a.v) + t * a.v_token + vc;
 
-    uint4 x[kRopeBatch], y[kRopeBatch];
-    auto load = [&](int u, uint4 &x, uint4 &y) {
-        if (u >= nqk) {
-            const int h = quotient(u - nqk, P.by_vec), c = (u - nqk - h * (D / 8)) * 8;
-            x = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.v) + t * a.v_token + h * a.v_head + c);
-            return;
-        }
-        const int h = quotient(u, P.by_uph), w = u - h * uph;
-        const T *src = h < a.Hq ? static_cast<const T *>(a.q) + t * a.q_token + h * a.q_head
-                                : static_cast<const T *>(a.k) + t * a.k_token + (h - a.Hq) * a.k_head;
-        if (MODE == kScalar) {
-            x.x = *reinterpret_cast<const uint16_t *>(src + (w < rot ? w : w + pairs));
-            if (w < rot) y.x = *reinterpret_cast<const uint16_t *>(src + w + pairs);
-        } else if (MODE == kHalves && w < rot) {
-            x = *reinterpret_cast<const uint4 *>(src + w * 8);
-            y = *reinterpret_cast<const uint4 *>(src + w * 8 + pairs);
-        } else {
-            x = *reinterpret_cast<const uint4 *>(src + (MODE == kHalves ? (w - rot) * 8 + 2 * pairs : w * 8));
+    uint4 x[kRopeBatch], y[kRopeBatch], z[kRopeBatch];
+    auto load = [&](int hb, int vb) {
+#pragma unroll
+        for (int e = 0; e < kRopeBatch; ++e) {
+            const int h = hb + e * step;
+            if (h0 < step && h < heads) {
+                const T *src = h < a.Hq ? q + h * a.q_head : k + (h - a.Hq) * a.k_head;
+                if (MODE == kScalar) {
+                    x[e].x = *reinterpret_cast<const uint16_t *>(src);
+                    if (turns) y[e].x = *reinterpret_cast<const uint16_t *>(src + pairs);
+                } else {
+                    x[e] = *reinterpret_cast<const uint4 *>(src);
+                    if (MODE == kHalves && turns) y[e] = *reinterpret_cast<const uint4 *>(src + pairs);
+                }
+            }
+            const int v = vb + e * vstep;
+            if (a.k_cache && vh0 < vstep && v < a.Hk)
+                z[e] = *reinterpret_cast<const uint4 *>(vs + v * a.v_head);
         }
     };
-#pragma unroll
-    for (int e = 0; e < kRopeBatch; ++e)
-        if (tid + e * kRopeThreads < units) load(tid + e * kRopeThreads, x[e], y[e]);
+    load(h0, vh0);
 
     if (tid < pairs) {
-        const uint64_t turn = (uint64_t)(int64_t)pos * P.turns[tid];  // modulo one turn
+        const uint64_t turn = (uint64_t)(int64_t)pos * per_position;  // modulo one turn
         const float half_turns = (float)(int32_t)(turn >> 32) * 0x1p-31f;
         float sn, cs;
         sincospif(half_turns, &sn, &cs);
-        s_cos[tid] = cs * a.scale;
-        s_sin[tid] = (a.inverse ? -sn : sn) * a.scale;
+        s_angle[tid] = make_float2(cs * a.scale, (a.inverse ? -sn : sn) * a.scale);
     }
     int64_t slot_off = -1;
     if (slot >= 0 && (int64_t)slot < (int64_t)a.num_blocks * a.block_size)
@@ -90,81 +112,85 @@ __global__ void __launch_bounds__(kRopeThreads, 4)
     else if (slot != -1 && tid == 0)
         set_error(err, kErrBadIndex);
     __syncthreads();
-
-    auto store = [&](int u, uint4 x, uint4 y) {
-        if (u >= nqk) {
-            const int h = quotient(u - nqk, P.by_vec), c = (u - nqk - h * (D / 8)) * 8;
-            if (slot_off >= 0)
-                *reinterpret_cast<uint4 *>(static_cast<T *>(a.v_cache) + slot_off + h * a.cache_head + c) = x;
-            return;
+    // this piece's angles; pairs that do not turn (an interleaved vector that
+    // the last pair ends inside of) keep their columns by cosine 1, sine 0
+    float2 r[kAngles];
+    if (turns) {
+#pragma unroll
+        for (int e = 0; e < kAngles; ++e) {
+            const int i = w * kAngles + e;
+            r[e] = MODE != kInterleaved || i < pairs ? s_angle[i] : make_float2(1.f, 0.f);
         }
-        int h = quotient(u, P.by_uph);
-        const int w = u - h * uph;
-        T *dst, *dst2 = nullptr;
-        if (h < a.Hq) {
-            dst = static_cast<T *>(a.q_out) + t * a.q_out_token + h * a.q_out_head;
-        } else {
-            h -= a.Hq;
-            dst = a.k_out ? static_cast<T *>(a.k_out) + t * a.k_out_token + h * a.k_out_head : nullptr;
-            if (slot_off >= 0) dst2 = static_cast<T *>(a.k_cache) + slot_off + h * a.cache_head;
-        }
+    }
+    T *const qo = static_cast<T *>(a.q_out) + t * a.q_out_token + c;
+    T *const ko = a.k_out ? static_cast<T *>(a.k_out) + t * a.k_out_token + c : nullptr;
+    T *const kc = slot_off >= 0 ? static_cast<T *>(a.k_cache) + slot_off + c : nullptr;
+    T *const vo = slot_off >= 0 ? static_cast<T *>(a.v_cache) + slot_off + vc : nullptr;
+    auto put = [&](T *dst, const uint4 &x, const uint4 &y) {
         if (MODE == kScalar) {
-            const T xs = *reinterpret_cast<const T *>(&x.x), ys = *reinterpret_cast<const T *>(&y.x);
-            if (w < rot) {
-                const float p = to_f<T>(xs), q = to_f<T>(ys);
-                const T r = from_f<T>(p * s_cos[w] - q * s_sin[w]), s = from_f<T>(p * s_sin[w] + q * s_cos[w]);
-                if (dst) dst[w] = r, dst[w + pairs] = s;
-                if (dst2) dst2[w] = r, dst2[w + pairs] = s;
-            } else {
-                if (dst) dst[w + pairs] = xs;
-                if (dst2) dst2[w + pairs] = xs;
-            }
-            return;
-        }
-        int c = w * 8;
-        if (MODE == kHalves && w < rot) {
-            T *xs = reinterpret_cast<T *>(&x), *ys = reinterpret_cast<T *>(&y);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float p = to_f<T>(xs[e]), q = to_f<T>(ys[e]);
-                xs[e] = from_f<T>(p * s_cos[c + e] - q * s_sin[c + e]);
-                ys[e] = from_f<T>(p * s_sin[c + e] + q * s_cos[c + e]);
-            }
-            if (dst) *reinterpret_cast<uint4 *>(dst + c + pairs) = y;
-            if (dst2) *reinterpret_cast<uint4 *>(dst2 + c + pairs) = y;
-        } else if (MODE == kHalves) {
-            c = (w - rot) * 8 + 2 * pairs;
+            *reinterpret_cast<uint16_t *>(dst) = (uint16_t)x.x;
+            if (turns) *reinterpret_cast<uint16_t *>(dst + pairs) = (uint16_t)y.x;
         } else {
-            T *xs = reinterpret_cast<T *>(&x);
+            *reinterpret_cast<uint4 *>(dst) = x;
+            if (MODE == kHalves && turns) *reinterpret_cast<uint4 *>(dst + pairs) = y;
+        }
+    };
+    auto store = [&](int hb, int vb) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = w * 4 + e;
-                if (i < pairs) {
-                    const float p = to_f<T>(xs[2 * e]), q = to_f<T>(xs[2 * e + 1]);
-                    xs[2 * e] = from_f<T>(p * s_cos[i] - q * s_sin[i]);
-                    xs[2 * e + 1] = from_f<T>(p * s_sin[i] + q * s_cos[i]);
+        for (int e = 0; e < kRopeBatch; ++e) {
+            const int h = hb + e * step;
+            if (h0 < step && h < heads) {
+                if (turns) {
+                    uint32_t *const xs = reinterpret_cast<uint32_t *>(&x[e]), *const ys = reinterpret_cast<uint32_t *>(&y[e]);
+                    if (MODE == kScalar) {
+                        const float p = to_f<T>(*reinterpret_cast<const T *>(xs)), q = to_f<T>(*reinterpret_cast<const T *>(ys));
+                        xs[0] = pack2<T>(p * r[0].x - q * r[0].y, 0.f);
+                        ys[0] = pack2<T>(p * r[0].y + q * r[0].x, 0.f);
+                    } else if (MODE == kInterleaved) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float p, q;
+                            unpack2<T>(xs[i], p, q);
+                            xs[i] = pack2<T>(p * r[i % kAngles].x - q * r[i % kAngles].y,
+                                             p * r[i % kAngles].y + q * r[i % kAngles].x);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 r0 = r[2 * i % kAngles], r1 = r[(2 * i + 1) % kAngles];
+                            float p0, p1, q0, q1;
+                            unpack2<T>(xs[i], p0, p1);
+                            unpack2<T>(ys[i], q0, q1);
+                            xs[i] = pack2<T>(p0 * r0.x - q0 * r0.y, p1 * r1.x - q1 * r1.y);
+                            ys[i] = pack2<T>(p0 * r0.y + q0 * r0.x, p1 * r1.y + q1 * r1.x);
+                        }
+                    }
+                }
+                if (h < a.Hq) {
+                    put(qo + h * a.q_out_head, x[e], y[e]);
+                } else {
+                    if (ko) put(ko + (h - a.Hq) * a.k_out_head, x[e], y[e]);
+                    if (kc) put(kc + (h - a.Hq) * a.cache_head, x[e], y[e]);
                 }
             }
+            const int v = vb + e * vstep;
+            if (vo && vh0 < vstep && v < a.Hk) *reinterpret_cast<uint4 *>(vo + v * a.cache_head) = z[e];
         }
-        if (dst) *reinterpret_cast<uint4 *>(dst + c) = x;
-        if (dst2) *reinterpret_cast<uint4 *>(dst2 + c) = x;
     };
-    for (int u0 = 0;;) {
-#pragma unroll
-        for (int e = 0; e < kRopeBatch; ++e)
-            if (u0 + tid + e * kRopeThreads < units) store(u0 + tid + e * kRopeThreads, x[e], y[e]);
-        u0 += kRopeBatch * kRopeThreads;
-        if (u0 >= units) break;
-#pragma unroll
-        for (int e = 0; e < kRopeBatch; ++e)
-            if (u0 + tid + e * kRopeThreads < units) load(u0 + tid + e * kRopeThreads, x[e], y[e]);
+    for (int hb = h0, vb = vh0;;) {
+        store(hb, vb);
+        hb += kRopeBatch * step;
+        vb += kRopeBatch * vstep;
+        if (hb >= heads && vb >= a.Hk) break;
+        load(hb, vb);
     }
+    }  // the next token's angles go to the other buffer: one barrier per token
 }
 
-uint32_t inverse_of(int n) { return n > 1 ? (uint32_t)(((1ull << 32) + n - 1) / n) : 0; }
-
-template <typename T> int launch(const RopeParams &p, int mode, int *err, cudaStream_t stream) {
-    const dim3 grid((unsigned)p.a.T);
+template <typename T> int launch(const RopeParams &p, int mode, int nsm, int *err, cudaStream_t stream) {
+    // as many CTAs as fit at once (8192 rows of 48 heads: a CTA per row, with its
+    // set-up each time, took 44 us)
+    const dim3 grid((unsigned)std::min(p.a.T, kRopeCtas * std::max(1, nsm)));
     switch (mode) {
         case kHalves: return spec_launch(sgmv_rope_kernel<T, kHalves>, grid, kRopeThreads, 0, 1, stream, p, err);
         case kInterleaved:
@@ -175,16 +201,15 @@ template <typename T> int launch(const RopeParams &p, int mode, int *err, cudaSt
 
 }  // namespace
 
-int rope_launch(const sgmv_rope_args &a, const uint64_t *turns, int *err, cudaStream_t stream) {
+int rope_launch(const sgmv_rope_args &a, const uint64_t *turns, int nsm, int *err, cudaStream_t stream) {
     RopeParams p;
     p.a = a;
     for (int i = 0; i < a.pairs; ++i) p.turns[i] = turns[i];
     const int mode = a.interleaved ? kInterleaved : a.pairs % 8 == 0 ? kHalves : kScalar, rest = a.D - 2 * a.pairs;
     p.rot = mode == kHalves ? a.pairs / 8 : mode == kInterleaved ? a.D / 8 : a.pairs;
     p.uph = mode == kHalves ? p.rot + rest / 8 : mode == kInterleaved ? p.rot : p.rot + rest;
-    p.by_uph = inverse_of(p.uph);
-    p.by_vec = inverse_of(a.D / 8);
-    return a.dtype == SGMV_F16 ? launch<__half>(p, mode, err, stream) : launch<__nv_bfloat16>(p, mode, err, stream);
+    return a.dtype == SGMV_F16 ? launch<__half>(p, mode, nsm, err, stream)
+                                 : launch<__nv_bfloat16>(p, mode, nsm, err, stream);
 }
 
 }  // namespace sgmv

@@ -15,7 +15,8 @@ constexpr int kRopeMaxPairs = kSpecMaxD / 2;
 
 // Every launcher returns a cudaError_t value.
 // turns[i]: turns per position of pair i, modulo one, times 2^64.
-int rope_launch(const sgmv_rope_args &a, const uint64_t *turns, int *err, cudaStream_t stream);
+int rope_launch(const sgmv_rope_args &a, const uint64_t *turns, int nsm, int *err,
+                cudaStream_t stream);
 int tree_attention_launch(const sgmv_tree_attention_args &a, int nsm, int *err,
                           cudaStream_t stream);
 // The tensor-core form, for D <= kMmaMaxD.

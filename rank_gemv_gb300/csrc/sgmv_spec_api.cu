@@ -74,7 +74,7 @@ int sgmv_rope(const sgmv_rope_args *args, void *stream) {
     }
     int *err = device_error_word();
     if (!err) return SGMV_ERR_CUDA;
-    return finish("rotary kernel", rope_launch(a, turns, err, static_cast<cudaStream_t>(stream)), 1);
+    return finish("rotary kernel", rope_launch(a, turns, device_sms(), err, static_cast<cudaStream_t>(stream)), 1);
 }
 
 int sgmv_rope_frequencies(double *inv_freq, int32_t pairs, double base, double factor,
