@@ -38,6 +38,7 @@
 // the rows that do see them.
 #include <math.h>
 
+#include <algorithm>
 #include <numeric>
 #include <type_traits>
 
@@ -57,8 +58,8 @@ constexpr int kSegs = 4;                 // segments known ahead
 constexpr float kUnset = -3e38f;         // ref of a row that has seen nothing
 constexpr float kBias = 7.f;             // weights are 2^(kBias + score - ref) ...
 constexpr float kSlack = 8.f;            // ... <= 2^(kBias + kSlack), finite in f16
-constexpr int kMaxCtas = 152;
-constexpr int kSeqTable = 512;           // entries of the table that finds a tile's sequence
+constexpr int kMaxSms = 152;
+constexpr int kSeqTable = 128;           // entries of the table that finds a tile's sequence
 constexpr int kMaxParts = 64;            // parts of an item (about)
 
 template <int RT> struct Shape {
@@ -66,13 +67,19 @@ template <int RT> struct Shape {
     static constexpr int kRows = RT / kGroups;            // rows per warpgroup
     static constexpr int kSoft = 128 * kGroups;           // softmax threads
     static constexpr int kThreads = kSoft + 64 + kLoaders;
-    static constexpr int kQ = RT > 64 ? 1 : 2;            // Q buffers
-    static constexpr int kStages = RT > 64 ? 4 : 5;
+    // Two CTAs per SM where they fit: one's sums and segment changes hide behind
+    // the other's loads (128 decode rows, XXX us with one, YYY with two).
+    static constexpr int kPerSm = RT <= 16 ? 2 : 1;
+    static constexpr int kQ = RT > 64 || kPerSm > 1 ? 1 : 2;  // Q buffers
+    static constexpr int kStages = kPerSm > 1 ? 3 : RT > 64 ? 4 : 5;
     static constexpr int kWords = RT < 32 ? 1 : RT / 32;  // words of one bit per row
     static constexpr uint32_t kQBytes = RT * 256u;
-    static constexpr uint32_t kPBytes = (RT > 64 ? 2 : 1) * kHalf;
+    // A token's row of P: 64 columns of 128-byte swizzle, or 16 of 32-byte swizzle
+    static constexpr uint32_t kPRow = RT <= 16 ? 32 : 128;
+    static constexpr uint32_t kPBytes = (RT > 64 ? 2 : 1) * kTok * kPRow;
     // shares claimed at run time, per CTA: their least tiles, and how many of them
-    static constexpr int kLeast = RT / 8, kClaims = RT <= 32 ? 8 : RT <= 64 ? 4 : 2;
+    static constexpr int kLeast = RT / 8, kClaims = RT <= 16 ? 4 : RT <= 32 ? 8 : RT <= 64 ? 4 : 2;
+    static constexpr int kMaxCtas = kMaxSms * kPerSm;
     static constexpr int kShares = kMaxCtas * (1 + kClaims);
     static constexpr uint32_t kTmem = RT <= 16 ? 64 : RT <= 32 ? 128 : RT <= 64 ? 256 : 512;
     // dynamic shared memory
@@ -311,7 +318,7 @@ __device__ __forceinline__ int2 row_place(const MmaParams &P, int t0, int h, int
 }
 
 template <typename T, int RT>
-__global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
+__global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
     sgmv_tree_mma_kernel(const __grid_constant__ MmaParams P) {
     using S = Shape<RT>;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -319,7 +326,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
     extern __shared__ __align__(1024) uint8_t dsm[];
     __shared__ __align__(8) uint64_t full[S::kStages], empty[S::kStages], q_full[S::kQ], q_empty[S::kQ];
     __shared__ __align__(8) uint64_t seg_full[kSegs], seg_empty[kSegs], aux_full[kSegs];
-    __shared__ __align__(8) uint64_t p_full, tab_ready, drained;
+    __shared__ __align__(8) uint64_t p_full, pv_done, tab_ready, drained;
     __shared__ uint32_t s_tmem;
     __shared__ int s_lost, s_poison, s_longest, s_known, s_loading;
     __shared__ int64_t s_sum[32];
@@ -343,6 +350,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
                 mbar_init(&aux_full[i], 32);
             }
             mbar_init(&p_full, S::kSoft);
+            mbar_init(&pv_done, 1);
             mbar_init(&tab_ready, kLoaders);
             mbar_init(&drained, 1);
             mbar_init_fence();
@@ -712,7 +720,10 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
         // descriptors of the first stage and buffers; offsets add to them (bytes / 16)
         const uint64_t k_desc = sw128_desc(ring, 16, 1024), v_desc = sw128_desc(ring, kHalf, 1024);
         const uint64_t q_desc = sw128_desc(ring + S::kOffQ, 16, 1024);
-        const uint64_t p_desc = sw128_desc(ring + S::kOffP, kHalf, 1024);
+        // 32-byte swizzle is layout 6, its 8-token groups are 256 bytes apart
+        const uint64_t p_desc = S::kPRow == 128 ? sw128_desc(ring + S::kOffP, kHalf, 1024)
+                                                : sw128_desc(ring + S::kOffP, kHalf, 256) ^ (4ull << 61);
+        constexpr uint32_t p_step = 16 * S::kPRow >> 4;
         const bool wide = D > 64;
         int k_st = 0, v_st = 1 % S::kStages;  // ring stages of the next K and V
         uint32_t k_ph = 0, v_ph = 0;
@@ -772,8 +783,9 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
                 const uint64_t vd = v_desc + (uint32_t)v_st * (kStage >> 4);
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                    mma_on(on, tmem + 2 * RT, vd + kk * 128, p_desc + kk * 128, idesc_o, kk ? 1u : (uint32_t)t);
-                commit_on(on, &empty[v_st]);  // also tells the softmax that P has been read
+                    mma_on(on, tmem + 2 * RT, vd + kk * 128, p_desc + kk * p_step, idesc_o, kk ? 1u : (uint32_t)t);
+                commit_on(on, &empty[v_st]);
+                commit_on(on, &pv_done);
                 skip(v_st, v_ph);
             }
             if (lane == 0) mbar_arrive(&seg_empty[i % kSegs]);
@@ -787,17 +799,24 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
         const int wg = warp >> 2, tok = tid & 127, r0 = wg * S::kRows, d = tok;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t t_s = tmem + lanes + (uint32_t)r0, t_o = tmem + lanes + 2 * RT + (uint32_t)r0;
-        uint8_t *const prow = sm + S::kOffP + (uint32_t)(wg >> 1) * kHalf;
-        const int pchunk = (wg & 1) * 4;
+        // where this thread's 16-byte pieces of P go
+        auto p_at = [&](int q) {
+            return sm + S::kOffP + (S::kPRow == 128 ? (uint32_t)(wg >> 1) * kHalf + sw128_offset(tok, (wg & 1) * 4 + q)
+                                                    : (uint32_t)(tok * 32 + ((q ^ (tok >> 2 & 1)) << 4)));
+        };
         const float c = P.c;
         float l[S::kRows];
         volatile Segment &cur = s_cur;
         int g = 0;              // tile
         // K of tile g is the ring's operand 2g, V is 2g + 1.  The commit that
-        // frees an operand's stage is the softmax's signal that the product is
-        // done; it waits for each before the stage can be freed again.
-        auto done = [&](int pos) {
-            await(&empty[pos % S::kStages], (uint32_t)(pos / S::kStages) & 1, lost);
+        // frees K's stage is the signal that the scores are there: the stage can
+        // be freed again only after this tile's P is complete.
+        auto scores_done = [&](int g) {
+            await(&empty[2 * g % S::kStages], (uint32_t)(2 * g / S::kStages) & 1, lost);
+            tc_fence_after();
+        };
+        auto pv_finished = [&](int g) {
+            await(&pv_done, (uint32_t)g & 1, lost);
             tc_fence_after();
         };
         for (int seg = 0;; ++seg) {
@@ -817,7 +836,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
 #pragma unroll
             for (int r = 0; r < S::kRows; ++r) l[r] = 0.f;
             for (int tile = first; tile < end; ++tile, ++g) {
-                done(2 * g);
+                scores_done(g);
                 if (!aux && (tile + 1) * P.tok > prefix) {
                     await(&aux_full[seg % kSegs], (uint32_t)(seg / kSegs) & 1, lost);
                     aux = true;
@@ -883,7 +902,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
 #pragma unroll
                     for (int r = 0; r < S::kRows; ++r) l[r] *= s_fac[r0 + r];
                     if (tile != first) {
-                        done(2 * g - 1);
+                        pv_finished(g - 1);
                         tmem_load(t_o, s);
 #pragma unroll
                         for (int i = 0; i < S::kRows; ++i) s[i] *= s_fac[r0 + i];
@@ -899,10 +918,10 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
                     p[i + 1] = from_f<T>(s[i + 1]);
                 }
                 // the previous tile's P has been read
-                if (g > 0) done(2 * g - 1);
+                if (g > 0) pv_finished(g - 1);
 #pragma unroll
                 for (int q = 0; q < S::kRows / 8; ++q)
-                    sts128(prow + sw128_offset(tok, pchunk + q), reinterpret_cast<const uint4 *>(p)[q]);
+                    sts128(p_at(q), reinterpret_cast<const uint4 *>(p)[q]);
                 if (tree) {
                     // non-finite v of tree nodes: out of the tile, noted; what TMA
                     // brought from the last page past the end: zeroed
@@ -966,7 +985,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, 1)
                 }
                 s_ref[r] = -kUnset;
             }
-            done(2 * g - 1);
+            pv_finished(g - 1);
             group_bar(wg);
             {
                 const bool poison = *(volatile int *)&s_poison == seg, ok = !*lost;
@@ -1063,7 +1082,7 @@ __global__ void __launch_bounds__(kJoinThreads) sgmv_tree_join_kernel(const __gr
 
 template <typename T, int RT>
 int launch(const MmaParams &p, int ctas, cudaStream_t stream) {
-    static_assert(Shape<RT>::kBytes <= 227 * 1024 - 8192, "shared memory");
+    static_assert((Shape<RT>::kBytes + 4096) * Shape<RT>::kPerSm <= 227 * 1024, "shared memory");
     const cudaError_t e = cudaFuncSetAttribute(sgmv_tree_mma_kernel<T, RT>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)Shape<RT>::kBytes);
@@ -1071,7 +1090,7 @@ int launch(const MmaParams &p, int ctas, cudaStream_t stream) {
     const int r = spec_launch(sgmv_tree_mma_kernel<T, RT>, dim3((unsigned)ctas), Shape<RT>::kThreads,
                               Shape<RT>::kBytes, 1, stream, p);
     if (r != (int)cudaSuccess) return r;
-    return spec_launch(sgmv_tree_join_kernel<T, RT>, dim3((unsigned)(8 * ctas)), kJoinThreads, 0, 1, stream, p);
+    return spec_launch(sgmv_tree_join_kernel<T, RT>, dim3(8 * kMaxSms), kJoinThreads, 0, 1, stream, p);
 }
 
 // Rows per tile: what a sequence of average length fills.
@@ -1081,6 +1100,8 @@ int row_tile(int32_t T, int32_t B, int32_t group) {
 }
 
 constexpr size_t kHeadBytes = 256;
+
+int max_ctas(int rt) { return rt == 16 ? Shape<16>::kMaxCtas : kMaxSms; }
 
 size_t shares_of(int rt) {
     return rt == 16   ? Shape<16>::kShares
@@ -1098,7 +1119,7 @@ size_t tree_mma_workspace(int32_t T, int32_t B, int32_t group) {
 
 int tree_mma_launch(const sgmv_tree_attention_args &a, int nsm, int *err, cudaStream_t stream) {
     const int group = a.Hq / a.Hkv, rt = row_tile(a.T, a.B, group);
-    const int ctas = nsm < 1 ? 1 : nsm < kMaxCtas ? nsm : kMaxCtas;
+    const int ctas = std::min(std::max(1, nsm) * (max_ctas(rt) / kMaxSms), max_ctas(rt));
     MmaParams p;
     p.a = a;
     p.c = a.scale * 1.4426950408889634f;
