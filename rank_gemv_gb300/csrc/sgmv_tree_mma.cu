@@ -253,13 +253,16 @@ __device__ __forceinline__ bool group_any(int g, bool v) {
         : "memory");
     return r != 0;
 }
+// Tensor memory, 32 lanes x N columns; the whole warp, brought together first.
 template <int N> __device__ __forceinline__ void tmem_load(uint32_t addr, float (&v)[N]) {
+    __syncwarp();
     if constexpr (N == 32)
         tmem_ld32(addr, v);
     else
         tmem_ld16(addr, v);
 }
 template <int N> __device__ __forceinline__ void tmem_store(uint32_t addr, const float (&v)[N]) {
+    __syncwarp();
 #pragma unroll
     for (int i = 0; i < N; i += 16)
         asm volatile(
@@ -347,9 +350,9 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
             for (int i = 0; i < kSegs; ++i) {
                 mbar_init(&seg_full[i], 1);
                 mbar_init(&seg_empty[i], 2 + kLoaders / 32);  // MMA, softmax, loaders
-                mbar_init(&aux_full[i], 32);
+                mbar_init(&aux_full[i], 1);
             }
-            mbar_init(&p_full, S::kSoft);
+            mbar_init(&p_full, S::kSoft / 32);
             mbar_init(&pv_done, 1);
             mbar_init(&tab_ready, kLoaders);
             mbar_init(&drained, 1);
@@ -532,21 +535,25 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
             }
             __syncwarp();
             w += end - tile;
-            // the row tile's queries
+            // the rows' places, then their queries
             const int qb = i % S::kQ, R = min(RT, q.n * group - rt * RT);
-            if (i >= S::kQ) await(&q_empty[qb], (uint32_t)(i / S::kQ - 1) & 1, lost);
-            uint8_t *const qs = sm + S::kOffQ + (uint32_t)qb * S::kQBytes;
-            for (int e = lane; e < RT * cpr; e += 32) {
-                const int m = e / cpr, c = e - m * cpr, r = rt * RT + m, node = r / group;
-                const T *src = static_cast<const T *>(a.q);
-                if (m < R)
-                    src += (int64_t)(q.t0 + node) * a.q_token + (int64_t)(h * group + r - node * group) * a.q_head + c * 8;
-                cp_async16(qs + (uint32_t)(c >> 3) * (RT * 128u) + sw128_offset(m, c & 7), src, m < R ? 16u : 0u);
-            }
-            cp_async_arrive(&q_full[qb]);
-            // the rows' places
             int2 *const place = reinterpret_cast<int2 *>(sm + S::kOffRow) + (i % kSegs) * RT;
             for (int r = lane; r < R; r += 32) place[r] = row_place(P, q.t0, h, rt * RT + r);
+            __syncwarp();
+            if (i >= S::kQ) await(&q_empty[qb], (uint32_t)(i / S::kQ - 1) & 1, lost);
+            uint8_t *const qs = sm + S::kOffQ + (uint32_t)qb * S::kQBytes;
+            for (int m = lane / cpr, c = lane % cpr; m < RT;) {
+                const T *src = static_cast<const T *>(a.q);
+                if (m < R) {
+                    const int2 at = place[m];
+                    src += (int64_t)(at.x < 0 ? ~at.x : at.x) * a.q_token + (int64_t)at.y * a.q_head + c * 8;
+                }
+                cp_async16(qs + (uint32_t)(c >> 3) * (RT * 128u) + sw128_offset(m, c & 7), src, m < R ? 16u : 0u);
+                m += 32 / cpr;
+                c += 32 % cpr;
+                if (c >= cpr) c -= cpr, ++m;
+            }
+            cp_async_arrive(&q_full[qb]);
             if (build) {
                 // see[j]: the rows that see tree node j.  Every node of this row
                 // tile marks itself and its ancestors with its rows' bits.
@@ -576,7 +583,8 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
                 __syncwarp();
             }
             if (tree) see_user[see] = i;
-            mbar_arrive(&aux_full[i % kSegs]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&aux_full[i % kSegs]);
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp > kWalkWarp) {
@@ -715,7 +723,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
     } else if (warp == kMmaWarp) {
         // ---- MMA issuer ------------------------------------------------------
         const uint32_t idesc_s = idesc_f16(kBf16, kTok, RT) & ~(1u << 16);   // both K-major
-        const uint32_t idesc_o = idesc_f16(kBf16, kTok, RT) | (1u << 15);    // both MN-major
+        const uint32_t idesc_o = idesc_f16(kBf16, kTok, RT) | (1u << 15);  // both MN-major
         const uint32_t ring = smem_addr(sm), on = elect();
         // descriptors of the first stage and buffers; offsets add to them (bytes / 16)
         const uint64_t k_desc = sw128_desc(ring, 16, 1024), v_desc = sw128_desc(ring, kHalf, 1024);
@@ -775,7 +783,9 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
             const int tiles = s.end - s.tile;
             if (s.end == 0) break;
             for (int t = 0; t < tiles; ++t, ++g) {
-                scores(g + 1);  // nothing at the end
+                // A tile ahead; but with one Q buffer the next segment's first scores
+                // wait for its Q, and must not hold up this segment's last product.
+                if (S::kQ > 1 || t + 1 < tiles) scores(g + 1);  // nothing at the end
                 await(&full[v_st], v_ph, lost);
                 await(&p_full, (uint32_t)g & 1, lost);
                 if (!P.box) fence_proxy_async();
@@ -787,6 +797,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
                 commit_on(on, &empty[v_st]);
                 commit_on(on, &pv_done);
                 skip(v_st, v_ph);
+                if (S::kQ == 1 && t + 1 == tiles) scores(g + 1);
             }
             if (lane == 0) mbar_arrive(&seg_empty[i % kSegs]);
             __syncwarp();
@@ -947,14 +958,15 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
                             if (bad16<T>(x[q] >> 16)) any = true, x[q] &= 0xffffu;
                         }
                         if (any) {
-                            sts128(at, u);
                             s_poison = seg;
+                            sts128(at, u);
                         }
                     }
                 }
                 fence_proxy_async();
                 tc_fence_before();
-                mbar_arrive(&p_full);
+                __syncwarp();  // one arrival per warp: a warp's own 32 would be served one by one
+                if (lane == 0) mbar_arrive(&p_full);
             }
             if (!aux) await(&aux_full[seg % kSegs], (uint32_t)(seg / kSegs) & 1, lost);
 
