@@ -451,10 +451,9 @@ int sgmv_rope_frequencies(double *inv_freq, int32_t pairs, double base, double f
  *     exp(scale * score); block_table int32 [B][max_blocks], row stride
  *     table_row; prefix_lens int32 [B]; tree_ptr int32 [B+1]
  *   scale: multiplied onto the scores (usually D^-1/2)
- *   workspace: sgmv_tree_attention_workspace_bytes() bytes, 256-byte aligned.
- *     It must be all zero before its first use; every call leaves it ready
- *     for the next (but for one that reports SGMV_ERR_TIMEOUT: zero it
- *     again).  Calls that run at the same time need separate ones.
+ *   workspace: sgmv_tree_attention_workspace_bytes() bytes, 256-byte aligned;
+ *     what it holds does not matter.  Calls that run at the same time need
+ *     separate ones.
  * Hq a multiple of Hkv, D a multiple of 8 up to 256.  Scores, softmax and
  * sums are fp32; the weights p are rounded to the inputs' type for the
  * tensor cores, the output once.  out must not overlap the inputs.  Rows in

@@ -17,17 +17,18 @@
 // ordinary tile needs one vote and no reduction over tokens.
 //
 // Decomposition: the (sequence, head, row tile) items, each of ceil(length /
-// 128) token tiles, form one line of work for a persistent grid of one CTA
-// per SM.  A CTA takes its share of the line's first part, then claims small
-// shares of the rest as it finishes.  A share that covers an item writes its
-// output; items cut across shares leave unnormalised O, sums and references in
-// the workspace, and a second, small kernel joins them, in share order (so
-// results do not depend on who claimed what).  Joined by whichever CTA finished last,
-// behind a fence and a counter, each join cost 15 us of that CTA's time: its
-// chain of loads queued behind the stream of K and V.
+// 128) token tiles, form one line of work that is cut into equal shares, one
+// per CTA of a grid that fills the GPU once.  A share that covers an item
+// writes its output; items cut across shares leave unnormalised O, sums and
+// references in the workspace, and a second, small kernel joins them, in share
+// order.  (Joined by whichever CTA finished last, behind a fence and a counter, each join
+// took 15 us: its chain of loads queued behind the stream of K and V.  Claiming the
+// last quarter of the line in small shares at run time balanced the SMs' unequal
+// bandwidth, but its parts and joins cost more than it won: 188, 287 and 67 us against
+// 182, 275 and 61 on 32 trees, 64 heads on 8, and 128 decode rows.)
 //
 // Warps: 4, 4, 8 or 16 for the softmax (32 rows each four); one that issues the
-// MMAs, a score product ahead of the softmax; one that walks the line, claims,
+// MMAs, a score product ahead of the softmax; one that walks the line,
 // brings Q in and says which rows see which tree nodes; two that bring K and V
 // into a ring of 32 KB stages, through the block table: by TMA, or, for pages
 // that are no multiple of 8 tokens, with cp.async, 16 bytes per lane.
@@ -59,7 +60,7 @@ constexpr float kUnset = -3e38f;         // ref of a row that has seen nothing
 constexpr float kBias = 7.f;             // weights are 2^(kBias + score - ref) ...
 constexpr float kSlack = 8.f;            // ... <= 2^(kBias + kSlack), finite in f16
 constexpr int kMaxSms = 152;
-constexpr int kSeqTable = 128;           // entries of the table that finds a tile's sequence
+constexpr int kSeqTable = 64;            // entries of the table that finds a tile's sequence
 constexpr int kMaxParts = 64;            // parts of an item (about)
 
 template <int RT> struct Shape {
@@ -68,7 +69,8 @@ template <int RT> struct Shape {
     static constexpr int kSoft = 128 * kGroups;           // softmax threads
     static constexpr int kThreads = kSoft + 64 + kLoaders;
     // Two CTAs per SM where they fit: one's sums and segment changes hide behind
-    // the other's loads (128 decode rows, XXX us with one, YYY with two).
+    // the other's loads (128 decode rows 76 us
+    // with one, 67 with two).
     static constexpr int kPerSm = RT <= 16 ? 2 : 1;
     static constexpr int kQ = RT > 64 || kPerSm > 1 ? 1 : 2;  // Q buffers
     static constexpr int kStages = kPerSm > 1 ? 3 : RT > 64 ? 4 : 5;
@@ -77,10 +79,6 @@ template <int RT> struct Shape {
     // A token's row of P: 64 columns of 128-byte swizzle, or 16 of 32-byte swizzle
     static constexpr uint32_t kPRow = RT <= 16 ? 32 : 128;
     static constexpr uint32_t kPBytes = (RT > 64 ? 2 : 1) * kTok * kPRow;
-    // shares claimed at run time, per CTA: their least tiles, and how many of them
-    static constexpr int kLeast = RT / 8, kClaims = RT <= 16 ? 4 : RT <= 32 ? 8 : RT <= 64 ? 4 : 2;
-    static constexpr int kMaxCtas = kMaxSms * kPerSm;
-    static constexpr int kShares = kMaxCtas * (1 + kClaims);
     static constexpr uint32_t kTmem = RT <= 16 ? 64 : RT <= 32 ? 128 : RT <= 64 ? 256 : 512;
     // dynamic shared memory
     static constexpr uint32_t kOffQ = kStages * kStage;
@@ -94,12 +92,14 @@ template <int RT> struct Shape {
 struct MmaParams {
     // the caches as [page][head][token][D], boxes of `box` tokens by 64 columns
     CUtensorMap map_k, map_v;
+    CUtensorMap map_q;  // q as [token][head][D], boxes of a row tile's nodes x the group x 64 columns
+    int32_t q_box;    // 0: row tiles do not hold whole nodes, or q's strides do not fit a map: cp.async
     int32_t box;      // tokens per box; 0: cp.async
     int32_t tok;      // tokens per tile: 128, or the boxes that fit in 128
     sgmv_tree_attention_args a;
     float c;          // scale * log2(e)
     int32_t group;    // query heads per KV head
-    int *claim;       // shares claimed (0 between calls); shares of this call
+    int *shares;      // shares of this call
     struct Cut *cut;  // [share]: the cut item that begins there
     float *ml;        // [share][2][RT][2]: reference and sum of parts of items
     float *part;      // [share][2][RT][128]
@@ -122,24 +122,12 @@ struct Segment {
     int see;                         // which tree table
 };
 
-// How the line of W tiles is cut.  Share i < ctas is CTA i's own, `own` tiles
-// each; the rest is cut into shares of `small` tiles that CTAs claim as they
-// finish: with equal shares alone, the SMs' unequal memory bandwidth left the
-// slowest CTA at 202 us and the average at 177 (32 trees over 4096 tokens).
+// How the line of W tiles is cut: share i is tiles [i own, (i + 1) own).
 struct Plan {
-    int64_t W, own, split, small;    // split: where the claimed shares begin
-    int32_t ctas, shares, stride;
+    int64_t W, own;
+    int32_t stride;
     int64_t before[kSeqTable];       // tiles before every stride-th sequence
-
-    __device__ __forceinline__ int of(int64_t w) const {
-        return w < split ? (int)(w / own) : ctas + (int)((w - split) / small);
-    }
-    __device__ __forceinline__ void range(int id, int64_t &w, int64_t &w1) const {
-        w = id < ctas ? id * own : split + (id - ctas) * small;
-        w1 = w + (id < ctas ? own : small);
-        const int64_t end = id < ctas ? split : W;
-        w1 = w1 < end ? w1 : end;
-    }
+    int32_t t0[kSeqTable], n[kSeqTable], prefix[kSeqTable];  // of the sequences, if there are no more
 };
 
 // A sequence's part of the line.
@@ -148,12 +136,18 @@ struct Sequence {
     uint32_t items;
 
     // false: bad metadata
-    template <int RT> __device__ __forceinline__ bool enter(const MmaParams &P, int b_) {
+    template <int RT> __device__ __forceinline__ bool enter(const MmaParams &P, int b_, const Plan *plan = nullptr) {
         const sgmv_tree_attention_args &a = P.a;
         b = b_;
-        t0 = a.tree_ptr[b];
-        n = a.tree_ptr[b + 1] - t0;
-        prefix = a.prefix_lens[b];
+        if (plan && a.B <= kSeqTable) {
+            t0 = plan->t0[b];
+            n = plan->n[b];
+            prefix = plan->prefix[b];
+        } else {
+            t0 = a.tree_ptr[b];
+            n = a.tree_ptr[b + 1] - t0;
+            prefix = a.prefix_lens[b];
+        }
         items = 0;
         tiles = 1;
         if (!(t0 >= 0 && n >= 0 && n <= SGMV_TREE_MAX_NODES && (int64_t)t0 + n <= a.T && prefix >= 0 &&
@@ -331,7 +325,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
     __shared__ __align__(8) uint64_t seg_full[kSegs], seg_empty[kSegs], aux_full[kSegs];
     __shared__ __align__(8) uint64_t p_full, pv_done, tab_ready, drained;
     __shared__ uint32_t s_tmem;
-    __shared__ int s_lost, s_poison, s_longest, s_known, s_loading;
+    __shared__ int s_lost, s_poison, s_longest, s_known;
     __shared__ int64_t s_sum[32];
     __shared__ Plan plan;
     __shared__ Segment s_seg[kSegs], s_cur;        // s_cur: the softmax warps' segment
@@ -346,7 +340,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
         if (lane == 0) {
             for (int i = 0; i < S::kStages; ++i)
                 mbar_init(&full[i], P.box ? kLoaders / 32 : kLoaders), mbar_init(&empty[i], 1);
-            for (int i = 0; i < S::kQ; ++i) mbar_init(&q_full[i], 32), mbar_init(&q_empty[i], 1);
+            for (int i = 0; i < S::kQ; ++i) mbar_init(&q_full[i], P.q_box ? 1 : 32), mbar_init(&q_empty[i], 1);
             for (int i = 0; i < kSegs; ++i) {
                 mbar_init(&seg_full[i], 1);
                 mbar_init(&seg_empty[i], 2 + kLoaders / 32);  // MMA, softmax, loaders
@@ -357,7 +351,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
             mbar_init(&tab_ready, kLoaders);
             mbar_init(&drained, 1);
             mbar_init_fence();
-            s_lost = s_longest = s_known = s_loading = 0;
+            s_lost = s_longest = s_known = 0;
             s_poison = -1;
             for (int i = 0; i < kSegs; ++i) s_seg[i].tile = s_seg[i].end = 0;
         }
@@ -370,7 +364,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
     if (P.tok < kTok)
         for (uint32_t i = tid * 16u; i < S::kOffQ; i += S::kThreads * 16u)
             sts128(sm + i, make_uint4(0, 0, 0, 0));
-    if (a.D % 64 != 0)
+    if (a.D % 64 != 0 && !(P.box && P.q_box))
         for (uint32_t i = (P.box ? S::kOffQ : 0u) + tid * 16u; i < S::kOffP; i += S::kThreads * 16u)
             sts128(sm + i, make_uint4(0, 0, 0, 0));
     fence_proxy_async();
@@ -390,6 +384,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
             if (!q.template enter<RT>(P, b) && blockIdx.x == 0) set_error(P.err, kErrBadSegments);
             own = q.work();
             if (own) longest = max(longest, q.tiles);
+            if (b < kSeqTable) plan.t0[b] = q.t0, plan.n[b] = q.n, plan.prefix[b] = q.prefix;
         }
         int64_t run = own;
         for (int o = 1; o < 32; o <<= 1) {
@@ -414,25 +409,12 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
     tc_fence_after();
     const uint32_t tmem = s_tmem;
     const int ctas = (int)gridDim.x;
-    const int64_t even = W / ctas, least = (s_longest + kMaxParts - 1) / kMaxParts;
-    const bool claims = even >= 4 * S::kLeast && even >= 8 && even >= 4 * least;
     if (tid == 0) {
         plan.W = W;
         plan.stride = stride;
-        plan.ctas = ctas;
-        if (claims) {
-            plan.own = even - even / 4;
-            plan.split = plan.own * ctas;
-            const int64_t small = (W - plan.split + (int64_t)ctas * S::kClaims - 1) / ((int64_t)ctas * S::kClaims);
-            plan.small = max(max(small, (int64_t)S::kLeast), least);
-            plan.shares = ctas + (int)((W - plan.split + plan.small - 1) / plan.small);
-        } else {
-            plan.own = max((W + ctas - 1) / ctas, max(least, (int64_t)1));
-            plan.split = W;
-            plan.small = 1;
-            plan.shares = (int)((W + plan.own - 1) / plan.own);
-        }
-        if (blockIdx.x == 0) P.claim[1] = plan.shares;
+        // no more than kMaxParts parts or so of an item, for the join's sake
+        plan.own = max(max((W + ctas - 1) / ctas, ((int64_t)s_longest + kMaxParts - 1) / kMaxParts), (int64_t)1);
+        if (blockIdx.x == 0) *P.shares = (int)((W + plan.own - 1) / plan.own);
     }
     __syncthreads();
     if (plan.own * blockIdx.x >= W) {
@@ -450,53 +432,33 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
 
     if (warp == kWalkWarp) {
         // ---- the walk along the line ---------------------------------------------
-        int64_t base = 0, w = 0, w1 = 0;  // first tile of the sequence; next tile; end of the share
-        int id = (int)blockIdx.x, see = 0, see_b = -1, see_rt = -1, see_user[2] = {-1, -1};
+        const int id = (int)blockIdx.x;
+        int64_t w = plan.own * id, base = 0;   // next tile; first tile of its sequence
+        const int64_t w1 = min(W, w + plan.own);  // end of the share
+        int see = 0, see_b = -1, see_rt = -1, see_user[2] = {-1, -1};
         Sequence q;
-        q.items = 0;
-        q.tiles = 1;
-        plan.range(id, w, w1);
-        bool seek = true;
+        {   // the table's last entry at or before w
+            int lo = 0, hi = (a.B - 1) / plan.stride;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (plan.before[mid] <= w) lo = mid;
+                else hi = mid - 1;
+            }
+            base = plan.before[lo];
+            q.template enter<RT>(P, lo * plan.stride, &plan);
+        }
         for (int i = 0;; ++i) {
             if (i >= kSegs) await(&seg_empty[i % kSegs], (uint32_t)(i / kSegs - 1) & 1, lost);
             if (w >= w1) {
-                id = -1;
-                if (claims) {
-                    // not before the last known segment is being loaded
-                    const uint64_t t0 = global_ns();
-                    while (*(volatile int *)&s_loading < i && !*lost)
-                        if (global_ns() - t0 > kWaitLimitNs) *lost = 1;
-                    __syncwarp();
-                    if (lane == 0) {
-                        id = ctas + atomicAdd(&P.claim[0], 1);
-                        if (id >= plan.shares) id = -1;
-                    }
-                    id = __shfl_sync(0xffffffffu, id, 0);
+                if (lane == 0) {
+                    s_seg[i % kSegs].tile = s_seg[i % kSegs].end = 0;
+                    mbar_arrive(&seg_full[i % kSegs]);
                 }
-                if (id < 0) {
-                    if (lane == 0) {
-                        s_seg[i % kSegs].tile = s_seg[i % kSegs].end = 0;
-                        mbar_arrive(&seg_full[i % kSegs]);
-                    }
-                    break;
-                }
-                plan.range(id, w, w1);
-                seek = w >= base + q.work();
-            }
-            if (seek) {  // the table's last entry at or before w
-                int lo = 0, hi = (a.B - 1) / plan.stride;
-                while (lo < hi) {
-                    const int mid = (lo + hi + 1) >> 1;
-                    if (plan.before[mid] <= w) lo = mid;
-                    else hi = mid - 1;
-                }
-                base = plan.before[lo];
-                q.template enter<RT>(P, lo * plan.stride);
-                seek = false;
+                break;
             }
             while (w >= base + q.work()) {
                 base += q.work();
-                q.template enter<RT>(P, q.b + 1);
+                q.template enter<RT>(P, q.b + 1, &plan);
             }
             const uint32_t rel = (uint32_t)(w - base), item = rel / (uint32_t)q.tiles;
             const int h = (int)(item / (uint32_t)q.nrt), rt = (int)(item - (uint32_t)h * (uint32_t)q.nrt);
@@ -526,7 +488,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
                         cut.h = h;
                         cut.rt = rt;
                         cut.first = id;
-                        cut.parts = plan.of(w + q.tiles - 1) - id + 1;
+                        cut.parts = (int)((w + q.tiles - 1) / plan.own) - id + 1;
                     }
                     P.cut[id] = cut;
                 }
@@ -535,25 +497,36 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
             }
             __syncwarp();
             w += end - tile;
-            // the rows' places, then their queries
+            // the row tile's queries, and the rows' places
             const int qb = i % S::kQ, R = min(RT, q.n * group - rt * RT);
+            if (i >= S::kQ) await(&q_empty[qb], (uint32_t)(i / S::kQ - 1) & 1, lost);
+            uint8_t *const qs = sm + S::kOffQ + (uint32_t)qb * S::kQBytes;
+            if (P.q_box && lane == 0) {
+                // (rows past R are the next sequence's or zeros: finite or not,
+                // they end in columns of the products that nobody reads)
+                const int halves = D > 64 ? 2 : 1;
+                mbar_arrive_expect_tx(&q_full[qb], (uint32_t)halves * RT * 128u);
+                for (int half = 0; half < halves; ++half)
+                    tma_load_3d(qs + half * RT * 128, &P.map_q, half * 64, h * group, q.t0 + rt * RT / group, &q_full[qb]);
+            }
+            __syncwarp();
             int2 *const place = reinterpret_cast<int2 *>(sm + S::kOffRow) + (i % kSegs) * RT;
             for (int r = lane; r < R; r += 32) place[r] = row_place(P, q.t0, h, rt * RT + r);
             __syncwarp();
-            if (i >= S::kQ) await(&q_empty[qb], (uint32_t)(i / S::kQ - 1) & 1, lost);
-            uint8_t *const qs = sm + S::kOffQ + (uint32_t)qb * S::kQBytes;
-            for (int m = lane / cpr, c = lane % cpr; m < RT;) {
-                const T *src = static_cast<const T *>(a.q);
-                if (m < R) {
-                    const int2 at = place[m];
-                    src += (int64_t)(at.x < 0 ? ~at.x : at.x) * a.q_token + (int64_t)at.y * a.q_head + c * 8;
+            if (!P.q_box) {
+                for (int m = lane / cpr, c = lane % cpr; m < RT;) {
+                    const T *src = static_cast<const T *>(a.q);
+                    if (m < R) {
+                        const int2 at = place[m];
+                        src += (int64_t)(at.x < 0 ? ~at.x : at.x) * a.q_token + (int64_t)at.y * a.q_head + c * 8;
+                    }
+                    cp_async16(qs + (uint32_t)(c >> 3) * (RT * 128u) + sw128_offset(m, c & 7), src, m < R ? 16u : 0u);
+                    m += 32 / cpr;
+                    c += 32 % cpr;
+                    if (c >= cpr) c -= cpr, ++m;
                 }
-                cp_async16(qs + (uint32_t)(c >> 3) * (RT * 128u) + sw128_offset(m, c & 7), src, m < R ? 16u : 0u);
-                m += 32 / cpr;
-                c += 32 % cpr;
-                if (c >= cpr) c -= cpr, ++m;
+                cp_async_arrive(&q_full[qb]);
             }
-            cp_async_arrive(&q_full[qb]);
             if (build) {
                 // see[j]: the rows that see tree node j.  Every node of this row
                 // tile marks itself and its ancestors with its rows' bits.
@@ -629,7 +602,6 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
             for (int i = 0;; ++i) {
                 const Segment s = wait_segment(i);
                 if (s.end == 0) break;
-                if (lt == 0) *(volatile int *)&s_loading = i + 1;
                 if (!looked) look(s, s.tile);
                 for (int tile = s.tile; tile < s.end; ++tile) {
                     // boxes past the end, and pages out of range, read as zeros
@@ -694,7 +666,6 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
             for (int i = 0;; ++i) {
                 const Segment s = wait_segment(i);
                 if (s.end == 0) break;
-                if (lt == 0) *(volatile int *)&s_loading = i + 1;
                 for (int tile = s.tile; tile < s.end; ++tile, ++g) {
                     // where the tile's tokens are (elements from the cache's start)
                     for (int m = lt; m < kTok; m += kLoaders) {
@@ -760,7 +731,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
             await(&full[k_st], k_ph, lost);
             --left;
             // cp.async (generic proxy) data -> tensor core (async proxy)
-            if (first || !P.box) fence_proxy_async();
+            if ((first && !P.q_box) || !P.box) fence_proxy_async();
             tc_fence_after();
             const uint64_t kd = k_desc + (uint32_t)k_st * (kStage >> 4);
             const uint64_t qd = q_desc + (uint32_t)qb * (S::kQBytes >> 4);
@@ -1055,8 +1026,7 @@ __global__ void __launch_bounds__(kJoinThreads) sgmv_tree_join_kernel(const __gr
     pdl_wait();
     pdl_trigger();
     const int warps = gridDim.x * (kJoinThreads / 32), lane = threadIdx.x & 31;
-    const int units = P.claim[1] * RT;
-    if (blockIdx.x == 0 && threadIdx.x == 0) P.claim[0] = 0;  // ready for the next call
+    const int units = *P.shares * RT;
     for (int u = blockIdx.x * (kJoinThreads / 32) + threadIdx.x / 32; u < units; u += warps) {
         const int id = u / RT, r = u % RT;
         const Cut cut = P.cut[id];
@@ -1113,20 +1083,14 @@ int row_tile(int32_t T, int32_t B, int32_t group) {
 
 constexpr size_t kHeadBytes = 256;
 
-int max_ctas(int rt) { return rt == 16 ? Shape<16>::kMaxCtas : kMaxSms; }
-
-size_t shares_of(int rt) {
-    return rt == 16   ? Shape<16>::kShares
-           : rt == 32 ? Shape<32>::kShares
-           : rt == 64 ? Shape<64>::kShares
-                      : Shape<128>::kShares;
-}
+// CTAs, and so shares, at most.
+int max_ctas(int rt) { return kMaxSms * (rt == 16 ? Shape<16>::kPerSm : 1); }
 
 }  // namespace
 
 size_t tree_mma_workspace(int32_t T, int32_t B, int32_t group) {
     const int rt = row_tile(T, B, group);
-    return kHeadBytes + shares_of(rt) * (sizeof(Cut) + 2u * (size_t)rt * 130u * 4u);
+    return kHeadBytes + (size_t)max_ctas(rt) * (sizeof(Cut) + 2u * (size_t)rt * 130u * 4u);
 }
 
 int tree_mma_launch(const sgmv_tree_attention_args &a, int nsm, int *err, cudaStream_t stream) {
@@ -1136,15 +1100,15 @@ int tree_mma_launch(const sgmv_tree_attention_args &a, int nsm, int *err, cudaSt
     p.a = a;
     p.c = a.scale * 1.4426950408889634f;
     p.group = group;
-    p.claim = static_cast<int *>(a.workspace);
+    p.shares = static_cast<int *>(a.workspace);
     p.cut = reinterpret_cast<Cut *>(static_cast<uint8_t *>(a.workspace) + kHeadBytes);
-    p.ml = reinterpret_cast<float *>(p.cut + shares_of(rt));
-    p.part = p.ml + shares_of(rt) * 2 * rt * 2;
+    p.ml = reinterpret_cast<float *>(p.cut + max_ctas(rt));
+    p.part = p.ml + max_ctas(rt) * 2 * rt * 2;
     p.err = err;
     const bool bf16 = a.dtype == SGMV_BF16;
-    // Boxes are as high as pages allow: TMA's cost here is per box (at pages
-    // of 24 tokens, boxes of 8 filling every tile measured 115 us, boxes of 24 and tiles of
-    // 120 tokens XX us, on 128 sequences of up to 2100 tokens, 4 heads of 80)
+    // Boxes are as high as pages allow, for TMA's cost here is per box: at pages of
+    // 24 tokens, boxes of 8 filling every tile took 115 us, boxes of 24 and tiles of
+    // 120 tokens 109 us (128 sequences of up to 2100 tokens, 4 heads of 80).
     p.box = std::gcd(a.block_size, kTok);
     p.tok = kTok;
     if (a.block_size % 8 == 0 && a.block_size < kTok && a.block_size > p.box) {
@@ -1162,6 +1126,13 @@ int tree_mma_launch(const sgmv_tree_attention_args &a, int nsm, int *err, cudaSt
             p.box = 0, p.tok = kTok;  // strides that a tensor map cannot hold
     } else {
         p.box = 0;
+    }
+    p.q_box = 0;
+    if (rt % group == 0) {
+        const cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)a.Hq, (cuuint64_t)a.T};
+        const cuuint64_t strides[2] = {(cuuint64_t)a.q_head * 2u, (cuuint64_t)a.q_token * 2u};
+        const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)(rt / group)};
+        p.q_box = tmap_encode(&p.map_q, bf16, 3, a.q, dims, strides, box, true);
     }
     const bool h = a.dtype == SGMV_F16;
     using B16 = __nv_bfloat16;

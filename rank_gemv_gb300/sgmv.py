@@ -496,9 +496,9 @@ def sgmv_tree_attention(out, q, k_cache, v_cache, block_table, prefix_lens, tree
     Row t of sequence b (tree_ptr[b] <= t < tree_ptr[b + 1]) sees the
     prefix_lens[b] tokens of its context, its ancestors by `parents` (None: a
     chain) and itself.  scale defaults to D ** -0.5; lse (fp32 [T, Hq]) receives
-    the log-sum-exp.  workspace: uint8 device tensor of
-    sgmv_tree_attention_workspace_bytes(T, B, Hq, Hkv, D) bytes, zeroed once
-    before its first use (a zeroed one is made when None)."""
+    the log-sum-exp.  workspace: uint8 device tensor of at least
+    sgmv_tree_attention_workspace_bytes(T, B, Hq, Hkv, D) bytes; one is
+    allocated when None."""
     qshape, dtype = q.shape, q.dtype
     if len(qshape) != 3 or dtype not in _DTYPES:
         raise TypeError("q must be a [T, heads, D] tensor of f16 or bf16")
@@ -513,7 +513,7 @@ def sgmv_tree_attention(out, q, k_cache, v_cache, block_table, prefix_lens, tree
     table, width, row = _table(block_table, B)
     lib = load_library()
     if workspace is None:
-        workspace = torch.zeros(lib.sgmv_tree_attention_workspace_bytes(T, B, Hq, shape[2], D),
+        workspace = torch.empty(lib.sgmv_tree_attention_workspace_bytes(T, B, Hq, shape[2], D),
                                 dtype=torch.uint8, device=q.device)
     args = _ATTENTION_ARGS.pack(
         oo[0], qi[0], k_cache.data_ptr(), v_cache.data_ptr(), 0 if lse is None else lse.data_ptr(),

@@ -136,7 +136,7 @@ def test_many_ragged_sequences(sgmv, dtype):
                                                   (8, 8, 8, 4000, 40), (8, 20, 8, 9000, 17), (4, 3, 2, 60000, 5)])
 @pytest.mark.parametrize("bs", [16, 24])
 def test_much_work(sgmv, group, n, Hkv, prefix, B, bs):
-    """More work than every SM's own share: parts of items are claimed and joined."""
+    """Every SM busy with several items, their ends cut and joined."""
     rng = np.random.default_rng(B)
     lens = [prefix] + [int(x) for x in rng.integers(prefix // 3, prefix, B - 1)]
     nodes = [n] + [int(x) for x in rng.integers(1, n + 1, B - 1)]
@@ -241,14 +241,16 @@ def test_strides(sgmv, dtype, order):
 
 
 @pytest.mark.parametrize("Hq,D,n", [(4, 64, 3), (32, 128, 9), (2, 256, 2)])
-def test_workspace_is_left_ready_and_results_repeat(sgmv, Hq, D, n):
+def test_results_repeat_whatever_the_workspace_holds(sgmv, Hq, D, n):
     b = Batch([3000, 700, 10], [n, 1, 2], Hq, 2, D, 16, torch.bfloat16, seed=7).dirty()
     size = sgmv.sgmv_tree_attention_workspace_bytes(b.T, b.B, Hq, 2, D)
-    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    ws = torch.full((size,), 0xff, dtype=torch.uint8, device="cuda")
     b.run(sgmv, workspace=ws)
     first, lse = b.out.clone(), b.lse.clone()
     b.check()
-    for _ in range(3):  # the same bits, with the workspace as the last call left it
+    for fill in (None, 0, 0x7f):  # as the last call left it, and other contents
+        if fill is not None:
+            ws.fill_(fill)
         b.out.zero_()
         b.run(sgmv, workspace=ws)
         assert torch.equal(b.out, first) and torch.equal(b.lse, lse)
