@@ -139,9 +139,11 @@ int num_sms() {
     return cache[dev];
 }
 
-// Encodes the B tensor map, then launches.  With H2 and every CTA's first
-// column multiples of 256, B is viewed as [L][H2/256][r][256] so that one
-// copy brings a whole chunk; otherwise as [L][r][H2], one copy per 256 columns.
+// Encodes the B tensor map, then launches.  When every CTA's columns are whole
+// chunks (hn of them, a multiple of 256), B is viewed as [L][H2/256][r][256] so
+// that one copy brings a chunk; otherwise as [L][r][H2], one copy per 256
+// columns.  A map serves copies of its own rank only, so the two views are not
+// mixed in a launch.
 int stream_launch(int in_dtype, StreamLaunch &l) {
     StreamParams &p = l.p;
     p.inject = g_inject_timeout;
@@ -149,7 +151,7 @@ int stream_launch(int in_dtype, StreamLaunch &l) {
     const cuuint64_t es = 2;
     if (p.np < 1 || p.np > kStreamMaxProblems) return (int)cudaErrorInvalidValue;
     p.b4d = 0;
-    if (p.H2 % 256 == 0 && p.jc % 256 == 0) {
+    if (p.H2 % p.hn == 0 && p.jc % p.hn == 0) {
         const cuuint64_t dims[4] = {256, (cuuint64_t)p.r, (cuuint64_t)p.H2 / 256, (cuuint64_t)p.L};
         const cuuint64_t strides[3] = {(cuuint64_t)p.H2 * es, 256 * es,
                                        (cuuint64_t)p.r * p.H2 * es};
