@@ -35,17 +35,6 @@ struct RopeParams {
     int32_t rot, uph;               // pieces that rotate, pieces in all, per head
 };
 
-// 16-bit pairs of a vector, widened and rounded
-template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
-template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
 // Pieces of a head: the rotating ones, then the copied columns.  Piece w of
 // heads h0, h0 + step, ... (q's heads, then k's) is one thread's.
 template <typename T, int MODE>

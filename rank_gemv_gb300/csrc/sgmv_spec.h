@@ -7,8 +7,22 @@
 #include <stdint.h>
 
 #include "sgmv.h"
+#include "sgmv_device.cuh"
 
 namespace sgmv {
+
+#ifdef __CUDACC__
+// Two fp32 values rounded to a 16-bit pair, in one instruction.
+template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+#endif
 
 constexpr int kSpecMaxD = 256;               // widest head
 constexpr int kRopeMaxPairs = kSpecMaxD / 2;

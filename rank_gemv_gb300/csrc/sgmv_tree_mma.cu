@@ -892,18 +892,17 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
                     }
                     weights();
                 }
-                T p[S::kRows];  // rounded to the tensor cores' operand type
+                uint32_t p[S::kRows / 2];  // rounded to the tensor cores' operand type
 #pragma unroll
                 for (int i = 0; i < S::kRows; i += 2) {
                     add_pair(l[i], l[i + 1], s[i], s[i + 1]);
-                    p[i] = from_f<T>(s[i]);
-                    p[i + 1] = from_f<T>(s[i + 1]);
+                    p[i / 2] = pack2<T>(s[i], s[i + 1]);
                 }
                 // the previous tile's P has been read
                 if (g > 0) pv_finished(g - 1);
 #pragma unroll
                 for (int q = 0; q < S::kRows / 8; ++q)
-                    sts128(p_at(q), reinterpret_cast<const uint4 *>(p)[q]);
+                    sts128(p_at(q), make_uint4(p[4 * q], p[4 * q + 1], p[4 * q + 2], p[4 * q + 3]));
                 if (tree) {
                     // non-finite v of tree nodes: out of the tile, noted; what TMA
                     // brought from the last page past the end: zeroed

@@ -406,12 +406,33 @@ def _cache(k_cache, v_cache, dtype, ndim):
     return shape, stride
 
 
+_I32, _F32 = torch.int32, torch.float32
+
+
 def _list(t, name, n):
     """Pointer of a contiguous int32 tensor of n entries (or of None)."""
     if t is None:
         return 0
-    if _meta(t, name).numel() != n:
+    if t.dtype != _I32 or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous int32 tensor")
+    if t.numel() != n:
         raise ValueError(f"{name} must have {n} entries")
+    return t.data_ptr()
+
+
+def _rows(t, name, shape):
+    """(pointer, row stride) of a float32 [T, V] tensor with contiguous rows (or of None)."""
+    if t is None:
+        return 0, 0
+    s0, s1 = t.stride()
+    if t.dtype != _F32 or t.shape != shape or (s1 != 1 and shape[1] > 1):
+        raise TypeError(f"{name} must be float32 [T, V] with contiguous rows")
+    return t.data_ptr(), s0
+
+
+def _uniform(t, name, n):
+    if t.dtype != _F32 or not t.is_contiguous() or t.numel() != n:
+        raise TypeError(f"{name} must be a contiguous float32 tensor of {n} entries")
     return t.data_ptr()
 
 
@@ -531,25 +552,23 @@ def sgmv_tree_verify(target, draft, tokens, parents, tree_ptr, u_accept, u_sampl
     node) and draft [T, V] (what each node's children were drawn from, or None)
     with the uniform numbers u_accept [T] and u_sample [B]; returns (count [B],
     path [B, max_path], token [B]), int32 (`out`: such a tuple to write into)."""
-    T, V = target.shape
+    shape = target.shape
+    T, V = shape
     B = tree_ptr.numel() - 1
-    for t, name in ((target, "target"), (draft, "draft")):
-        if t is not None and (t.dtype != torch.float32 or t.shape != (T, V) or (V > 1 and t.stride(1) != 1)):
-            raise TypeError(f"{name} must be float32 [T, V] with contiguous rows")
-    for t, name, n in ((u_accept, "u_accept", T), (u_sample, "u_sample", B)):
-        if t.dtype != torch.float32 or not t.is_contiguous() or t.numel() != n:
-            raise TypeError(f"{name} must be a contiguous float32 tensor of {n} entries")
     if out is None:
         dev = target.device
-        out = (torch.empty(B, dtype=torch.int32, device=dev), torch.empty(B, max_path, dtype=torch.int32, device=dev),
-               torch.empty(B, dtype=torch.int32, device=dev))
-    count, path, token = out
+        out = (torch.empty(B, dtype=_I32, device=dev), torch.empty(B, max_path, dtype=_I32, device=dev),
+               torch.empty(B, dtype=_I32, device=dev))
+        count, path, token = [t.data_ptr() for t in out]
+    else:
+        count, path, token = (_list(out[0], "count", B), _list(out[1], "path", B * max_path),
+                              _list(out[2], "token", B))
+    tp, t0 = _rows(target, "target", shape)
+    dp, d0 = _rows(draft, "draft", shape)
     args = _VERIFY_ARGS.pack(
-        target.data_ptr(), 0 if draft is None else draft.data_ptr(), _list(tokens, "tokens", T),
-        _list(parents, "parents", T), _list(tree_ptr, "tree_ptr", B + 1), u_accept.data_ptr(),
-        u_sample.data_ptr(), _list(count, "count", B), _list(path, "path", B * max_path),
-        _list(token, "token", B), target.stride(0), 0 if draft is None else draft.stride(0), T, B, V,
-        max_path)
+        tp, dp, _list(tokens, "tokens", T), _list(parents, "parents", T),
+        _list(tree_ptr, "tree_ptr", B + 1), _uniform(u_accept, "u_accept", T),
+        _uniform(u_sample, "u_sample", B), count, path, token, t0, d0, T, B, V, max_path)
     _check(load_library().sgmv_tree_verify(args, _stream(target.device)), "sgmv_tree_verify")
     return out
 
