@@ -40,6 +40,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <climits>
 #include <numeric>
 #include <type_traits>
 
@@ -151,7 +152,7 @@ struct Sequence {
         items = 0;
         tiles = 1;
         if (!(t0 >= 0 && n >= 0 && n <= SGMV_TREE_MAX_NODES && (int64_t)t0 + n <= a.T && prefix >= 0 &&
-              (int64_t)prefix + n <= (int64_t)a.max_blocks * a.block_size))
+              (int64_t)prefix + n <= (int64_t)a.max_blocks * a.block_size && prefix <= INT_MAX - 2 * kTok - n))
             return false;
         if (n == 0) return true;
         total = prefix + n;

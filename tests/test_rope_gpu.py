@@ -155,6 +155,36 @@ def test_frequencies(sgmv):
     assert np.allclose(got, base * keep + base / 4 * (1 - keep), rtol=1e-13)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("T,Hq,Hk,D,pairs", [(1300, 32, 8, 128, 64), (2500, 7, 7, 80, 16), (4100, 1, 1, 64, 32),
+                                             (1217, 40, 40, 128, 32), (1999, 3, 2, 96, 20), (5000, 2, 2, 8, 4)])
+def test_many_rows(sgmv, dtype, interleaved, T, Hq, Hk, D, pairs):
+    """Several rows per CTA: against the reference, append and in-place included."""
+    g = torch.Generator("cuda").manual_seed(T)
+    qkv = rand(g, T, Hq + 2 * Hk, D, dtype=dtype)
+    q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hk], qkv[:, Hq + Hk:]
+    positions = torch.randint(0, 100000, (T,), generator=g, device="cuda", dtype=torch.int32)
+    f = sgmv.sgmv_rope_frequencies(pairs)
+    slots = torch.randperm(T + 5, generator=g, device="cuda")[:T].to(torch.int32)
+    slots[7::50] = -1
+    kc, vc = rand(g, T + 5, 1, Hk, D, dtype=dtype), rand(g, T + 5, 1, Hk, D, dtype=dtype)
+    want_k, want_v = kc.clone(), vc.clone()
+    q_out, k_out = torch.empty(T, Hq, D, device="cuda", dtype=dtype), torch.empty(T, Hk, D, device="cuda", dtype=dtype)
+    before = qkv.clone()
+    sgmv.sgmv_rope(q, k, positions, f, interleaved, q_out=q_out, k_out=k_out, v=v, k_cache=kc, v_cache=vc, slots=slots)
+    check_error_word(0)
+    assert torch.equal(qkv, before)
+    pos = positions.cpu().numpy()
+    close(q_out, q, pos, f.numpy(), interleaved)
+    close(k_out, k, pos, f.numpy(), interleaved)
+    live = slots >= 0
+    want_k[slots[live].long(), 0], want_v[slots[live].long(), 0] = k_out[live], v[live]
+    assert torch.equal(kc, want_k) and torch.equal(vc, want_v)
+    sgmv.sgmv_rope(q, k, positions, f, interleaved)
+    assert torch.equal(q, q_out) and torch.equal(k, k_out) and torch.equal(v, before[:, Hq + Hk:])
+
+
 def test_other_stream(sgmv):
     g = torch.Generator("cuda").manual_seed(5)
     q = rand(g, 64, 8, 128, dtype=torch.bfloat16)
