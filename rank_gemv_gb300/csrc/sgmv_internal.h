@@ -126,7 +126,8 @@ int tc_launch(const TCArgs &g);
 
 // Encode a tiled tensor map (f16 / bf16 elements, 128-byte swizzle or none).
 bool tmap_encode(CUtensorMap *m, bool bf16, int rank, const void *ptr, const cuuint64_t *dims,
-                 const cuuint64_t *strides, const cuuint32_t *box, bool swizzle128);
+                 const cuuint64_t *strides, const cuuint32_t *box, bool swizzle128,
+                 CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 
 // Launch one CUDA-core kernel; returns a cudaError_t value.
 int cc_launch_f16(const CCLaunch &l);

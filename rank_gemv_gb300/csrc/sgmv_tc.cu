@@ -793,7 +793,8 @@ EncodeTiledFn tiled_encoder() {
 }  // namespace
 
 bool tmap_encode(CUtensorMap *m, bool bf16, int rank, const void *ptr, const cuuint64_t *dims,
-                 const cuuint64_t *strides, const cuuint32_t *box, bool swizzle128) {
+                 const cuuint64_t *strides, const cuuint32_t *box, bool swizzle128,
+                 CUtensorMapL2promotion promotion) {
     EncodeTiledFn fn = tiled_encoder();
     if (!fn) return false;
     const cuuint32_t es[5] = {1, 1, 1, 1, 1};
@@ -801,7 +802,7 @@ bool tmap_encode(CUtensorMap *m, bool bf16, int rank, const void *ptr, const cuu
               (cuuint32_t)rank, const_cast<void *>(ptr), dims, strides, box, es,
               CU_TENSOR_MAP_INTERLEAVE_NONE,
               swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+              promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 namespace {

@@ -226,13 +226,8 @@ __device__ __forceinline__ void add_pair(float &x, float &y, float a, float b) {
     asm("add.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(w));
     asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
 }
-// floats as integers of the same order
-__device__ __forceinline__ int ordered(float f) {
-    const int i = __float_as_int(f);
-    return i ^ ((i >> 31) & 0x7fffffff);
-}
-__device__ __forceinline__ float unordered(int i) {
-    return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
+__device__ __forceinline__ void sts16(void *p, uint16_t v) {
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(smem_addr(p)), "h"(v) : "memory");
 }
 // Barrier of the 128 threads of softmax warpgroup g; with a vote.
 __device__ __forceinline__ void group_bar(int g) {
@@ -272,9 +267,16 @@ template <int N> __device__ __forceinline__ void tmem_store(uint32_t addr, const
             : "memory");
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-// v[i], i < N: row i's partial of every lane.  Afterwards each lane holds the
-// sums over the warp of N / 32 (at least 1) rows, the first of them returned.
-template <int N> __device__ __forceinline__ int warp_sums(float (&v)[N], int lane) {
+// v[i], i < N: row i's partial of every lane.  Afterwards lane l holds, in
+// v[0], the whole warp's sum or maximum (NaN wins) of the row returned; a row of
+// N < 32 is held by 32 / N lanes.
+template <bool MAX> __device__ __forceinline__ float join2(float a, float b) {
+    if (!MAX) return a + b;
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
+template <bool MAX, int N> __device__ __forceinline__ int warp_rows(float (&v)[N], int lane) {
     int row = 0;
     int n = N;
 #pragma unroll
@@ -288,10 +290,10 @@ template <int N> __device__ __forceinline__ int warp_sums(float (&v)[N], int lan
                 if (i < n) {
                     const float give = up ? v[i] : v[i + n];
                     const float keep = up ? v[i + n] : v[i];
-                    v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                    v[i] = join2<MAX>(keep, __shfl_xor_sync(0xffffffffu, give, o));
                 }
         } else {
-            v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+            v[0] = join2<MAX>(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
         }
     }
     return row;
@@ -855,18 +857,18 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
                         s[i + 1] = exp2_approx(s[i + 1]);
                     }
                 };
-                weights();
-                if (group_any(wg, top > kBias + kSlack)) {
+                bool moved = tile == first;  // nothing to refer to yet
+                if (!moved) {
+                    weights();
+                    moved = group_any(wg, top > kBias + kSlack);
+                }
+                if (moved) {
                     // new references: the larger of the old and this tile's maximum
                     tmem_load(ts, s);
-                    int mine = 0;
 #pragma unroll
-                    for (int i = 0; i < S::kRows; ++i) {
-                        const float y = !edge || (vis >> i & 1u) ? s[i] * c : -INFINITY;
-                        const int m = __reduce_max_sync(0xffffffffu, ordered(y));
-                        if (lane == i) mine = m;
-                    }
-                    if (lane < S::kRows) s_red[warp & 3][r0 + lane] = unordered(mine);
+                    for (int i = 0; i < S::kRows; ++i) s[i] = !edge || (vis >> i & 1u) ? s[i] * c : -INFINITY;
+                    const int row = warp_rows<true>(s, lane);
+                    s_red[warp & 3][r0 + row] = s[0];
                     group_bar(wg);
                     if (tok < S::kRows) {
                         const int r = r0 + tok;
@@ -946,8 +948,8 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
                 float v[S::kRows];
 #pragma unroll
                 for (int r = 0; r < S::kRows; ++r) v[r] = l[r];
-                const int r = warp_sums(v, lane);
-                if (S::kRows == 32 || (lane & 1) == 0) s_red[warp & 3][r0 + r] = v[0];
+                const int r = warp_rows<false>(v, lane);
+                s_red[warp & 3][r0 + r] = v[0];
             }
             group_bar(wg);
             const bool whole = cur.whole != 0;
@@ -958,11 +960,11 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
                 const float L = s_red[0][r] + s_red[1][r] + s_red[2][r] + s_red[3][r], ref = -s_ref[r];
                 if (!whole) {
                     *reinterpret_cast<float2 *>(P.ml + ((int64_t)slot * RT + r) * 2) = make_float2(ref, L);
-                } else if (r < R) {
-                    const int2 to = place[r];
+                } else {
+                    const int2 to = place[r < R ? r : 0];
                     const bool none = to.x < 0 || L == 0.f;
                     s_fac[r] = none ? 0.f : 1.f / L;
-                    if (a.lse)
+                    if (a.lse && r < R)
                         a.lse[(int64_t)(to.x < 0 ? ~to.x : to.x) * a.Hq + to.y] =
                             none ? -INFINITY : (ref + log2f(L)) * 0.693147180559945309f;
                 }
@@ -990,17 +992,25 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
                     }
                 }
                 if (whole) {
-                    if (d < D && ok) {
-                        T *const out = static_cast<T *>(a.out) + d;
+                    // through the idle P buffer, a row of 256 bytes each, to whole
+                    // vectors (and little code: this path is cold in the instruction cache)
+                    uint8_t *const rows = sm + S::kOffP + r0 * 256;
 #pragma unroll
-                        for (int i = 0; i < S::kRows; ++i) {
-                            if (r0 + i < R) {
-                                const int2 to = place[r0 + i];
-                                const float f = s_fac[r0 + i];
-                                out[(int64_t)(to.x < 0 ? ~to.x : to.x) * a.out_token + (int64_t)to.y * a.out_head] =
-                                    from_f<T>(f == 0.f ? 0.f : v[i] * f);
-                            }
-                        }
+                    for (int i = 0; i < S::kRows; i += 2) {
+                        const float f0 = s_fac[r0 + i], f1 = s_fac[r0 + i + 1];
+                        const uint32_t two = pack2<T>(f0 == 0.f ? 0.f : v[i] * f0, f1 == 0.f ? 0.f : v[i + 1] * f1);
+                        sts16(rows + i * 256 + d * 2, (uint16_t)two);
+                        sts16(rows + (i + 1) * 256 + d * 2, (uint16_t)(two >> 16));
+                    }
+                    group_bar(wg);
+                    const int used = min(S::kRows, R - r0);
+#pragma unroll 1
+                    for (int m = tok >> 4; m < used; m += 8) {  // 16 lanes per row
+                        const int2 to = place[r0 + m];
+                        T *const out = static_cast<T *>(a.out) + (int64_t)(to.x < 0 ? ~to.x : to.x) * a.out_token +
+                                       (int64_t)to.y * a.out_head;
+                        const int col = (tok & 15) * 8;
+                        if (col < D && ok) *reinterpret_cast<uint4 *>(out + col) = lds128(rows + m * 256 + col * 2);
                     }
                 } else {
                     float *const part = P.part + ((int64_t)slot * RT + r0) * 128 + d;
@@ -1121,8 +1131,17 @@ int tree_mma_launch(const sgmv_tree_attention_args &a, int nsm, int *err, cudaSt
         const cuuint64_t strides[3] = {(cuuint64_t)a.cache_token * 2u, (cuuint64_t)a.cache_head * 2u,
                                        (cuuint64_t)a.cache_block * 2u};
         const cuuint32_t box[4] = {64, (cuuint32_t)p.box, 1, 1};
-        if (!tmap_encode(&p.map_k, bf16, 4, a.k_cache, dims, strides, box, true) ||
-            !tmap_encode(&p.map_v, bf16, 4, a.v_cache, dims, strides, box, true))
+        // What L2 fetches around a row of a box is this head's only if the rows of
+        // a head are contiguous or as wide; else it is another CTA's (heads of 64 columns side by
+        // side: AAA us with 256 bytes, BBB with 128)
+        const int row = a.D * 2;
+        const CUtensorMapL2promotion fetch =
+            a.cache_token == a.D || row % 256 == 0 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+            : row % 128 == 0                       ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+            : row % 64 == 0                        ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B
+                                                   : CU_TENSOR_MAP_L2_PROMOTION_NONE;
+        if (!tmap_encode(&p.map_k, bf16, 4, a.k_cache, dims, strides, box, true, fetch) ||
+            !tmap_encode(&p.map_v, bf16, 4, a.v_cache, dims, strides, box, true, fetch))
             p.box = 0, p.tok = kTok;  // strides that a tensor map cannot hold
     } else {
         p.box = 0;
