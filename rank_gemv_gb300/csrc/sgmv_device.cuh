@@ -144,6 +144,14 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const void *map, int c0, 
         : "memory");
 }
 
+// As far as L2 only.
+__device__ __forceinline__ void tma_prefetch_3d(const void *map, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
+
 __device__ __forceinline__ void tma_load_4d(void *dst, const void *map, int c0, int c1, int c2,
                                             int c3, uint64_t *bar) {
     asm volatile(

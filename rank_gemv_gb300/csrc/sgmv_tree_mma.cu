@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
     __shared__ int s_lost, s_poison, s_longest, s_known;
     __shared__ int64_t s_sum[32];
     __shared__ Plan plan;
-    __shared__ Segment s_seg[kSegs], s_cur;        // s_cur: the softmax warps' segment
+    __shared__ Segment s_seg[kSegs], s_cur[2];     // s_cur: the softmax warps' segment, and the next
     __shared__ int16_t s_parent[SGMV_TREE_MAX_NODES];
     __shared__ __align__(16) float s_ref[RT], s_fac[RT];  // s_ref: -ref
     __shared__ float s_red[4][RT];
@@ -501,22 +501,22 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
             __syncwarp();
             w += end - tile;
             // the row tile's queries, and the rows' places
-            const int qb = i % S::kQ, R = min(RT, q.n * group - rt * RT);
-            if (i >= S::kQ) await(&q_empty[qb], (uint32_t)(i / S::kQ - 1) & 1, lost);
+            const int qb = i % S::kQ, R = min(RT, q.n * group - rt * RT), halves = D > 64 ? 2 : 1;
             uint8_t *const qs = sm + S::kOffQ + (uint32_t)qb * S::kQBytes;
-            if (P.q_box && lane == 0) {
-                // (rows past R are the next sequence's or zeros: finite or not,
-                // they end in columns of the products that nobody reads)
-                const int halves = D > 64 ? 2 : 1;
-                mbar_arrive_expect_tx(&q_full[qb], (uint32_t)halves * RT * 128u);
-                for (int half = 0; half < halves; ++half)
-                    tma_load_3d(qs + half * RT * 128, &P.map_q, half * 64, h * group, q.t0 + rt * RT / group, &q_full[qb]);
-            }
-            __syncwarp();
             int2 *const place = reinterpret_cast<int2 *>(sm + S::kOffRow) + (i % kSegs) * RT;
-            for (int r = lane; r < R; r += 32) place[r] = row_place(P, q.t0, h, rt * RT + r);
-            __syncwarp();
-            if (!P.q_box) {
+            auto bring_q = [&]() {
+                if (P.q_box) {
+                    // (rows past R are the next sequence's or zeros: finite or not,
+                    // they end in columns of the products that nobody reads)
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&q_full[qb], (uint32_t)halves * RT * 128u);
+                        for (int half = 0; half < halves; ++half)
+                            tma_load_3d(qs + half * RT * 128, &P.map_q, half * 64, h * group, q.t0 + rt * RT / group,
+                                        &q_full[qb]);
+                    }
+                    __syncwarp();
+                    return;
+                }
                 for (int m = lane / cpr, c = lane % cpr; m < RT;) {
                     const T *src = static_cast<const T *>(a.q);
                     if (m < R) {
@@ -529,7 +529,13 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
                     if (c >= cpr) c -= cpr, ++m;
                 }
                 cp_async_arrive(&q_full[qb]);
-            }
+            };
+            if (i < S::kQ && P.q_box) bring_q();
+            else if (P.q_box && lane < halves)  // its buffer is in use: as far as L2
+                tma_prefetch_3d(&P.map_q, lane * 64, h * group, q.t0 + rt * RT / group);
+            for (int r = lane; r < R; r += 32) place[r] = row_place(P, q.t0, h, rt * RT + r);
+            __syncwarp();
+            if (i < S::kQ && !P.q_box) bring_q();
             if (build) {
                 // see[j]: the rows that see tree node j.  Every node of this row
                 // tile marks itself and its ancestors with its rows' bits.
@@ -561,6 +567,10 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
             if (tree) see_user[see] = i;
             __syncwarp();
             if (lane == 0) mbar_arrive(&aux_full[i % kSegs]);
+            if (i >= S::kQ) {
+                await(&q_empty[qb], (uint32_t)(i / S::kQ - 1) & 1, lost);
+                bring_q();
+            }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp > kWalkWarp) {
@@ -791,7 +801,6 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
         };
         const float c = P.c;
         float l[S::kRows];
-        volatile Segment &cur = s_cur;
         int g = 0;              // tile
         // K of tile g is the ring's operand 2g, V is 2g + 1.  The commit that
         // frees K's stage is the signal that the scores are there: the stage can
@@ -804,14 +813,16 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
             await(&pv_done, (uint32_t)g & 1, lost);
             tc_fence_after();
         };
+        // (one warp looks, so that all agree even when waits have run out)
+        auto look = [&](int seg) {
+            const Segment &s = wait_segment(seg);
+            if (lane == 0) s_cur[seg & 1] = s;
+        };
+        if (warp == 0) look(0);
         for (int seg = 0;; ++seg) {
             named_sync<6, S::kSoft>();  // every thread is done with the last segment
-            if (warp == 0) {
-                if (lane == 0 && seg > 0) mbar_arrive(&seg_empty[(seg - 1) % kSegs]);
-                const Segment &s = wait_segment(seg);
-                if (lane == 0) s_cur = s;
-            }
-            named_sync<6, S::kSoft>();
+            if (tid == 0 && seg > 0) mbar_arrive(&seg_empty[(seg - 1) % kSegs]);
+            volatile Segment &cur = s_cur[seg & 1];
             const int prefix = cur.prefix, end = cur.end, first = cur.tile;
             if (end == 0) break;
             const int R = min(RT, cur.n * group - cur.rt * RT);  // rows in use
@@ -884,9 +895,9 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
                         s_ref[r] = -now;
                     }
                     group_bar(wg);
-#pragma unroll
-                    for (int r = 0; r < S::kRows; ++r) l[r] *= s_fac[r0 + r];
                     if (tile != first) {
+#pragma unroll
+                        for (int r = 0; r < S::kRows; ++r) l[r] *= s_fac[r0 + r];
                         pv_finished(g - 1);
                         tmem_load(t_o, s);
 #pragma unroll
@@ -911,12 +922,10 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
                     // brought from the last page past the end: zeroed
                     const int v0 = max(0, cur.prefix - tile * P.tok), v1 = min(P.tok, cur.total - tile * P.tok);
                     const int ve = P.box ? (v1 + P.box - 1) / P.box * P.box : v1;
-                    const int cpr = D / 8;
-                    const int pv = 2 * g + 1;
+                    const int pv = 2 * g + 1, cc = tid & 15;  // 16 lanes per token
                     await(&full[pv % S::kStages], (uint32_t)(pv / S::kStages) & 1, lost);
                     uint8_t *const vt = sm + (uint32_t)(pv % S::kStages) * kStage;
-                    for (int i = tid; i < (ve - v0) * cpr; i += S::kSoft) {
-                        const int m = v0 + i / cpr, cc = i % cpr;
+                    for (int m = v0 + (tid >> 4); m < ve && cc * 8 < D; m += S::kSoft / 16) {
                         uint8_t *const at = vt + (uint32_t)(cc >> 3) * kHalf + sw128_offset(m, cc & 7);
                         if (m >= v1) {
                             sts128(at, make_uint4(0, 0, 0, 0));
@@ -1019,6 +1028,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
                         if (r0 + i < R) part[i * 128] = v[i];
                 }
             }
+            if (warp == 0) look(seg + 1);
         }
         if (tid == 0 && *lost) set_error(P.err, kErrTimeout);
     }
