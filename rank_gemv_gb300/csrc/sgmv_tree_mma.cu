@@ -2,13 +2,14 @@
 // 128 columns.
 //
 // The rows of one sequence that share a KV head (nodes x query heads of the
-// group) are cut into row tiles of RT = 16, 32, 64 or 128, the tokens into
+// group) are cut into row tiles of RT = 8, 16, 32, 64 or 128, the tokens into
 // tiles of 128.  Both products run transposed, so that the long axis (tokens,
 // then head columns) fills the 128 lanes of the tensor cores however few rows
 // there are:
 //
 //   S^T [tokens x RT] = K . Q^T          A = K tile (K-major),  B = Q rows
 //   O^T [columns x RT] += V^T . P^T      A = V tile (M-major),  B = P
+// (of 16 columns at least: with RT = 8 nobody reads the others)
 //
 // with S^T and O^T in tensor memory.  A softmax thread owns one token: it
 // reads its scores, makes p = 2^(c s - ref[row]) and writes them as one row
@@ -27,7 +28,7 @@
 // bandwidth, but its parts and joins cost more than it won: 188, 287 and 67 us against
 // 182, 275 and 61 on 32 trees, 64 heads on 8, and 128 decode rows.)
 //
-// Warps: 4, 4, 8 or 16 for the softmax (32 rows each four); one that issues the
+// Warps: 4, 4, 4, 8 or 16 for the softmax (32 rows each four); one that issues the
 // MMAs, a score product ahead of the softmax; one that walks the line,
 // brings Q in and says which rows see which tree nodes; two that bring K and V
 // into a ring of 32 KB stages, through the block table: by TMA, or, for pages
@@ -67,6 +68,7 @@ constexpr int kMaxParts = 64;            // parts of an item (about)
 template <int RT> struct Shape {
     static constexpr int kGroups = RT > 32 ? RT / 32 : 1;  // softmax warpgroups
     static constexpr int kRows = RT / kGroups;            // rows per warpgroup
+    static constexpr int kN = RT < 16 ? 16 : RT;          // columns of the products, the least there is
     static constexpr int kSoft = 128 * kGroups;           // softmax threads
     static constexpr int kThreads = kSoft + 64 + kLoaders;
     // Two CTAs per SM where they fit: one's sums and segment changes hide behind
@@ -76,7 +78,7 @@ template <int RT> struct Shape {
     static constexpr int kQ = RT > 64 || kPerSm > 1 ? 1 : 2;  // Q buffers
     static constexpr int kStages = kPerSm > 1 ? 3 : RT > 64 ? 4 : 5;
     static constexpr int kWords = RT < 32 ? 1 : RT / 32;  // words of one bit per row
-    static constexpr uint32_t kQBytes = RT * 256u;
+    static constexpr uint32_t kQBytes = kN * 256u;
     // A token's row of P: 64 columns of 128-byte swizzle, or 16 of 32-byte swizzle
     static constexpr uint32_t kPRow = RT <= 16 ? 32 : 128;
     static constexpr uint32_t kPBytes = (RT > 64 ? 2 : 1) * kTok * kPRow;
@@ -248,13 +250,22 @@ template <int N> __device__ __forceinline__ void tmem_load(uint32_t addr, float 
     __syncwarp();
     if constexpr (N == 32)
         tmem_ld32(addr, v);
-    else
+    else if constexpr (N == 16)
         tmem_ld16(addr, v);
+    else
+        tmem_ld8(addr, v);
 }
 template <int N> __device__ __forceinline__ void tmem_store(uint32_t addr, const float (&v)[N]) {
     __syncwarp();
+    if constexpr (N == 8)
+        asm volatile(
+            "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr),
+            "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+            "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
+            "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
+            : "memory");
 #pragma unroll
-    for (int i = 0; i < N; i += 16)
+    for (int i = 0; i + 16 <= N; i += 16)
         asm volatile(
             "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
             "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr + i),
@@ -511,7 +522,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
                     if (lane == 0) {
                         mbar_arrive_expect_tx(&q_full[qb], (uint32_t)halves * RT * 128u);
                         for (int half = 0; half < halves; ++half)
-                            tma_load_3d(qs + half * RT * 128, &P.map_q, half * 64, h * group, q.t0 + rt * RT / group,
+                            tma_load_3d(qs + half * S::kN * 128, &P.map_q, half * 64, h * group, q.t0 + rt * RT / group,
                                         &q_full[qb]);
                     }
                     __syncwarp();
@@ -523,7 +534,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
                         const int2 at = place[m];
                         src += (int64_t)(at.x < 0 ? ~at.x : at.x) * a.q_token + (int64_t)at.y * a.q_head + c * 8;
                     }
-                    cp_async16(qs + (uint32_t)(c >> 3) * (RT * 128u) + sw128_offset(m, c & 7), src, m < R ? 16u : 0u);
+                    cp_async16(qs + (uint32_t)(c >> 3) * (S::kN * 128u) + sw128_offset(m, c & 7), src, m < R ? 16u : 0u);
                     m += 32 / cpr;
                     c += 32 % cpr;
                     if (c >= cpr) c -= cpr, ++m;
@@ -706,8 +717,8 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
         }
     } else if (warp == kMmaWarp) {
         // ---- MMA issuer ------------------------------------------------------
-        const uint32_t idesc_s = idesc_f16(kBf16, kTok, RT) & ~(1u << 16);   // both K-major
-        const uint32_t idesc_o = idesc_f16(kBf16, kTok, RT) | (1u << 15);  // both MN-major
+        const uint32_t idesc_s = idesc_f16(kBf16, kTok, S::kN) & ~(1u << 16);   // both K-major
+        const uint32_t idesc_o = idesc_f16(kBf16, kTok, S::kN) | (1u << 15);  // both MN-major
         const uint32_t ring = smem_addr(sm), on = elect();
         // descriptors of the first stage and buffers; offsets add to them (bytes / 16)
         const uint64_t k_desc = sw128_desc(ring, 16, 1024), v_desc = sw128_desc(ring, kHalf, 1024);
@@ -748,13 +759,13 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
             tc_fence_after();
             const uint64_t kd = k_desc + (uint32_t)k_st * (kStage >> 4);
             const uint64_t qd = q_desc + (uint32_t)qb * (S::kQBytes >> 4);
-            const uint32_t d = tmem + (uint32_t)((g & 1) * RT);
+            const uint32_t d = tmem + (uint32_t)((g & 1) * S::kN);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) mma_on(on, d, kd + kk * 2, qd + kk * 2, idesc_s, kk != 0);
             if (wide) {
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_on(on, d, kd + (kHalf >> 4) + kk * 2, qd + RT * 8u + kk * 2, idesc_s, 1);
+                    mma_on(on, d, kd + (kHalf >> 4) + kk * 2, qd + S::kN * 8u + kk * 2, idesc_s, 1);
             }
             commit_on(on, &empty[k_st]);  // also tells the softmax that the scores are there
             if (left == 0) commit_on(on, &q_empty[qb]);
@@ -777,7 +788,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
                 const uint64_t vd = v_desc + (uint32_t)v_st * (kStage >> 4);
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                    mma_on(on, tmem + 2 * RT, vd + kk * 128, p_desc + kk * p_step, idesc_o, kk ? 1u : (uint32_t)t);
+                    mma_on(on, tmem + 2 * S::kN, vd + kk * 128, p_desc + kk * p_step, idesc_o, kk ? 1u : (uint32_t)t);
                 commit_on(on, &empty[v_st]);
                 commit_on(on, &pv_done);
                 skip(v_st, v_ph);
@@ -793,7 +804,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
         // ---- softmax and output: thread = token, then = head column ------------
         const int wg = warp >> 2, tok = tid & 127, r0 = wg * S::kRows, d = tok;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t t_s = tmem + lanes + (uint32_t)r0, t_o = tmem + lanes + 2 * RT + (uint32_t)r0;
+        const uint32_t t_s = tmem + lanes + (uint32_t)r0, t_o = tmem + lanes + 2 * S::kN + (uint32_t)r0;
         // where this thread's 16-byte pieces of P go
         auto p_at = [&](int q) {
             return sm + S::kOffP + (S::kPRow == 128 ? (uint32_t)(wg >> 1) * kHalf + sw128_offset(tok, (wg & 1) * 4 + q)
@@ -837,7 +848,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
                     await(&aux_full[seg % kSegs], (uint32_t)(seg / kSegs) & 1, lost);
                     aux = true;
                 }
-                const uint32_t ts = t_s + (uint32_t)((g & 1) * RT);
+                const uint32_t ts = t_s + (uint32_t)((g & 1) * S::kN);
                 // which rows see this token: all, none, or a node's
                 const int j = tile * P.tok + tok;
                 const bool tree = (tile + 1) * P.tok > prefix, edge = tree || P.tok < kTok;
@@ -1095,8 +1106,12 @@ int launch(const MmaParams &p, int ctas, cudaStream_t stream) {
     return spec_launch(sgmv_tree_join_kernel<T, RT>, dim3(8 * kMaxSms), kJoinThreads, 0, 1, stream, p);
 }
 
-// Rows per tile: what a sequence of average length fills.
+// Rows per tile: what a sequence of average length fills.  8 rows are half the
+// softmax's work of 16 (512 sequences of 100 tokens, 32 heads on 8: 62 us against 74; 256 of
+// 512 tokens: 76 against 89), but only where each sequence has one token: a ragged
+// batch's larger trees would read K and V twice for it.
 int row_tile(int32_t T, int32_t B, int32_t group) {
+    if (T <= B && group <= 8) return 8;
     const int64_t rows = ((int64_t)T + B - 1) / B * group;
     return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
 }
@@ -1104,7 +1119,7 @@ int row_tile(int32_t T, int32_t B, int32_t group) {
 constexpr size_t kHeadBytes = 256;
 
 // CTAs, and so shares, at most.
-int max_ctas(int rt) { return kMaxSms * (rt == 16 ? Shape<16>::kPerSm : 1); }
+int max_ctas(int rt) { return kMaxSms * (rt <= 16 ? Shape<16>::kPerSm : 1); }
 
 }  // namespace
 
@@ -1167,6 +1182,7 @@ int tree_mma_launch(const sgmv_tree_attention_args &a, int nsm, int *err, cudaSt
     const bool h = a.dtype == SGMV_F16;
     using B16 = __nv_bfloat16;
     switch (rt) {
+        case 8: return h ? launch<__half, 8>(p, ctas, stream) : launch<B16, 8>(p, ctas, stream);
         case 16: return h ? launch<__half, 16>(p, ctas, stream) : launch<B16, 16>(p, ctas, stream);
         case 32: return h ? launch<__half, 32>(p, ctas, stream) : launch<B16, 32>(p, ctas, stream);
         case 64: return h ? launch<__half, 64>(p, ctas, stream) : launch<B16, 64>(p, ctas, stream);

@@ -161,6 +161,28 @@ def test_much_work(sgmv, group, n, Hkv, prefix, B, bs):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("group,Hkv,D", [(1, 4, 128), (2, 2, 64), (3, 2, 80), (5, 1, 128), (8, 2, 96), (9, 1, 64)])
+@pytest.mark.parametrize("nodes", ["one", "uneven", "padded"])
+@pytest.mark.parametrize("bs", [16, 24, 5])
+def test_a_token_per_sequence(sgmv, dtype, group, Hkv, D, nodes, bs):
+    """Decoding without drafts; and as many rows in all, but with sequences that
+    have none or several of them, or rows that are padding.  Short and long contexts, scores
+    that grow along one of them (its running maximum moves)."""
+    prefix = [0, 1, 127, 128, 4000, 16, 300, 1100]
+    counts = {"one": [1] * 8, "uneven": [0, 9, 1, 0, 1, 3, 0, 2], "padded": [1] * 8}[nodes]
+    trees = None
+    if nodes == "padded":
+        trees = [[-2] if s in (1, 4) else [-1] for s in range(8)]
+    b = Batch(prefix, counts, group * Hkv, Hkv, D, bs, dtype, seed=group + bs, parents=trees or "random")
+    at = torch.tensor(ref.slots_of(b.table, 7, range(b.total[7]), bs), device="cuda")
+    grow = torch.linspace(0, 4.0, len(at), device="cuda")[:, None, None].to(dtype)
+    b.k.view(-1, Hkv, D)[at] *= grow
+    b.dirty().run(sgmv)
+    check_error_word(0)
+    b.check()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("n", [1, 4, 31, 200])
 def test_chains_without_parents(sgmv, dtype, n):
     b = Batch([150, 0, 3], [n, n, 1], 4, 1, 64, 32, dtype, seed=n, parents=None).dirty().run(sgmv)
