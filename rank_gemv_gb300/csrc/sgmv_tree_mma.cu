@@ -843,15 +843,43 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
 #pragma unroll
             for (int r = 0; r < S::kRows; ++r) l[r] = 0.f;
             for (int tile = first; tile < end; ++tile, ++g) {
+                const bool tree = (tile + 1) * P.tok > prefix, edge = tree || P.tok < kTok;
+                if (tree) {
+                    // while the scores are made: non-finite v of tree nodes, out of the
+                    // tile and noted; what TMA brought from the last page past the end, zeroed
+                    const int v0 = max(0, cur.prefix - tile * P.tok), v1 = min(P.tok, cur.total - tile * P.tok);
+                    const int ve = P.box ? (v1 + P.box - 1) / P.box * P.box : v1;
+                    const int pv = 2 * g + 1, cc = tid & 15;  // 16 lanes per token
+                    await(&full[pv % S::kStages], (uint32_t)(pv / S::kStages) & 1, lost);
+                    uint8_t *const vt = sm + (uint32_t)(pv % S::kStages) * kStage;
+                    for (int m = v0 + (tid >> 4); m < ve && cc * 8 < D; m += S::kSoft / 16) {
+                        uint8_t *const at = vt + (uint32_t)(cc >> 3) * kHalf + sw128_offset(m, cc & 7);
+                        if (m >= v1) {
+                            sts128(at, make_uint4(0, 0, 0, 0));
+                            continue;
+                        }
+                        uint4 u = lds128(at);
+                        uint32_t *const x = reinterpret_cast<uint32_t *>(&u);
+                        bool any = false;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            if (bad16<T>(x[q])) any = true, x[q] &= 0xffff0000u;
+                            if (bad16<T>(x[q] >> 16)) any = true, x[q] &= 0xffffu;
+                        }
+                        if (any) {
+                            s_poison = seg;
+                            sts128(at, u);
+                        }
+                    }
+                }
                 scores_done(g);
-                if (!aux && (tile + 1) * P.tok > prefix) {
+                if (!aux && tree) {
                     await(&aux_full[seg % kSegs], (uint32_t)(seg / kSegs) & 1, lost);
                     aux = true;
                 }
                 const uint32_t ts = t_s + (uint32_t)((g & 1) * S::kN);
                 // which rows see this token: all, none, or a node's
                 const int j = tile * P.tok + tok;
-                const bool tree = (tile + 1) * P.tok > prefix, edge = tree || P.tok < kTok;
                 uint32_t vis = 0xffffffffu;
                 if (edge && (tok >= P.tok || j >= prefix))
                     vis = tok < P.tok && j < cur.total ? see[(j - prefix) * S::kWords] : 0u;
@@ -928,34 +956,6 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
 #pragma unroll
                 for (int q = 0; q < S::kRows / 8; ++q)
                     sts128(p_at(q), make_uint4(p[4 * q], p[4 * q + 1], p[4 * q + 2], p[4 * q + 3]));
-                if (tree) {
-                    // non-finite v of tree nodes: out of the tile, noted; what TMA
-                    // brought from the last page past the end: zeroed
-                    const int v0 = max(0, cur.prefix - tile * P.tok), v1 = min(P.tok, cur.total - tile * P.tok);
-                    const int ve = P.box ? (v1 + P.box - 1) / P.box * P.box : v1;
-                    const int pv = 2 * g + 1, cc = tid & 15;  // 16 lanes per token
-                    await(&full[pv % S::kStages], (uint32_t)(pv / S::kStages) & 1, lost);
-                    uint8_t *const vt = sm + (uint32_t)(pv % S::kStages) * kStage;
-                    for (int m = v0 + (tid >> 4); m < ve && cc * 8 < D; m += S::kSoft / 16) {
-                        uint8_t *const at = vt + (uint32_t)(cc >> 3) * kHalf + sw128_offset(m, cc & 7);
-                        if (m >= v1) {
-                            sts128(at, make_uint4(0, 0, 0, 0));
-                            continue;
-                        }
-                        uint4 u = lds128(at);
-                        uint32_t *const x = reinterpret_cast<uint32_t *>(&u);
-                        bool any = false;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            if (bad16<T>(x[q])) any = true, x[q] &= 0xffff0000u;
-                            if (bad16<T>(x[q] >> 16)) any = true, x[q] &= 0xffffu;
-                        }
-                        if (any) {
-                            s_poison = seg;
-                            sts128(at, u);
-                        }
-                    }
-                }
                 fence_proxy_async();
                 tc_fence_before();
                 __syncwarp();  // one arrival per warp: a warp's own 32 would be served one by one
@@ -975,20 +975,25 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
             const bool whole = cur.whole != 0;
             const int slot = cur.slot;
             const int2 *const place = reinterpret_cast<const int2 *>(sm + S::kOffRow) + (seg % kSegs) * RT;
-            if (tok < S::kRows) {
-                const int r = r0 + tok;
-                const float L = s_red[0][r] + s_red[1][r] + s_red[2][r] + s_red[3][r], ref = -s_ref[r];
-                if (!whole) {
-                    *reinterpret_cast<float2 *>(P.ml + ((int64_t)slot * RT + r) * 2) = make_float2(ref, L);
+            // One warp does the factors, another the rest.  (A row that saw anything has
+            // a weight of 2^kBias or more: the approximations of 1 / L and log2 L are at
+            // their 2^-22 or so.)
+            if ((tok & 31) < S::kRows && tok < 64) {
+                const int r = r0 + (tok & 31);
+                const float L = s_red[0][r] + s_red[1][r] + s_red[2][r] + s_red[3][r];
+                const int2 to = place[r < R ? r : 0];
+                const bool none = to.x < 0 || L == 0.f;
+                if (tok < 32) {
+                    s_fac[r] = none ? 0.f : __fdividef(1.f, L);
                 } else {
-                    const int2 to = place[r < R ? r : 0];
-                    const bool none = to.x < 0 || L == 0.f;
-                    s_fac[r] = none ? 0.f : 1.f / L;
-                    if (a.lse && r < R)
+                    const float ref = -s_ref[r];
+                    if (!whole)
+                        *reinterpret_cast<float2 *>(P.ml + ((int64_t)slot * RT + r) * 2) = make_float2(ref, L);
+                    else if (a.lse && r < R)
                         a.lse[(int64_t)(to.x < 0 ? ~to.x : to.x) * a.Hq + to.y] =
-                            none ? -INFINITY : (ref + log2f(L)) * 0.693147180559945309f;
+                            none ? -INFINITY : (ref + __log2f(L)) * 0.693147180559945309f;
+                    s_ref[r] = -kUnset;
                 }
-                s_ref[r] = -kUnset;
             }
             pv_finished(g - 1);
             group_bar(wg);
@@ -1017,8 +1022,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
                     uint8_t *const rows = sm + S::kOffP + r0 * 256;
 #pragma unroll
                     for (int i = 0; i < S::kRows; i += 2) {
-                        const float f0 = s_fac[r0 + i], f1 = s_fac[r0 + i + 1];
-                        const uint32_t two = pack2<T>(f0 == 0.f ? 0.f : v[i] * f0, f1 == 0.f ? 0.f : v[i + 1] * f1);
+                        const uint32_t two = pack2<T>(v[i] * s_fac[r0 + i], v[i + 1] * s_fac[r0 + i + 1]);
                         sts16(rows + i * 256 + d * 2, (uint16_t)two);
                         sts16(rows + (i + 1) * 256 + d * 2, (uint16_t)(two >> 16));
                     }
@@ -1030,7 +1034,9 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
                         T *const out = static_cast<T *>(a.out) + (int64_t)(to.x < 0 ? ~to.x : to.x) * a.out_token +
                                        (int64_t)to.y * a.out_head;
                         const int col = (tok & 15) * 8;
-                        if (col < D && ok) *reinterpret_cast<uint4 *>(out + col) = lds128(rows + m * 256 + col * 2);
+                        if (col < D && ok)  // (no weights at all: zeros, whatever v holds)
+                            *reinterpret_cast<uint4 *>(out + col) =
+                                s_fac[r0 + m] == 0.f ? make_uint4(0, 0, 0, 0) : lds128(rows + m * 256 + col * 2);
                     }
                 } else {
                     float *const part = P.part + ((int64_t)slot * RT + r0) * 128 + d;
