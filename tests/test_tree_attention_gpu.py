@@ -183,6 +183,20 @@ def test_a_token_per_sequence(sgmv, dtype, group, Hkv, D, nodes, bs):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("group,tree", [(1, [-1]), (4, [-1, 0, -2, 0, 1]), (16, [-1, 0, 1, 2, 3, 4, 5, 6, 7])])
+@pytest.mark.parametrize("prefix", [1100, 20000])
+def test_one_sequence_in_many_parts(sgmv, dtype, group, tree, prefix):
+    """A single sequence and KV head, cut into as many parts as there are, with
+    scores that grow (parts differ in their maxima) and a row that sees nothing."""
+    b = Batch([prefix], None, group, 1, 64, 16, dtype, seed=group, parents=[tree])
+    at = torch.tensor(ref.slots_of(b.table, 0, range(b.total[0]), 16), device="cuda")
+    b.k.view(-1, 1, 64)[at] *= torch.linspace(0, 3.0, len(at), device="cuda")[:, None, None].to(dtype)
+    b.dirty().run(sgmv)
+    check_error_word(0)
+    b.check()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("n", [1, 4, 31, 200])
 def test_chains_without_parents(sgmv, dtype, n):
     b = Batch([150, 0, 3], [n, n, 1], 4, 1, 64, 32, dtype, seed=n, parents=None).dirty().run(sgmv)
