@@ -64,6 +64,7 @@ constexpr float kSlack = 8.f;            // ... <= 2^(kBias + kSlack), finite in
 constexpr int kMaxSms = 152;
 constexpr int kSeqTable = 64;            // entries of the table that finds a tile's sequence
 constexpr int kMaxParts = 64;            // parts of an item (about)
+constexpr int kEnd = 1;                  // what an item's end costs, in tiles
 
 template <int RT> struct Shape {
     static constexpr int kGroups = RT > 32 ? RT / 32 : 1;  // softmax warpgroups
@@ -164,7 +165,7 @@ struct Sequence {
         items = (uint32_t)P.a.Hkv * (uint32_t)nrt;
         return true;
     }
-    __device__ __forceinline__ int64_t work() const { return (int64_t)items * tiles; }
+    __device__ __forceinline__ int64_t work() const { return (int64_t)items * (tiles + kEnd); }
 };
 
 // Bounded wait of a whole warp.  When one runs out (or another role's did),
@@ -462,8 +463,22 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
             base = plan.before[lo];
             q.template enter<RT>(P, lo * plan.stride, &plan);
         }
+        if (lane == 0) P.cut[id] = Cut{};
         for (int i = 0;; ++i) {
             if (i >= kSegs) await(&seg_empty[i % kSegs], (uint32_t)(i / kSegs - 1) & 1, lost);
+            uint32_t item = 0;
+            int tile = 0;
+            while (w < w1) {
+                while (w >= base + q.work()) {
+                    base += q.work();
+                    q.template enter<RT>(P, q.b + 1, &plan);
+                }
+                const uint32_t rel = (uint32_t)(w - base), each = (uint32_t)(q.tiles + kEnd);
+                item = rel / each;
+                tile = (int)(rel - item * each);
+                if (tile < q.tiles) break;
+                w += (int)each - tile;  // nothing to do for an end itself
+            }
             if (w >= w1) {
                 if (lane == 0) {
                     s_seg[i % kSegs].tile = s_seg[i % kSegs].end = 0;
@@ -471,13 +486,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
                 }
                 break;
             }
-            while (w >= base + q.work()) {
-                base += q.work();
-                q.template enter<RT>(P, q.b + 1, &plan);
-            }
-            const uint32_t rel = (uint32_t)(w - base), item = rel / (uint32_t)q.tiles;
             const int h = (int)(item / (uint32_t)q.nrt), rt = (int)(item - (uint32_t)h * (uint32_t)q.nrt);
-            const int tile = (int)(rel - item * (uint32_t)q.tiles);
             const int end = w1 - w < q.tiles - tile ? tile + (int)(w1 - w) : q.tiles;
             const bool tree = end * P.tok > q.prefix, build = tree && (see_b != q.b || see_rt != rt);
             if (build) see ^= 1;
@@ -495,16 +504,14 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
                 s.whole = tile == 0 && end == q.tiles;
                 s.slot = 2 * id + (tile == 0 ? 1 : 0);
                 s.see = see;
-                if (w + (end - tile) == w1) {  // the share's last: the only item that it may begin and not end
+                if (tile == 0 && !s.whole) {  // the share's last: the only item that it may begin and not end
                     Cut cut = {};
-                    if (tile == 0 && !s.whole) {
-                        cut.t0 = q.t0;
-                        cut.n = q.n;
-                        cut.h = h;
-                        cut.rt = rt;
-                        cut.first = id;
-                        cut.parts = (int)((w + q.tiles - 1) / plan.own) - id + 1;
-                    }
+                    cut.t0 = q.t0;
+                    cut.n = q.n;
+                    cut.h = h;
+                    cut.rt = rt;
+                    cut.first = id;
+                    cut.parts = (int)((w + q.tiles - 1) / plan.own) - id + 1;
                     P.cut[id] = cut;
                 }
                 *(volatile int *)&s_known = i + 1;
