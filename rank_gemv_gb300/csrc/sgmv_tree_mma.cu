@@ -18,8 +18,8 @@
 // ordinary tile needs one vote and no reduction over tokens.
 //
 // Decomposition: the (sequence, head, row tile) items, each of ceil(length /
-// 128) token tiles, form one line of work that is cut into equal shares, one
-// per CTA of a grid that fills the GPU once.  A share that covers an item
+// 128) token tiles and one or two more for what its end costs, form one line of work
+// that is cut into equal shares, one per CTA of a grid that fills the GPU once.  A share that covers an item
 // writes its output; items cut across shares leave unnormalised O, sums and
 // references in the workspace, and a second, small kernel joins them, in share
 // order.  (Joined by whichever CTA finished last, behind a fence and a counter, each join
@@ -64,7 +64,6 @@ constexpr float kSlack = 8.f;            // ... <= 2^(kBias + kSlack), finite in
 constexpr int kMaxSms = 152;
 constexpr int kSeqTable = 64;            // entries of the table that finds a tile's sequence
 constexpr int kMaxParts = 64;            // parts of an item (about)
-constexpr int kEnd = 1;                  // what an item's end costs, in tiles
 
 template <int RT> struct Shape {
     static constexpr int kGroups = RT > 32 ? RT / 32 : 1;  // softmax warpgroups
@@ -78,6 +77,10 @@ template <int RT> struct Shape {
     static constexpr int kPerSm = RT <= 16 ? 2 : 1;
     static constexpr int kQ = RT > 64 || kPerSm > 1 ? 1 : 2;  // Q buffers
     static constexpr int kStages = kPerSm > 1 ? 3 : RT > 64 ? 4 : 5;
+    // What an item costs beside its tiles, in tiles: with 0, 1 and 2, 32 trees over 4096
+    // tokens took 202, 191 and 191 us (32 nodes, RT 32), 227, 209 and 204 (64), 155,
+    // 145 and 137 (64 nodes, 32 heads on 8, RT 128; 136 with 3).
+    static constexpr int kEnd = RT > 32 ? 2 : 1;
     static constexpr int kWords = RT < 32 ? 1 : RT / 32;  // words of one bit per row
     static constexpr uint32_t kQBytes = kN * 256u;
     // A token's row of P: 64 columns of 128-byte swizzle, or 16 of 32-byte swizzle
@@ -127,7 +130,7 @@ struct Segment {
     int see;                         // which tree table
 };
 
-// How the line of W tiles is cut: share i is tiles [i own, (i + 1) own).
+// How the line of W tiles (ends counted) is cut: share i is [i own, (i + 1) own).
 struct Plan {
     int64_t W, own;
     int32_t stride;
@@ -137,7 +140,7 @@ struct Plan {
 
 // A sequence's part of the line.
 struct Sequence {
-    int b, t0, n, prefix, total, tiles, nrt;
+    int b, t0, n, prefix, total, tiles, nrt, each;  // each: an item's place on the line
     uint32_t items;
 
     // false: bad metadata
@@ -154,18 +157,19 @@ struct Sequence {
             prefix = a.prefix_lens[b];
         }
         items = 0;
-        tiles = 1;
+        tiles = each = 1;
         if (!(t0 >= 0 && n >= 0 && n <= SGMV_TREE_MAX_NODES && (int64_t)t0 + n <= a.T && prefix >= 0 &&
               (int64_t)prefix + n <= (int64_t)a.max_blocks * a.block_size && prefix <= INT_MAX - 2 * kTok - n))
             return false;
         if (n == 0) return true;
         total = prefix + n;
         tiles = (total + P.tok - 1) / P.tok;
+        each = tiles + Shape<RT>::kEnd;
         nrt = (n * P.group + RT - 1) / RT;
         items = (uint32_t)P.a.Hkv * (uint32_t)nrt;
         return true;
     }
-    __device__ __forceinline__ int64_t work() const { return (int64_t)items * (tiles + kEnd); }
+    __device__ __forceinline__ int64_t work() const { return (int64_t)items * each; }
 };
 
 // Bounded wait of a whole warp.  When one runs out (or another role's did),
@@ -473,11 +477,11 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
                     base += q.work();
                     q.template enter<RT>(P, q.b + 1, &plan);
                 }
-                const uint32_t rel = (uint32_t)(w - base), each = (uint32_t)(q.tiles + kEnd);
-                item = rel / each;
-                tile = (int)(rel - item * each);
+                const uint32_t rel = (uint32_t)(w - base);
+                item = rel / (uint32_t)q.each;
+                tile = (int)(rel - item * (uint32_t)q.each);
                 if (tile < q.tiles) break;
-                w += (int)each - tile;  // nothing to do for an end itself
+                w += q.each - tile;  // nothing to do for an end itself
             }
             if (w >= w1) {
                 if (lane == 0) {
