@@ -18,9 +18,10 @@
 // ordinary tile needs one vote and no reduction over tokens.
 //
 // Decomposition: the (sequence, head, row tile) items, each of ceil(length /
-// 128) token tiles and one or two more for what its end costs, form one line of work
-// that is cut into equal shares, one per CTA of a grid that fills the GPU once.  A share that covers an item
-// writes its output; items cut across shares leave unnormalised O, sums and
+// 128) token tiles and one or two more for what its end costs, form one line of
+// work that is cut into equal shares, one per CTA of a grid that fills the GPU
+// once.  A share that covers an item writes its output; items cut across shares
+// leave unnormalised O, sums and
 // references in the workspace, and a second, small kernel joins them, in share
 // order.  (Joined by whichever CTA finished last, behind a fence and a counter, each join
 // took 15 us: its chain of loads queued behind the stream of K and V.  Claiming the
