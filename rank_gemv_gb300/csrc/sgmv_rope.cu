@@ -101,15 +101,12 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
     else if (slot != -1 && tid == 0)
         set_error(err, kErrBadIndex);
     __syncthreads();
-    // this piece's angles; pairs that do not turn (an interleaved vector that
-    // the last pair ends inside of) keep their columns by cosine 1, sine 0
+    // this piece's angles (an interleaved vector may hold columns past the last
+    // pair: those are left as they are below, and their angles are not used)
     float2 r[kAngles];
     if (turns) {
 #pragma unroll
-        for (int e = 0; e < kAngles; ++e) {
-            const int i = w * kAngles + e;
-            r[e] = MODE != kInterleaved || i < pairs ? s_angle[i] : make_float2(1.f, 0.f);
-        }
+        for (int e = 0; e < kAngles; ++e) r[e] = s_angle[w * kAngles + e];
     }
     T *const qo = static_cast<T *>(a.q_out) + t * a.q_out_token + c;
     T *const ko = a.k_out ? static_cast<T *>(a.k_out) + t * a.k_out_token + c : nullptr;
@@ -140,8 +137,10 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
                         for (int i = 0; i < 4; ++i) {
                             float p, q;
                             unpack2<T>(xs[i], p, q);
-                            xs[i] = pack2<T>(p * r[i % kAngles].x - q * r[i % kAngles].y,
-                                             p * r[i % kAngles].y + q * r[i % kAngles].x);
+                            const uint32_t turned = pack2<T>(p * r[i % kAngles].x - q * r[i % kAngles].y,
+                                                             p * r[i % kAngles].y + q * r[i % kAngles].x);
+                            // (a select: cosine 1 and sine 0 would make NaN of an infinity's neighbour)
+                            if (w * 4 + i < pairs) xs[i] = turned;
                         }
                     } else {
 #pragma unroll
