@@ -112,9 +112,21 @@ _PTR_ARRAYS = [None] + [ctypes.c_void_p * n for n in range(1, 5)]
 
 
 def _stream(device):
-    """Handle of the current stream (without a Stream object, which costs a microsecond)."""
+    """Handle of the current stream (without a Stream object, which costs a microsecond).
+    A device that is not a GPU is refused: a kernel could not use its addresses."""
     index = device.index
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
+    if index is None:  # not a tensor's on a GPU
+        if device.type != "cuda":
+            raise ValueError(f"Expected a cuda device, but got: {device}")
+        index = torch.cuda.current_device()
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _on_gpu(tensors):
+    """Every tensor a kernel is to read or write (None: not given) must be on the GPU."""
+    for t in tensors:
+        if t is not None and not t.is_cuda:
+            raise ValueError(f"Expected a cuda device, but got a tensor on: {t.device}")
 
 
 def _meta(t, name):
@@ -501,6 +513,7 @@ def sgmv_rope(q, k, positions, inv_freq, interleaved=False, scale=1.0, inverse=F
         _list(slots, "slots", T), inv_freq.data_ptr(), qo[1], qo[2], qi[1], qi[2], ko[1], ko[2],
         ki[1], ki[2], vi[1], vi[2], cs[0], cs[1], cs[2], T, Hq, Hk, D, inv_freq.numel(), blocks, bs,
         _DTYPES[dtype], interleaved, inverse, scale)
+    _on_gpu((q, k, q_out, k_out, v, k_cache, v_cache, positions, slots))
     _check(load_library().sgmv_rope(args, _stream(first.device)), "sgmv_rope")
     return q_out, k_out
 
@@ -543,6 +556,7 @@ def sgmv_tree_attention(out, q, k_cache, v_cache, block_table, prefix_lens, tree
         workspace.numel() * workspace.element_size(), oo[1], oo[2], qi[1], qi[2], cs[0], cs[1],
         cs[2], row, T, B, Hq, shape[2], D, shape[0], shape[1], width, _DTYPES[dtype],
         D ** -0.5 if scale is None else scale)
+    _on_gpu((q, out, k_cache, v_cache, lse, block_table, prefix_lens, tree_ptr, parents, workspace))
     _check(lib.sgmv_tree_attention(args, _stream(q.device)), "sgmv_tree_attention")
     return out
 
@@ -569,6 +583,7 @@ def sgmv_tree_verify(target, draft, tokens, parents, tree_ptr, u_accept, u_sampl
         tp, dp, _list(tokens, "tokens", T), _list(parents, "parents", T),
         _list(tree_ptr, "tree_ptr", B + 1), _uniform(u_accept, "u_accept", T),
         _uniform(u_sample, "u_sample", B), count, path, token, t0, d0, T, B, V, max_path)
+    _on_gpu((target, draft, tokens, parents, tree_ptr, u_accept, u_sample, *out))
     _check(load_library().sgmv_tree_verify(args, _stream(target.device)), "sgmv_tree_verify")
     return out
 
@@ -590,6 +605,7 @@ def sgmv_cache_commit(k_cache, v_cache, block_table, prefix_lens, path, count):
         k_cache.data_ptr(), v_cache.data_ptr(), table, _list(prefix_lens, "prefix_lens", B),
         _list(path, "path", B * width), _list(count, "count", B), layer_stride, cs[-4], cs[-3],
         cs[-2], row, layers, B, Hkv, D, blocks, bs, max_blocks, width, _DTYPES[dtype])
+    _on_gpu((k_cache, v_cache, block_table, prefix_lens, path, count))
     _check(load_library().sgmv_cache_commit(args, _stream(k_cache.device)), "sgmv_cache_commit")
 
 
