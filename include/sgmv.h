@@ -453,7 +453,8 @@ int sgmv_rope_frequencies(double *inv_freq, int32_t pairs, double base, double f
  *   scale: multiplied onto the scores (usually D^-1/2)
  *   workspace: sgmv_tree_attention_workspace_bytes() bytes, 256-byte aligned;
  *     what it holds does not matter.  Calls that run at the same time need
- *     separate ones.
+ *     separate ones.  No batch of at most T rows and B sequences needs more
+ *     than the bytes of T and B (21 MB at most).
  * Hq a multiple of Hkv, D a multiple of 8 up to 256.  Scores, softmax and
  * sums are fp32; the weights p are rounded to the inputs' type for the
  * tensor cores, the output once.  out must not overlap the inputs.  Rows in

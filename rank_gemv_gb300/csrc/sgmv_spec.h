@@ -35,9 +35,9 @@ int tree_attention_launch(const sgmv_tree_attention_args &a, int nsm, int *err,
                           cudaStream_t stream);
 // The tensor-core form, for D <= kMmaMaxD.
 constexpr int kMmaMaxD = 128;
-size_t tree_mma_workspace(int32_t T, int32_t B, int32_t group);
+size_t tree_mma_workspace(int32_t T, int32_t group);
 int tree_mma_launch(const sgmv_tree_attention_args &a, int nsm, int *err, cudaStream_t stream);
-size_t tree_attention_workspace(int32_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D);
+size_t tree_attention_workspace(int32_t T, int32_t Hq, int32_t Hkv, int32_t D);
 int tree_verify_launch(const sgmv_tree_verify_args &a, int nsm, int *err, cudaStream_t stream);
 int cache_commit_launch(const sgmv_cache_commit_args &a, int *err, cudaStream_t stream);
 

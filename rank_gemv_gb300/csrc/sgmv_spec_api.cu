@@ -96,7 +96,7 @@ int sgmv_rope_frequencies(double *inv_freq, int32_t pairs, double base, double f
 
 size_t sgmv_tree_attention_workspace_bytes(int32_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D) {
     if (T < 1 || B < 1 || Hq < 1 || Hkv < 1 || D < 1) return 0;
-    return tree_attention_workspace(T, B, Hq, Hkv, D);
+    return tree_attention_workspace(T, Hq, Hkv, D);
 }
 
 int sgmv_tree_attention(const sgmv_tree_attention_args *args, void *stream) {

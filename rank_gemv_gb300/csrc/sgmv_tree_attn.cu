@@ -126,8 +126,8 @@ __global__ void __launch_bounds__(kRowThreads)
 
 }  // namespace
 
-size_t tree_attention_workspace(int32_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D) {
-    return D <= kMmaMaxD ? tree_mma_workspace(T, B, Hq / Hkv) : 256;
+size_t tree_attention_workspace(int32_t T, int32_t Hq, int32_t Hkv, int32_t D) {
+    return D <= kMmaMaxD ? tree_mma_workspace(T, Hq / Hkv) : 256;
 }
 
 int tree_attention_launch(const sgmv_tree_attention_args &a, int nsm, int *err,

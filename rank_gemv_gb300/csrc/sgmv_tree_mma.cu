@@ -1170,9 +1170,13 @@ int max_ctas(int rt) { return kMaxSms * (rt <= 16 ? Shape<16>::kPerSm : 1); }
 
 }  // namespace
 
-size_t tree_mma_workspace(int32_t T, int32_t B, int32_t group) {
-    const int rt = row_tile(T, B, group);
-    return kHeadBytes + (size_t)max_ctas(rt) * (sizeof(Cut) + 2u * (size_t)rt * 130u * 4u);
+// For the batch and every smaller one: fewer sequences or rows may make higher row
+// tiles, up to those of a single sequence with all the rows.
+size_t tree_mma_workspace(int32_t T, int32_t group) {
+    size_t most = 0;
+    for (int rt = 8, last = row_tile(T, 1, group); rt <= last; rt *= 2)
+        most = std::max(most, kHeadBytes + (size_t)max_ctas(rt) * (sizeof(Cut) + 2u * (size_t)rt * 130u * 4u));
+    return most;
 }
 
 int tree_mma_launch(const sgmv_tree_attention_args &a, int nsm, int *err, cudaStream_t stream) {

@@ -531,8 +531,8 @@ def sgmv_tree_attention(out, q, k_cache, v_cache, block_table, prefix_lens, tree
     prefix_lens[b] tokens of its context, its ancestors by `parents` (None: a
     chain) and itself.  scale defaults to D ** -0.5; lse (fp32 [T, Hq]) receives
     the log-sum-exp.  workspace: uint8 device tensor of at least
-    sgmv_tree_attention_workspace_bytes(T, B, Hq, Hkv, D) bytes; one is
-    allocated when None."""
+    sgmv_tree_attention_workspace_bytes(T, B, Hq, Hkv, D) bytes (those of the
+    largest T and B serve every batch); one is allocated when None."""
     qshape, dtype = q.shape, q.dtype
     if len(qshape) != 3 or dtype not in _DTYPES:
         raise TypeError("q must be a [T, heads, D] tensor of f16 or bf16")
