@@ -566,7 +566,11 @@ int sgmv_read_floor(const void *src, size_t bytes, int32_t T, int32_t L, int32_t
  * for a staged chunk, as if that wait had run out: SGMV_ERR_TIMEOUT is set in
  * the device error word, the chunk is then awaited with the full limit (so
  * the kernel still ends normally, with every copy landed) and the thread
- * writes no y.  Other kernels are unaffected.  Returns SGMV_OK.
+ * writes no y.  Launches of the tree attention for heads of up to 128 columns
+ * take theirs in one role of each CTA, given by the value: 1 the walk along
+ * the work, 2 the loading of K and V, 3 the matrix products, 4 the softmax;
+ * the status is the same, and the call writes no output.  Other kernels are
+ * unaffected.  Returns SGMV_OK.
  */
 int sgmv_debug_inject_wait_timeout(int enable);
 

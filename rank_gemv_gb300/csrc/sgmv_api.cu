@@ -146,7 +146,7 @@ int num_sms() {
 // mixed in a launch.
 int stream_launch(int in_dtype, StreamLaunch &l) {
     StreamParams &p = l.p;
-    p.inject = g_inject_timeout;
+    p.inject = g_inject_timeout != 0;
     const bool bf16 = in_dtype == SGMV_BF16;
     const cuuint64_t es = 2;
     if (p.np < 1 || p.np > kStreamMaxProblems) return (int)cudaErrorInvalidValue;
@@ -188,6 +188,8 @@ void sgmv::note_cuda_error(const char *what, cudaError_t e) { note(what, e); }
 int *sgmv::device_error_word() { return error_word(); }
 
 void sgmv::set_launch_count(int n) { g_launches = n; }
+
+int sgmv::injected_timeout() { return g_inject_timeout; }
 
 int sgmv::device_sms() { return num_sms(); }
 
@@ -978,7 +980,7 @@ int sgmv_fused_linear_lora(void *y, int y_dtype, const void *x, const void *W, c
 }
 
 int sgmv_debug_inject_wait_timeout(int enable) {
-    g_inject_timeout = enable ? 1 : 0;
+    g_inject_timeout = enable;
     return SGMV_OK;
 }
 

@@ -43,6 +43,8 @@ int cache_commit_launch(const sgmv_cache_commit_args &a, int *err, cudaStream_t 
 
 // Records how many kernels the calling thread's last call launched.
 void set_launch_count(int n);
+// What sgmv_debug_inject_wait_timeout was last given on the calling thread.
+int injected_timeout();
 // Streaming multiprocessors of the current device.
 int device_sms();
 

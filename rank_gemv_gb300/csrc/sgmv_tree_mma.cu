@@ -113,6 +113,7 @@ struct MmaParams {
     float *ml;        // [share][2][RT][2]: reference and sum of parts of items
     float *part;      // [share][2][RT][128]
     int *err;
+    int inject;       // diagnostic launch: the role (1 to 4) whose wait runs out
 };
 
 // An item whose parts are in the workspace; parts = 0: none.
@@ -173,21 +174,25 @@ struct Sequence {
     __device__ __forceinline__ int64_t work() const { return (int64_t)items * each; }
 };
 
-// Bounded wait of a whole warp.  When one runs out (or another role's did),
-// `lost` is set and every later wait returns at once: the roles then run
-// through their remaining steps on whatever the buffers hold, so that barriers
-// still meet and the kernel ends, and write no output.
-__device__ __forceinline__ void await(uint64_t *bar, uint32_t parity, volatile int *lost) {
-    if (!mbar_try_wait(bar, parity)) {
+// Bounded wait of a whole warp; false if it ran out for any lane.  Then, or when
+// another role's did, `lost` is set, and every wait that would last returns false at
+// once.  The roles that walk, load and multiply stop there, so that nothing is copied or
+// armed out of turn; the softmax warps, which meet at barriers of their own, finish
+// their segment on whatever the buffers hold and write none of it.  The end of the
+// kernel waits for the copies in flight and marks the share for the join.
+__device__ __forceinline__ bool await(uint64_t *bar, uint32_t parity, volatile int *lost) {
+    bool there = mbar_try_wait(bar, parity);
+    if (!there) {
         const uint64_t t0 = global_ns();
-        for (uint32_t i = 0; !mbar_try_wait(bar, parity); ++i) {
+        for (uint32_t i = 0;; ++i) {
             if (*lost || i >= kMaxPolls || global_ns() - t0 > kWaitLimitNs) {
                 *lost = 1;
                 break;
             }
+            if ((there = mbar_try_wait(bar, parity))) break;
         }
     }
-    __syncwarp();
+    return __all_sync(0xffffffffu, there);
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -445,11 +450,14 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
     volatile int *const lost = &s_lost;
     const int D = a.D, group = P.group;
     const int cpr = D / 8;  // 16-byte chunks per row
-    // a role's next segment: number i
-    auto wait_segment = [&](int i) -> const Segment & {
-        await(&seg_full[i % kSegs], (uint32_t)(i / kSegs) & 1, lost);
-        return s_seg[i % kSegs];
+    // a role's next segment, number i, is in s_seg[i % kSegs]
+    auto segment_there = [&](int i) { return await(&seg_full[i % kSegs], (uint32_t)(i / kSegs) & 1, lost); };
+    // A role takes an injected timeout as it would one of its waits.
+    auto injected = [&](int role) {
+        if (P.inject == role) *lost = 1;
+        return P.inject == role;
     };
+    int issued = 0;  // TMA copies of this warp: of Q (the walk), or K and V (the loaders)
 
     if (warp == kWalkWarp) {
         // ---- the walk along the line ---------------------------------------------
@@ -469,8 +477,8 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
             q.template enter<RT>(P, lo * plan.stride, &plan);
         }
         if (lane == 0) P.cut[id] = Cut{};
-        for (int i = 0;; ++i) {
-            if (i >= kSegs) await(&seg_empty[i % kSegs], (uint32_t)(i / kSegs - 1) & 1, lost);
+        for (int i = 0; !injected(1); ++i) {
+            if (i >= kSegs && !await(&seg_empty[i % kSegs], (uint32_t)(i / kSegs - 1) & 1, lost)) break;
             uint32_t item = 0;
             int tile = 0;
             while (w < w1) {
@@ -539,6 +547,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
                                         &q_full[qb]);
                     }
                     __syncwarp();
+                    issued = i + 1;
                     return;
                 }
                 for (int m = lane / cpr, c = lane % cpr; m < RT;) {
@@ -567,7 +576,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
                 see_rt = rt;
                 // the table's last user is done (those kSegs back were waited for)
                 const int u = see_user[see];
-                if (u >= 0 && i - u < kSegs) await(&seg_empty[u % kSegs], (uint32_t)(u / kSegs) & 1, lost);
+                if (u >= 0 && i - u < kSegs && !await(&seg_empty[u % kSegs], (uint32_t)(u / kSegs) & 1, lost)) break;
                 uint32_t *const tab = reinterpret_cast<uint32_t *>(sm + S::kOffSee) +
                                       see * SGMV_TREE_MAX_NODES * S::kWords;
                 for (int e = lane; e < q.n * S::kWords; e += 32) tab[e] = 0;
@@ -592,7 +601,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
             __syncwarp();
             if (lane == 0) mbar_arrive(&aux_full[i % kSegs]);
             if (i >= S::kQ) {
-                await(&q_empty[qb], (uint32_t)(i / S::kQ - 1) & 1, lost);
+                if (!await(&q_empty[qb], (uint32_t)(i / S::kQ - 1) & 1, lost)) break;
                 bring_q();
             }
         }
@@ -600,11 +609,12 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
     } else if (warp > kWalkWarp) {
         // ---- K and V: ring order K0, V0, K1, V1, ... ------------------------------
         const int lt = tid - S::kSoft - 64, halves = D > 64 ? 2 : 1;
-        int pos = 0, st = 0;
+        int st = 0;
         uint32_t ph = 1;  // parity of the stage's release that is waited for
         auto claim_stage = [&]() {
-            if (pos >= S::kStages) await(&empty[st], ph, lost);
-            ++pos;
+            if (issued >= S::kStages && !await(&empty[st], ph, lost)) return false;
+            ++issued;
+            return true;
         };
         auto advance = [&]() {
             if (++st == S::kStages) st = 0, ph ^= 1;
@@ -629,15 +639,17 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
                 }
             };
             auto copy_boxes = [&](const CUtensorMap *map, int32_t pg, int row, int head) {
-                claim_stage();
+                if (!claim_stage()) return false;
                 if (lane == 0) mbar_arrive_expect_tx(&full[st], bytes);
                 __syncwarp();
                 if (busy) tma_load_4d(sm + (uint32_t)st * kStage + at, map, half * 64, row, head, pg, &full[st]);
                 advance();
+                return true;
             };
-            bool looked = false;
-            for (int i = 0;; ++i) {
-                const Segment s = wait_segment(i);
+            bool looked = false, stop = injected(2);
+            for (int i = 0; !stop; ++i) {
+                if (!segment_there(i)) break;
+                const Segment s = s_seg[i % kSegs];
                 if (s.end == 0) break;
                 if (!looked) look(s, s.tile);
                 for (int tile = s.tile; tile < s.end; ++tile) {
@@ -654,14 +666,15 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
                     if (tile + 1 < s.end) {
                         look(s, tile + 1);
                     } else if (__shfl_sync(0xffffffffu, *(volatile int *)&s_known, 0) > i + 1) {
-                        const Segment &next = wait_segment(i + 1);
-                        look(next, next.tile);
-                        looked = true;
+                        looked = segment_there(i + 1);
+                        if (looked) look(s_seg[(i + 1) % kSegs], s_seg[(i + 1) % kSegs].tile);
                     }
-                    copy_boxes(&P.map_k, pg, row, s.h);
-                    copy_boxes(&P.map_v, pg, row, s.h);
+                    if (!copy_boxes(&P.map_k, pg, row, s.h) || !copy_boxes(&P.map_v, pg, row, s.h)) {
+                        stop = true;
+                        break;
+                    }
                 }
-                if (lane == 0) mbar_arrive(&seg_empty[i % kSegs]);
+                if (lane == 0 && !stop) mbar_arrive(&seg_empty[i % kSegs]);
                 __syncwarp();
             }
         } else {
@@ -670,7 +683,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
             constexpr int kBatch = 8;
             int g = 0;
             auto copy_tile = [&](const void *cache, int64_t off) {
-                claim_stage();
+                if (!claim_stage()) return false;
                 const T *const from = static_cast<const T *>(cache) + off;
                 const int64_t *const rows = tab + (g & 1) * kTok;
                 uint8_t *const dst = sm + (uint32_t)st * kStage;
@@ -699,9 +712,12 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
                 }
                 cp_async_arrive(&full[st]);
                 advance();
+                return true;
             };
-            for (int i = 0;; ++i) {
-                const Segment s = wait_segment(i);
+            bool stop = injected(2);
+            for (int i = 0; !stop; ++i) {
+                if (!segment_there(i)) break;
+                const Segment s = s_seg[i % kSegs];
                 if (s.end == 0) break;
                 for (int tile = s.tile; tile < s.end; ++tile, ++g) {
                     // where the tile's tokens are (elements from the cache's start)
@@ -719,11 +735,14 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
                         tab[(g & 1) * kTok + m] = off;
                     }
                     mbar_arrive(&tab_ready);  // (an mbarrier: its wait is bounded)
-                    await(&tab_ready, (uint32_t)g & 1, lost);
-                    copy_tile(a.k_cache, (int64_t)s.h * a.cache_head);
-                    copy_tile(a.v_cache, (int64_t)s.h * a.cache_head);
+                    if (!await(&tab_ready, (uint32_t)g & 1, lost) ||
+                        !copy_tile(a.k_cache, (int64_t)s.h * a.cache_head) ||
+                        !copy_tile(a.v_cache, (int64_t)s.h * a.cache_head)) {
+                        stop = true;
+                        break;
+                    }
                 }
-                if (lane == 0) mbar_arrive(&seg_empty[i % kSegs]);
+                if (lane == 0 && !stop) mbar_arrive(&seg_empty[i % kSegs]);
                 __syncwarp();
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
@@ -748,14 +767,18 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
             if (st >= S::kStages) st -= S::kStages, ph ^= 1;
         };
         int ahead = -1, left = 0;             // segment of the next score product, its tiles not yet issued
-        bool none = false;                    // no more of them
+        bool none = false, stop = false;      // no more of them; a wait ran out
         // Score product of tile g.  Its accumulator was last read for tile
         // g - 2, before that tile's P was complete.
         auto scores = [&](int g) {
             if (none) return;
             bool first = false;
             if (left == 0) {
-                const Segment &s = wait_segment(++ahead);
+                if (!segment_there(++ahead)) {
+                    none = stop = true;
+                    return;
+                }
+                const Segment &s = s_seg[ahead % kSegs];
                 left = s.end - s.tile;
                 if (s.end == 0) {
                     none = true;
@@ -764,8 +787,10 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
                 first = true;
             }
             const int qb = ahead % S::kQ;
-            if (first) await(&q_full[qb], (uint32_t)(ahead / S::kQ) & 1, lost);
-            await(&full[k_st], k_ph, lost);
+            if ((first && !await(&q_full[qb], (uint32_t)(ahead / S::kQ) & 1, lost)) || !await(&full[k_st], k_ph, lost)) {
+                none = stop = true;
+                return;
+            }
             --left;
             // cp.async (generic proxy) data -> tensor core (async proxy)
             if ((first && !P.q_box) || !P.box) fence_proxy_async();
@@ -785,17 +810,21 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
             skip(k_st, k_ph);
         };
         scores(0);
+        if (injected(3)) stop = true;
         int g = 0;
-        for (int i = 0;; ++i) {
-            const Segment &s = wait_segment(i);
+        for (int i = 0; !stop; ++i) {
+            if (!segment_there(i)) break;
+            const Segment &s = s_seg[i % kSegs];
             const int tiles = s.end - s.tile;
             if (s.end == 0) break;
             for (int t = 0; t < tiles; ++t, ++g) {
                 // A tile ahead; but with one Q buffer the next segment's first scores
                 // wait for its Q, and must not hold up this segment's last product.
                 if (S::kQ > 1 || t + 1 < tiles) scores(g + 1);  // nothing at the end
-                await(&full[v_st], v_ph, lost);
-                await(&p_full, (uint32_t)g & 1, lost);
+                if (stop || !await(&full[v_st], v_ph, lost) || !await(&p_full, (uint32_t)g & 1, lost)) {
+                    stop = true;
+                    break;
+                }
                 if (!P.box) fence_proxy_async();
                 tc_fence_after();
                 const uint64_t vd = v_desc + (uint32_t)v_st * (kStage >> 4);
@@ -807,12 +836,14 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
                 skip(v_st, v_ph);
                 if (S::kQ == 1 && t + 1 == tiles) scores(g + 1);
             }
-            if (lane == 0) mbar_arrive(&seg_empty[i % kSegs]);
+            if (lane == 0 && !stop) mbar_arrive(&seg_empty[i % kSegs]);
             __syncwarp();
         }
-        // nothing of this kernel's is in flight when tensor memory is returned
+        // nothing of this kernel's is in flight when tensor memory is returned (a
+        // wait with a limit of its own, whatever became of the others)
         commit_on(on, &drained);
-        await(&drained, 0, lost);
+        if (!mbar_wait(&drained, 0)) *lost = 1;
+        __syncwarp();
     } else {
         // ---- softmax and output: thread = token, then = head column ------------
         const int wg = warp >> 2, tok = tid & 127, r0 = wg * S::kRows, d = tok;
@@ -837,12 +868,16 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
             await(&pv_done, (uint32_t)g & 1, lost);
             tc_fence_after();
         };
-        // (one warp looks, so that all agree even when waits have run out)
+        // (one warp looks, so that all agree; once a wait has run out there are no more segments)
         auto look = [&](int seg) {
-            const Segment &s = wait_segment(seg);
-            if (lane == 0) s_cur[seg & 1] = s;
+            const bool there = segment_there(seg);
+            if (lane == 0) {
+                if (there && !*lost) s_cur[seg & 1] = s_seg[seg % kSegs];
+                else s_cur[seg & 1].end = 0;
+            }
         };
         if (warp == 0) look(0);
+        if (tid == 0) injected(4);
         for (int seg = 0;; ++seg) {
             named_sync<6, S::kSoft>();  // every thread is done with the last segment
             if (tid == 0 && seg > 0) mbar_arrive(&seg_empty[(seg - 1) % kSegs]);
@@ -1002,7 +1037,7 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
                     const float ref = -s_ref[r];
                     if (!whole)
                         *reinterpret_cast<float2 *>(P.ml + ((int64_t)slot * RT + r) * 2) = make_float2(ref, L);
-                    else if (a.lse && r < R)
+                    else if (a.lse && r < R && !*lost)
                         a.lse[(int64_t)(to.x < 0 ? ~to.x : to.x) * a.Hq + to.y] =
                             none ? -INFINITY : (ref + __log2f(L)) * 0.693147180559945309f;
                     s_ref[r] = -kUnset;
@@ -1060,11 +1095,23 @@ __global__ void __launch_bounds__(Shape<RT>::kThreads, Shape<RT>::kPerSm)
             }
             if (warp == 0) look(seg + 1);
         }
-        if (tid == 0 && *lost) set_error(P.err, kErrTimeout);
     }
     tc_fence_before();
     __syncthreads();
     if (warp == kMmaWarp) tmem_dealloc(tmem, S::kTmem);
+    if (*lost) {
+        if (tid == 0) set_error(P.err, kErrTimeout);
+        // the join leaves items with parts of this share alone
+        for (int r = tid; r < 2 * RT; r += S::kThreads)
+            *reinterpret_cast<float2 *>(P.ml + ((int64_t)blockIdx.x * 2 * RT + r) * 2) = make_float2(kUnset, -1.f);
+        // copies under way land while this shared memory is the CTA's
+        if (P.q_box && warp == kWalkWarp)
+            for (int i = max(0, issued - S::kQ); i < issued; ++i)
+                if (!mbar_wait(&q_full[i % S::kQ], (uint32_t)(i / S::kQ) & 1)) break;
+        if (P.box && warp > kWalkWarp)
+            for (int i = max(0, issued - S::kStages); i < issued; ++i)
+                if (!mbar_wait(&full[i % S::kStages], (uint32_t)(i / S::kStages) & 1)) break;
+    }
 }
 
 // Joins the parts of cut items: a warp per (share, row), the item being the one
@@ -1090,11 +1137,13 @@ __global__ void __launch_bounds__(kJoinThreads, 4) sgmv_tree_join_kernel(const _
         const int2 to = row_place(P, cut.t0, cut.h, cut.rt * RT + r);
         auto row_of = [&](int k) { return (int64_t)(2 * (id + k) + (k == 0)) * RT + r; };
         float M = kUnset, L = 0.f;
+        bool gone = false;  // a part's waits ran out: no output
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int k0 = 0; k0 < cut.parts; k0 += 32) {  // a lane per part
             const int n = min(32, cut.parts - k0);
             float2 ml = make_float2(kUnset, 0.f);
             if (lane < n) ml = *reinterpret_cast<const float2 *>(P.ml + row_of(k0 + lane) * 2);
+            gone |= __any_sync(0xffffffffu, ml.y < 0.f);
             float4 x[kJoinBatch];
             auto fetch = [&](int k) {
 #pragma unroll
@@ -1125,6 +1174,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) sgmv_tree_join_kernel(const _
                 }
             }
         }
+        if (gone) continue;
         const int64_t t = to.x < 0 ? ~to.x : to.x;
         const bool none = to.x < 0 || L == 0.f;
         const float f = none ? 0.f : 1.f / L;
@@ -1192,6 +1242,7 @@ int tree_mma_launch(const sgmv_tree_attention_args &a, int nsm, int *err, cudaSt
     p.ml = reinterpret_cast<float *>(p.cut + max_ctas(rt));
     p.part = p.ml + max_ctas(rt) * 2 * rt * 2;
     p.err = err;
+    p.inject = injected_timeout();
     const bool bf16 = a.dtype == SGMV_BF16;
     // Boxes are as high as pages allow, for TMA's cost here is per box: at pages of
     // 24 tokens, boxes of 8 filling every tile took 115 us, boxes of 24 and tiles of

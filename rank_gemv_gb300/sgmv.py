@@ -623,10 +623,11 @@ def sgmv_read_floor(src, nbytes, T, L, H1, H2, r, in_dtype=torch.float16, y_dtyp
     return ctas.value, cl.value
 
 
-def sgmv_debug_inject_wait_timeout(enable: bool) -> None:
-    """Make this thread's streaming-kernel launches take the timeout path at
-    their first wait (tests of device-side timeout reporting)."""
-    _check(load_library().sgmv_debug_inject_wait_timeout(1 if enable else 0),
+def sgmv_debug_inject_wait_timeout(enable: int) -> None:
+    """Make this thread's launches of the streaming kernel, and of the tree attention
+    in the role of this number, take the timeout path at their first wait (tests of
+    device-side timeout reporting; see include/sgmv.h)."""
+    _check(load_library().sgmv_debug_inject_wait_timeout(int(enable)),
            "sgmv_debug_inject_wait_timeout")
 
 
