@@ -381,7 +381,8 @@ int sgmv_copy_gather(int32_t n, void *const *dst, const void *const *src, const 
  *
  * Arguments travel in a struct, which is read before the call returns.  All
  * pointers are device pointers unless stated; f16 / bf16 data must be 16-byte
- * aligned and its strides multiples of 8 elements (SGMV_ERR_ALIGNMENT).
+ * aligned and its strides multiples of 8 elements (SGMV_ERR_ALIGNMENT); the
+ * stride of a dimension of one entry does not matter.
  * Metadata is checked on the device: a sequence with bad tree_ptr or too many
  * nodes is skipped (SGMV_ERR_BAD_SEGMENTS in the device error word), and a
  * parent, slot, token or path entry out of range is left out, a page out of

@@ -21,6 +21,12 @@ bool vectors(const void *p, int64_t s0, int64_t s1) {
     return aligned16(p) && s0 % 8 == 0 && s1 % 8 == 0;
 }
 
+// The stride of a dimension of one entry is never used and may be anything: it
+// becomes one that passes the checks here and fits a tensor map.
+void settle(int64_t &stride, int32_t entries, int32_t D) {
+    if (entries == 1) stride = D;
+}
+
 int check_head(int32_t D) {
     if (D < 1) return SGMV_ERR_INVALID_ARG;
     if (D % 8 != 0) return SGMV_ERR_ALIGNMENT;
@@ -43,7 +49,7 @@ extern "C" {
 int sgmv_rope(const sgmv_rope_args *args, void *stream) {
     set_launch_count(0);
     if (!args) return SGMV_ERR_INVALID_ARG;
-    const sgmv_rope_args &a = *args;
+    sgmv_rope_args a = *args;
     if (a.T < 0 || a.Hq < 0 || a.Hk < 0 || !half_type(a.dtype)) return SGMV_ERR_INVALID_ARG;
     const int st = check_head(a.D);
     if (st != SGMV_OK) return st;
@@ -56,6 +62,11 @@ int sgmv_rope(const sgmv_rope_args *args, void *stream) {
     if (!a.positions || (a.Hq > 0 && (!a.q || !a.q_out))) return SGMV_ERR_INVALID_ARG;
     if (a.Hk > 0 && (!a.k || (!a.k_out && !append) || (append && !a.v))) return SGMV_ERR_INVALID_ARG;
     if (a.Hk == 0 && append) return SGMV_ERR_INVALID_ARG;
+    for (int64_t *s : {&a.q_token, &a.q_out_token, &a.k_token, &a.k_out_token, &a.v_token}) settle(*s, a.T, a.D);
+    for (int64_t *s : {&a.q_head, &a.q_out_head}) settle(*s, a.Hq, a.D);
+    for (int64_t *s : {&a.k_head, &a.k_out_head, &a.v_head, &a.cache_head}) settle(*s, a.Hk, a.D);
+    settle(a.cache_block, a.num_blocks, a.D);
+    settle(a.cache_token, a.block_size, a.D);
     if (a.Hq > 0 && (!vectors(a.q, a.q_token, a.q_head) || !vectors(a.q_out, a.q_out_token, a.q_out_head)))
         return SGMV_ERR_ALIGNMENT;
     if (a.Hk > 0 && (!vectors(a.k, a.k_token, a.k_head) ||
@@ -102,7 +113,7 @@ size_t sgmv_tree_attention_workspace_bytes(int32_t T, int32_t B, int32_t Hq, int
 int sgmv_tree_attention(const sgmv_tree_attention_args *args, void *stream) {
     set_launch_count(0);
     if (!args) return SGMV_ERR_INVALID_ARG;
-    const sgmv_tree_attention_args &a = *args;
+    sgmv_tree_attention_args a = *args;
     if (a.T < 0 || a.B < 0 || a.Hq < 1 || a.Hkv < 1 || a.Hq % a.Hkv != 0 || !half_type(a.dtype) ||
         !(a.scale == a.scale))
         return SGMV_ERR_INVALID_ARG;
@@ -116,6 +127,11 @@ int sgmv_tree_attention(const sgmv_tree_attention_args *args, void *stream) {
         return SGMV_ERR_INVALID_ARG;
     if (a.num_blocks < 1 || a.block_size < 1 || a.max_blocks < 1 || a.table_row < 0)
         return SGMV_ERR_INVALID_ARG;
+    for (int64_t *s : {&a.q_token, &a.out_token}) settle(*s, a.T, a.D);
+    for (int64_t *s : {&a.q_head, &a.out_head}) settle(*s, a.Hq, a.D);
+    settle(a.cache_block, a.num_blocks, a.D);
+    settle(a.cache_token, a.block_size, a.D);
+    settle(a.cache_head, a.Hkv, a.D);
     if (!vectors(a.q, a.q_token, a.q_head) || !vectors(a.out, a.out_token, a.out_head) ||
         !vectors(a.k_cache, a.cache_block, a.cache_token) || !vectors(a.v_cache, a.cache_head, 0))
         return SGMV_ERR_ALIGNMENT;
@@ -148,7 +164,7 @@ int sgmv_tree_verify(const sgmv_tree_verify_args *args, void *stream) {
 int sgmv_cache_commit(const sgmv_cache_commit_args *args, void *stream) {
     set_launch_count(0);
     if (!args) return SGMV_ERR_INVALID_ARG;
-    const sgmv_cache_commit_args &a = *args;
+    sgmv_cache_commit_args a = *args;
     if (a.layers < 0 || a.B < 0 || a.Hkv < 1 || a.max_path < 0 || !half_type(a.dtype))
         return SGMV_ERR_INVALID_ARG;
     const int st = check_head(a.D);
@@ -159,6 +175,10 @@ int sgmv_cache_commit(const sgmv_cache_commit_args *args, void *stream) {
         return SGMV_ERR_INVALID_ARG;
     if (a.num_blocks < 1 || a.block_size < 1 || a.max_blocks < 1 || a.table_row < 0)
         return SGMV_ERR_INVALID_ARG;
+    settle(a.cache_layer, a.layers, a.D);
+    settle(a.cache_block, a.num_blocks, a.D);
+    settle(a.cache_token, a.block_size, a.D);
+    settle(a.cache_head, a.Hkv, a.D);
     if (!vectors(a.k_cache, a.cache_block, a.cache_token) ||
         !vectors(a.v_cache, a.cache_head, a.cache_layer))
         return SGMV_ERR_ALIGNMENT;

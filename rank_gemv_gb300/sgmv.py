@@ -407,7 +407,8 @@ def _cache(k_cache, v_cache, dtype, ndim):
     """Checked strides and shape of a pair of caches [blocks, block_size, Hkv, D]
     (ndim 5: [layers, blocks, block_size, Hkv, D])."""
     shape, stride = k_cache.shape, k_cache.stride()
-    if v_cache.shape != shape or v_cache.stride() != stride:
+    if v_cache.shape != shape or (v_cache.stride() != stride and any(
+            n > 1 and a != b for n, a, b in zip(shape, stride, v_cache.stride()))):
         raise ValueError("k_cache and v_cache differ in shape or strides")
     if k_cache.dtype != dtype or v_cache.dtype != dtype:
         raise TypeError(f"the caches must be {dtype}")
