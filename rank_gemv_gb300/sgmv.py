@@ -477,6 +477,8 @@ def sgmv_rope(q, k, positions, inv_freq, interleaved=False, scale=1.0, inverse=F
     of the rotated pairs (sgmv_rope_frequencies); inverse=True turns back, the
     gradient of the rotation."""
     first = q if q is not None else k
+    if first is None:
+        raise ValueError("q or k must be given")
     shape, dtype = first.shape, first.dtype
     if len(shape) != 3 or dtype not in _DTYPES:
         raise TypeError("q and k must be [T, heads, D] tensors of f16 or bf16")
@@ -494,6 +496,8 @@ def sgmv_rope(q, k, positions, inv_freq, interleaved=False, scale=1.0, inverse=F
             qo = _heads(q_out, "q_out", dtype, shape)
     else:
         Hq = 0
+        if q_out is not None:
+            raise ValueError("q_out without q")
     if k is not None:
         Hk = k.shape[1]
         kshape = (T, Hk, D)
@@ -502,7 +506,14 @@ def sgmv_rope(q, k, positions, inv_freq, interleaved=False, scale=1.0, inverse=F
             ko = _heads(k_out, "k_out", dtype, kshape)
         elif k_cache is None:
             k_out, ko = k, ki
-    if k_cache is not None:
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    if k_cache is None:
+        if v_cache is not None or slots is not None:
+            raise ValueError("v_cache and slots need k_cache")
+    else:
+        if k is None or v is None or v_cache is None or slots is None:
+            raise ValueError("an append needs k, v, k_cache, v_cache and slots")
         cshape, cs = _cache(k_cache, v_cache, dtype, 4)
         vi = _heads(v, "v", dtype, kshape)
         blocks, bs, ch, cd = cshape
