@@ -35,6 +35,10 @@ int tree_attention_launch(const sgmv_tree_attention_args &a, int nsm, int *err,
                           cudaStream_t stream);
 // The tensor-core form, for D <= kMmaMaxD.
 constexpr int kMmaMaxD = 128;
+// Its tokens per tile: 128, or as many whole pages of a multiple of 8 tokens as fit.
+inline int32_t tree_tile(int32_t block_size) {
+    return block_size > 0 && block_size < 128 && block_size % 8 == 0 ? 128 / block_size * block_size : 128;
+}
 size_t tree_mma_workspace(int32_t T, int32_t group);
 int tree_mma_launch(const sgmv_tree_attention_args &a, int nsm, int *err, cudaStream_t stream);
 size_t tree_attention_workspace(int32_t T, int32_t Hq, int32_t Hkv, int32_t D);

@@ -120,8 +120,10 @@ int sgmv_tree_attention(const sgmv_tree_attention_args *args, void *stream) {
     const int st = check_head(a.D);
     if (st != SGMV_OK) return st;
     if (a.T == 0 || a.B == 0) return SGMV_OK;
-    // a sequence's token tiles times its row tiles and heads are counted in 32 bits
-    if (a.Hq > 65535 || (double)a.Hq * SGMV_TREE_MAX_NODES / 16 * ((double)a.max_blocks * a.block_size / 128 + 1) > 2e9)
+    // a sequence's row tiles (of 8 rows at least) of all heads times its token tiles (and
+    // two more, and a part of one) are counted in 32 bits
+    if (a.Hq > 65535 || (double)a.Hq * SGMV_TREE_MAX_NODES / 8 *
+                                ((double)a.max_blocks * a.block_size / tree_tile(a.block_size) + 3) > 4294967295.0)
         return SGMV_ERR_UNSUPPORTED;
     if (!a.out || !a.q || !a.k_cache || !a.v_cache || !a.block_table || !a.prefix_lens || !a.tree_ptr)
         return SGMV_ERR_INVALID_ARG;

@@ -1247,12 +1247,8 @@ int tree_mma_launch(const sgmv_tree_attention_args &a, int nsm, int *err, cudaSt
     // Boxes are as high as pages allow, for TMA's cost here is per box: at pages of
     // 24 tokens, boxes of 8 filling every tile took 115 us, boxes of 24 and tiles of
     // 120 tokens 109 us (128 sequences of up to 2100 tokens, 4 heads of 80).
-    p.box = std::gcd(a.block_size, kTok);
-    p.tok = kTok;
-    if (a.block_size % 8 == 0 && a.block_size < kTok && a.block_size > p.box) {
-        p.box = a.block_size;
-        p.tok = kTok / p.box * p.box;
-    }
+    p.tok = tree_tile(a.block_size);
+    p.box = p.tok < kTok ? a.block_size : std::gcd(a.block_size, kTok);
     if (p.box >= 8) {
         const cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)a.block_size, (cuuint64_t)a.Hkv,
                                     (cuuint64_t)a.num_blocks};
