@@ -14,7 +14,7 @@ moves the accepted tokens' keys and values to their places:
     sgmv_tree_verify             which drafted tokens are accepted
     sgmv_cache_commit            their keys and values, all layers at once
 
-    python examples/speculative_decode.py [steps]
+    python examples/speculative_decode.py [tokens]
 """
 import os
 import sys
@@ -131,10 +131,13 @@ def step(model, req, parents=PARENTS, depth=DEPTH, tokens=None, greedy=False):
 
 
 def generate(model, req, length, parents=PARENTS, depth=DEPTH, greedy=False, tokens=None):
-    """At least `length` new tokens per request, as lists; and the steps it took."""
+    """At least `length` new tokens per request, as lists; and the steps it took.  Requests
+    that run ahead of the slowest use up their pages sooner: then ValueError."""
     out = [[] for _ in range(req.lens.numel())]
-    steps = 0
+    steps, held, room = 0, req.lens.tolist(), req.table.shape[1] * req.bs
     while min(map(len, out)) < length:
+        if max(h + len(o) for h, o in zip(held, out)) + len(parents) > room:
+            raise ValueError(f"a request's pages hold {room} tokens, too few for its next tree")
         count, path, token, drafted = step(model, req, parents, depth, tokens(out) if tokens else None, greedy)
         for b, (c, p, t) in enumerate(zip(count.tolist(), path.tolist(), token.tolist())):
             out[b] += [int(drafted[b, i]) for i in p[1:c]] + [t]
@@ -145,7 +148,8 @@ def generate(model, req, length, parents=PARENTS, depth=DEPTH, greedy=False, tok
 def main():
     steps = int(sys.argv[1]) if len(sys.argv) > 1 else 32
     model = Model()
-    req = Requests(model, batch=8, longest=1024)
+    # a step adds up to three tokens to a request, and one at least to the slowest
+    req = Requests(model, batch=8, longest=max(1024, (max(DEPTH) + 1) * steps + len(PARENTS)))
     out, took = generate(model, req, steps)
     assert sgmv.sgmv_get_device_error() == 0
     total = sum(map(len, out))
