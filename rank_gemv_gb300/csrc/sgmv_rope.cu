@@ -25,8 +25,11 @@ constexpr int kRopeBatch = 2;  // pieces of q or k, and of v, in flight per thre
 
 enum RopeMode : int {
     kHalves = 0,       // pairs (i, i + pairs), pairs a multiple of 8: 16-byte vectors
-    kInterleaved = 1,  // pairs (2i, 2i + 1): 16-byte vectors
+    kInterleaved = 1,  // pairs (2i, 2i + 1), pairs a multiple of 4: 16-byte vectors
     kScalar = 2,       // pairs (i, i + pairs) of any number: one pair or column at a time
+    // kInterleaved with a last pair inside a vector, whose other columns are copied (a
+    // mode of its own: looking in every vector cost 8192 rows 0.6 of 42 us)
+    kInterleavedPart = 3,
 };
 
 struct RopeParams {
@@ -41,13 +44,14 @@ template <typename T, int MODE>
 __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
     sgmv_rope_kernel(const __grid_constant__ RopeParams P, int *err) {
     const sgmv_rope_args &a = P.a;
-    constexpr int kAngles = MODE == kHalves ? 8 : MODE == kInterleaved ? 4 : 1;  // per piece
+    constexpr bool kAdjacent = MODE == kInterleaved || MODE == kInterleavedPart;
+    constexpr int kAngles = MODE == kHalves ? 8 : kAdjacent ? 4 : 1;  // per piece
     __shared__ __align__(16) float2 s_angles[2][kRopeMaxPairs];  // cosine, sine
     const int tid = threadIdx.x, pairs = a.pairs, D = a.D, uph = P.uph;
     pdl_wait();
     pdl_trigger();
     const int heads = a.Hq + a.Hk, step = kRopeThreads / uph, h0 = tid / uph, w = tid - h0 * uph;
-    const bool turns = w < P.rot && (MODE != kInterleaved || w * 4 < pairs);
+    const bool turns = w < P.rot && (!kAdjacent || w * 4 < pairs);
     // first column of the piece, and of its partners
     const int c = MODE == kScalar ? (w < P.rot ? w : w + pairs)
                                   : (MODE == kHalves && w >= P.rot ? (w - P.rot) * 8 + 2 * pairs : w * 8);
@@ -132,7 +136,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
                         const float p = to_f<T>(*reinterpret_cast<const T *>(xs)), q = to_f<T>(*reinterpret_cast<const T *>(ys));
                         xs[0] = pack2<T>(p * r[0].x - q * r[0].y, 0.f);
                         ys[0] = pack2<T>(p * r[0].y + q * r[0].x, 0.f);
-                    } else if (MODE == kInterleaved) {
+                    } else if (kAdjacent) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             float p, q;
@@ -140,7 +144,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
                             const uint32_t turned = pack2<T>(p * r[i % kAngles].x - q * r[i % kAngles].y,
                                                              p * r[i % kAngles].y + q * r[i % kAngles].x);
                             // (a select: cosine 1 and sine 0 would make NaN of an infinity's neighbour)
-                            if (w * 4 + i < pairs) xs[i] = turned;
+                            if (MODE == kInterleaved || w * 4 + i < pairs) xs[i] = turned;
                         }
                     } else {
 #pragma unroll
@@ -183,6 +187,8 @@ template <typename T> int launch(const RopeParams &p, int mode, int nsm, int *er
         case kHalves: return spec_launch(sgmv_rope_kernel<T, kHalves>, grid, kRopeThreads, 0, 1, stream, p, err);
         case kInterleaved:
             return spec_launch(sgmv_rope_kernel<T, kInterleaved>, grid, kRopeThreads, 0, 1, stream, p, err);
+        case kInterleavedPart:
+            return spec_launch(sgmv_rope_kernel<T, kInterleavedPart>, grid, kRopeThreads, 0, 1, stream, p, err);
         default: return spec_launch(sgmv_rope_kernel<T, kScalar>, grid, kRopeThreads, 0, 1, stream, p, err);
     }
 }
@@ -193,9 +199,11 @@ int rope_launch(const sgmv_rope_args &a, const uint64_t *turns, int nsm, int *er
     RopeParams p;
     p.a = a;
     for (int i = 0; i < a.pairs; ++i) p.turns[i] = turns[i];
-    const int mode = a.interleaved ? kInterleaved : a.pairs % 8 == 0 ? kHalves : kScalar, rest = a.D - 2 * a.pairs;
-    p.rot = mode == kHalves ? a.pairs / 8 : mode == kInterleaved ? a.D / 8 : a.pairs;
-    p.uph = mode == kHalves ? p.rot + rest / 8 : mode == kInterleaved ? p.rot : p.rot + rest;
+    const int mode = a.interleaved ? (a.pairs % 4 == 0 ? kInterleaved : kInterleavedPart)
+                     : a.pairs % 8 == 0 ? kHalves : kScalar;
+    const int rest = a.D - 2 * a.pairs;
+    p.rot = a.interleaved ? a.D / 8 : mode == kHalves ? a.pairs / 8 : a.pairs;
+    p.uph = a.interleaved ? p.rot : mode == kHalves ? p.rot + rest / 8 : p.rot + rest;
     return a.dtype == SGMV_F16 ? launch<__half>(p, mode, nsm, err, stream)
                                  : launch<__nv_bfloat16>(p, mode, nsm, err, stream);
 }
