@@ -456,10 +456,13 @@ int sgmv_rope_frequencies(double *inv_freq, int32_t pairs, double base, double f
  *     what it holds does not matter.  Calls that run at the same time need
  *     separate ones.  No batch of at most T rows and B sequences needs more
  *     than the bytes of T and B (21 MB at most).
- * Hq a multiple of Hkv, D a multiple of 8 up to 256.  Scores, softmax and
- * sums are fp32; the weights p are rounded to the inputs' type for the
- * tensor cores, the output once.  out must not overlap the inputs.  Rows in
- * no sequence are not written.
+ * Hq a multiple of Hkv, D a multiple of 8 up to 256.  Heads of more than 128
+ * columns run on the CUDA cores, a CTA per row and query head over the whole
+ * context: right, but for short contexts and few rows (32 rows over up to 4096
+ * tokens, 32 heads of 256: 1.3 ms; of 128: 0.17).  Scores, softmax and sums
+ * are fp32; the weights p are rounded to the inputs' type for the tensor
+ * cores, the output once.  out must not overlap the inputs.  Rows in no
+ * sequence are not written.
  */
 typedef struct {
     void *out;

@@ -2,8 +2,13 @@
 // paged cache: o = softmax(scale * q K^T) V over the context, the row's
 // ancestors in the tree and itself.
 //
-// One CTA per (row, head): its warps take the tokens in turn, keep a running
-// maximum and sum each, and join at the end.
+// This file: heads of more than 128 columns, on the CUDA cores.  One CTA per (row,
+// head): its warps take the tokens in turn, keep a running maximum and sum each, and join at
+// the end.  K and V are read for every row and query head, and the context is not
+// split, so it is the chain of tokens (a reduction over the warp and two exponentials each)
+// that bounds it, far from the bytes: 32 sequences of one row, up to 4096 tokens, 32
+// heads of 256: 1330 us (1.6 TB/s of algorithmic bytes); with trees of up to 16 rows 4700; one row over 32768
+// tokens, 32 heads on 8: 10200.
 #include <math.h>
 
 #include "sgmv_device.cuh"
