@@ -94,7 +94,8 @@ typedef enum {
 typedef enum {
     SGMV_F16 = 0,
     SGMV_BF16 = 1,
-    SGMV_F32 = 2                /* output y only */
+    SGMV_F32 = 2,               /* output y; logits */
+    SGMV_E4M3 = 3               /* caches of sgmv_cache_commit */
 } sgmv_dtype;
 
 /* Human-readable name of a status code (static string, never NULL). */
@@ -525,8 +526,8 @@ typedef struct {
 int sgmv_tree_verify(const sgmv_tree_verify_args *args, void *stream);
 
 /*
- * Moves the accepted nodes' k and v to their final places in the cache, in
- * place: position prefix_lens[b] + d takes what position prefix_lens[b] +
+ * Moves the accepted nodes' k and v to their final places in the cache (f16,
+ * bf16, or e4m3 with D and the strides multiples of 16), in place: position prefix_lens[b] + d takes what position prefix_lens[b] +
  * path[b][d] held, for d < count[b].  path rows ascend (as
  * sgmv_tree_verify writes them).  Afterwards the sequence's context is
  * prefix_lens[b] + count[b] long.  layers > 1 moves the same tokens in that
@@ -543,6 +544,132 @@ typedef struct {
     int32_t layers, B, Hkv, D, num_blocks, block_size, max_blocks, max_path, dtype;
 } sgmv_cache_commit_args;
 int sgmv_cache_commit(const sgmv_cache_commit_args *args, void *stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * A decoding step of models with normalised heads, with an 8-bit cache, and the
+ * sampling of its tokens.  The conventions are those above.
+ *
+ *   sgmv_norm_rope        norms of q and k per head, rotary positions, append
+ *   sgmv_norm_rope_grad   their gradient
+ *   sgmv_quant_attention  tree attention over an e4m3 cache
+ *   sgmv_sample           temperature, top-k, top-p and min-p
+ *
+ * An e4m3 cache holds 8-bit values (sign, 4 bits of exponent, 3 of mantissa; up to
+ * 448), in multiples of one positive fp32 scale per KV head for k and one for v:
+ * k_scale, v_scale [Hk].  Written, a value is divided by its scale (as a product
+ * with the fp32 reciprocal), limited to +-448 and rounded to nearest even, once; NaN
+ * stays NaN.  D and the cache's strides are multiples of 16 (SGMV_ERR_ALIGNMENT).
+ */
+
+/*
+ * Norms, rotary positions and append in one pass:
+ *   y = R(positions[t]) (w * x / sqrt(mean(x^2) + eps))
+ * for every head x of q with w = q_weight and of k with w = k_weight ([D], of q's
+ * type; NULL: that tensor is not normalised, x alone is rotated), R as in sgmv_rope
+ * (rope.scale included).  y is rounded once, to q_out, to k_out, and to the cache
+ * with v beside it: to q's type if k_scale and v_scale are NULL, else to e4m3.
+ * `rope` is as for sgmv_rope, with inverse = 0; its caches are of the type just
+ * said.  Squares are summed in fp32, and so must not pass its range (3.4e38).  eps > 0.
+ * T * (Hq + 2 Hk) below 2^31 (SGMV_ERR_UNSUPPORTED).
+ */
+typedef struct {
+    sgmv_rope_args rope;
+    const void *q_weight;
+    const void *k_weight;
+    const float *k_scale;
+    const float *v_scale;
+    float eps;
+} sgmv_norm_rope_args;
+int sgmv_norm_rope(const sgmv_norm_rope_args *args, void *stream);
+
+/*
+ * Gradients of the inputs of sgmv_norm_rope from those of q_out and k_out: with
+ * g = scale R^T dy, r = 1 / sqrt(mean(x^2) + eps), h = w * g,
+ *   dx = r (h - r^2 x mean(h * x)),   dw = sum over rows and heads of g * r x
+ * (dx = g for a tensor without a weight).  q, k, dq_out, dk_out, dq, dk [T][heads][D]
+ * of any token and head strides, dq and dk apart from the inputs; q or k may be
+ * left out (Hq or Hk = 0), and is not read without its weight.  dq_weight, dk_weight fp32 [D], written
+ * (not added to); given exactly where the weight is.  Sums are fp32, joined in fp64 in a fixed order:
+ * the same result in every run.
+ *   workspace: sgmv_norm_rope_grad_workspace_bytes(D) bytes, 16-byte aligned; what it
+ *     holds does not matter.  Calls that run at the same time need separate ones.
+ */
+typedef struct {
+    void *dq;
+    void *dk;
+    const void *dq_out;
+    const void *dk_out;
+    const void *q;
+    const void *k;
+    const void *q_weight;
+    const void *k_weight;
+    float *dq_weight;
+    float *dk_weight;
+    const int32_t *positions;
+    const double *inv_freq;
+    void *workspace;
+    uint64_t workspace_bytes;
+    int64_t dq_token, dq_head, dk_token, dk_head, dq_out_token, dq_out_head;
+    int64_t dk_out_token, dk_out_head, q_token, q_head, k_token, k_head;
+    int32_t T, Hq, Hk, D, pairs, dtype, interleaved;
+    float scale, eps;
+} sgmv_norm_rope_grad_args;
+size_t sgmv_norm_rope_grad_workspace_bytes(int32_t D);
+int sgmv_norm_rope_grad(const sgmv_norm_rope_grad_args *args, void *stream);
+
+/*
+ * sgmv_tree_attention over an e4m3 cache: out = v_scale[h] softmax(scale *
+ * k_scale[h] * q K^T) V, with K and V as stored (they are converted to q's type,
+ * exactly, for the products).  `attention` is as there, its caches of e4m3; D a
+ * multiple of 16, at most 128 (SGMV_ERR_UNSUPPORTED beyond).  Masks, padding, lse and
+ * values that are no numbers as there.
+ */
+typedef struct {
+    sgmv_tree_attention_args attention;
+    const float *k_scale;
+    const float *v_scale;
+} sgmv_quant_attention_args;
+size_t sgmv_quant_attention_workspace_bytes(int32_t T, int32_t B, int32_t Hq, int32_t Hkv,
+                                            int32_t D);
+int sgmv_quant_attention(const sgmv_quant_attention_args *args, void *stream);
+
+/*
+ * The next token of every row of logits [T][V] (f16, bf16 or fp32), from given
+ * random numbers.  Weights are whole numbers,
+ *   w_i = floor(2^38 exp((l_i - max l) / temperature))   (to a few units),
+ * and tokens are ranked by logit, ties by index, the lowest first.  Kept are
+ *   the first top_k                                (top_k <= 0 or >= V: all),
+ *   of those, as many of the first as it takes for their weights to reach
+ *     top_p of their sum, one at least            (top_p >= 1: all),
+ *   of those, the ones with w_i >= min_p 2^38      (min_p <= 0: all).
+ * The token is the first, by index, at which the running sum of the kept weights
+ * passes u of their sum; probs receives the kept weights over their sum, zero for
+ * the others: the distribution for sgmv_tree_verify.  temperature <= 0 or NaN, top_k = 1, or top_p <= 0
+ * or NaN: the likeliest token alone.  top_p and u count in multiples of 2^-24 (rounded
+ * down), limited to [0, 1].  NaN logits count as -inf, which is never drawn, others are limited
+ * to +-2^126; a row with no logit above -inf gives token -1 and zeros.  Sums are exact: the
+ * result does not depend on the order of summation.
+ *   temperature, top_p, min_p fp32 [T], top_k int32 [T]; each may be NULL: then
+ *     temperature_all, ... hold for every row
+ *   u fp32 [T], token int32 [T]: both or neither; probs fp32 [T][V], or NULL
+ *   logits_row, probs_row: elements between rows; logits aligned to its type
+ * V up to 2^24 (SGMV_ERR_UNSUPPORTED beyond).
+ */
+typedef struct {
+    const void *logits;
+    const float *u;
+    const float *temperature;
+    const int32_t *top_k;
+    const float *top_p;
+    const float *min_p;
+    int32_t *token;
+    float *probs;
+    int64_t logits_row, probs_row;
+    int32_t T, V, dtype, top_k_all;
+    float temperature_all, top_p_all, min_p_all;
+} sgmv_sample_args;
+int sgmv_sample(const sgmv_sample_args *args, void *stream);
 
 /*
  * Diagnostics (no counterpart on the pages).

@@ -18,6 +18,8 @@ _BINDING_NAMES = {
     "sgmv_debug_inject_wait_timeout", "sgmv_fused_workspace_bytes", "sgmv_fused_linear_lora",
     "sgmv_rope", "sgmv_rope_frequencies", "sgmv_tree_attention",
     "sgmv_tree_attention_workspace_bytes", "sgmv_tree_verify", "sgmv_cache_commit",
+    "sgmv_norm_rope", "sgmv_norm_rope_grad", "sgmv_norm_rope_grad_workspace_bytes",
+    "sgmv_quant_attention", "sgmv_quant_attention_workspace_bytes", "sgmv_sample",
     "SgmvError", "load_library",
 }
 

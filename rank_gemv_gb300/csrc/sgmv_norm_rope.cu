@@ -1,0 +1,527 @@
+// sgmv_norm_rope.cu -- norms of queries and keys for each head, the rotary
+// positions and the append to the cache (16-bit or e4m3) in one pass; and the
+// gradient of norms and rotation.
+//
+// One (token, head) is an item, its columns one group of G lanes': with
+//   r = (mean x^2 + eps)^-1/2,  y = scale R(pos) (w * x * r),
+// a lane holds the pairs that turn together, so that a row is read once, summed
+// over the group by shuffles, turned in registers and written once to each of its
+// places.  Items of q, k and v lie on one line, t * (Hq + 2 Hk) + head, of which
+// every CTA takes an equal contiguous part; the angles of kChunk tokens at a time
+// are computed into shared memory and used by all their heads.  Bounded by memory.
+//
+// Gradient: with g = scale R^T dy, xh = r x, h = w * g,
+//   dx = r (h - xh mean(h * xh)),   dw = sum over rows of g * xh.
+// A lane adds up its columns of dw in registers over all its items, a CTA then its
+// groups' in shared memory, in order; a second kernel adds the CTAs' sums, in order
+// too, so the result is the same in every run.  A CTA has rows of q or of k only.
+#include <cuda_fp8.h>
+
+#include <algorithm>
+
+#include "sgmv_device.cuh"
+#include "sgmv_spec.h"
+
+namespace sgmv {
+namespace {
+
+constexpr int kNormThreads = 256;
+constexpr int kNormCtas = 3;  // per SM
+constexpr int kChunk = 8;     // tokens whose angles are held
+
+enum NormMode : int {
+    kHalves = 0,       // pairs (i, i + pairs), pairs a multiple of 8: a lane has two vectors
+    kInterleaved = 1,  // pairs (2i, 2i + 1): one vector
+    kGather = 2,       // pairs (i, i + pairs) of any number: one vector, partners read singly
+};
+
+struct NormParams {
+    sgmv_norm_rope_args a;
+    uint64_t turns[kRopeMaxPairs];
+    int32_t rot, uph;  // lanes of a group whose columns turn, lanes with columns
+};
+struct GradParams {
+    sgmv_norm_rope_grad_args a;
+    uint64_t turns[kRopeMaxPairs];
+    int32_t rot, uph;
+    int32_t ctas_q;  // CTAs with rows of q; the others have rows of k
+    float *part;     // [CTA][D]
+};
+
+// Where a lane's columns are: [c, c + 8), and with kHalves [c + pairs, ...) if they turn.
+template <int MODE> struct Columns {
+    int c, d;    // d: second vector's first column (kHalves, turning lanes)
+    bool here, turns;
+    __device__ __forceinline__ Columns(int w, int rot, int uph, int pairs) {
+        here = w < uph;
+        turns = MODE == kHalves ? w < rot : here;
+        c = MODE == kHalves && !turns ? (w - rot) * 8 + 2 * pairs : w * 8;
+        d = c + pairs;
+    }
+};
+
+template <int G> __device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Angles (cosine, sine times scale) of tokens t0 ... of one chunk.
+__device__ __forceinline__ void chunk_angles(float2 (*s_angle)[kRopeMaxPairs], const int32_t *positions,
+                                             const uint64_t *turns, int64_t t0, int n, int pairs, float scale) {
+    for (int e = threadIdx.x; e < n * pairs; e += kNormThreads) {
+        const int k = e / pairs, i = e - k * pairs;
+        const float2 cs = rotary_angle(turns[i], positions[t0 + k]);
+        s_angle[k][i] = make_float2(cs.x * scale, cs.y * scale);
+    }
+}
+
+// Turns the lane's columns x (and y, kHalves) by the angles of its token, or back.
+// partner: of kGather, the columns' partners.
+template <int MODE, bool BACK>
+__device__ __forceinline__ void turn(const Columns<MODE> &col, const float2 *angle, int pairs, float (&x)[8],
+                                     float (&y)[8]) {
+    if (MODE == kHalves) {
+        if (!col.turns) return;
+        const float4 *const at = reinterpret_cast<const float4 *>(angle + col.c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 u = at[i];
+            const float c0 = u.x, s0 = BACK ? -u.y : u.y, c1 = u.z, s1 = BACK ? -u.w : u.w;
+            const float a = x[2 * i], b = x[2 * i + 1];
+            x[2 * i] = a * c0 - y[2 * i] * s0;
+            y[2 * i] = a * s0 + y[2 * i] * c0;
+            x[2 * i + 1] = b * c1 - y[2 * i + 1] * s1;
+            y[2 * i + 1] = b * s1 + y[2 * i + 1] * c1;
+        }
+    } else if (MODE == kInterleaved) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (col.c / 2 + i >= pairs) break;  // columns behind the last pair stay
+            const float2 u = angle[col.c / 2 + i];
+            const float s = BACK ? -u.y : u.y, a = x[2 * i], b = x[2 * i + 1];
+            x[2 * i] = a * u.x - b * s;
+            x[2 * i + 1] = a * s + b * u.x;
+        }
+    } else {  // y: the partners
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int j = col.c + i;
+            if (j >= 2 * pairs) break;
+            const bool second = j >= pairs;
+            const float2 u = angle[second ? j - pairs : j];
+            const float s = BACK != second ? u.y : -u.y;
+            x[i] = x[i] * u.x + y[i] * s;
+        }
+    }
+}
+// Column of the partner of column j, or j itself.
+__device__ __forceinline__ int partner_of(int j, int pairs) {
+    return j < pairs ? j + pairs : j < 2 * pairs ? j - pairs : j;
+}
+
+// Eight fp32 values as 8 bytes of e4m3: beyond 448 the largest value, NaN as NaN.
+__device__ __forceinline__ uint2 pack_e4m3(const float (&v)[8], float f) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i] * f, v[2 * i + 1] * f), __NV_SATFINITE, __NV_E4M3);
+    return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+}
+
+template <typename T, int MODE, int G, bool Q8>
+__global__ void __launch_bounds__(kNormThreads, kNormCtas)
+    sgmv_norm_rope_kernel(const __grid_constant__ NormParams P, int *err) {
+    const sgmv_rope_args &a = P.a.rope;
+    constexpr int kGroups = kNormThreads / G;
+    constexpr bool kTwo = MODE == kHalves;
+    __shared__ __align__(16) float2 s_angles[2][kChunk][kRopeMaxPairs];
+    const int g = threadIdx.x / G, pairs = a.pairs;
+    const Columns<MODE> col(threadIdx.x % G, P.rot, P.uph, pairs);
+    const bool append = a.k_cache != nullptr;
+    const int heads = a.Hq + a.Hk + (append ? a.Hk : 0);
+    pdl_wait();
+    pdl_trigger();
+    const int all = a.T * heads, own = (all + (int)gridDim.x - 1) / (int)gridDim.x;
+    const int i0 = min(all, own * (int)blockIdx.x), i1 = min(all, i0 + own);
+    // an item's rows, and what is read of them
+    struct Item {
+        int64_t t;
+        int h;
+        uint4 x, y;
+        int32_t slot;
+    };
+    auto fetch = [&](int i, Item &m) {
+        const int it = i / heads;
+        m.t = it;
+        m.h = i - it * heads;
+        m.slot = -1;
+        if (i >= i1) return;
+        const T *src = m.h < a.Hq ? static_cast<const T *>(a.q) + m.t * a.q_token + m.h * a.q_head
+                       : m.h < a.Hq + a.Hk
+                           ? static_cast<const T *>(a.k) + m.t * a.k_token + (m.h - a.Hq) * a.k_head
+                           : static_cast<const T *>(a.v) + m.t * a.v_token + (m.h - a.Hq - a.Hk) * a.v_head;
+        if (col.here) {
+            m.x = *reinterpret_cast<const uint4 *>(src + col.c);
+            if (kTwo && col.turns) m.y = *reinterpret_cast<const uint4 *>(src + col.d);
+            if (MODE == kGather && m.h < a.Hq + a.Hk) {
+                uint16_t *const p = reinterpret_cast<uint16_t *>(&m.y);
+                for (int e = 0; e < 8; ++e)
+                    p[e] = reinterpret_cast<const uint16_t *>(src)[partner_of(col.c + e, pairs)];
+            }
+        }
+        if (append && m.h >= a.Hq) m.slot = a.slots[m.t];
+    };
+    // the weights of this lane's columns
+    uint4 wq[2], wk[2];
+    auto weights = [&](const void *w, uint4 (&to)[2]) {
+        if (!w || !col.here) return;
+        const T *const src = static_cast<const T *>(w);
+        to[0] = *reinterpret_cast<const uint4 *>(src + col.c);
+        if (kTwo && col.turns) to[1] = *reinterpret_cast<const uint4 *>(src + col.d);
+        if (MODE == kGather)
+            for (int e = 0; e < 8; ++e)
+                reinterpret_cast<T *>(&to[1])[e] = src[partner_of(col.c + e, pairs)];
+    };
+    Item next;
+    fetch(i0 + g, next);
+    weights(P.a.q_weight, wq);
+    weights(P.a.k_weight, wk);
+    int buf = 0;
+    for (int c0 = i0; c0 < i1; buf ^= 1) {
+        const int t0 = c0 / heads, c1 = min((int64_t)i1, ((int64_t)t0 + kChunk) * heads);
+        chunk_angles(s_angles[buf], a.positions, P.turns, t0, (c1 - 1) / heads - t0 + 1, pairs, a.scale);
+        __syncthreads();
+        // (whole warps together: the sums are shuffled)
+        for (int ib = c0; ib < c1; ib += kGroups) {
+            const bool mine = ib + g < c1;
+            Item m;
+            if (mine) {
+                m = next;
+                // the group's next item, in this chunk or the next one
+                const int after = ib + g + kGroups;
+                fetch(after < c1 ? after : c1 + g, next);
+            }
+            if (!__any_sync(0xffffffffu, mine)) continue;
+            const bool is_v = mine && m.h >= a.Hq + a.Hk, is_k = mine && m.h >= a.Hq && !is_v;
+            float x[8], y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = y[e] = 0.f;
+            if (mine && col.here) {
+                unpack8<T>(m.x, x);
+                if ((kTwo && col.turns) || (MODE == kGather && !is_v)) unpack8<T>(m.y, y);
+            }
+            const bool normed = mine && !is_v && (is_k ? P.a.k_weight : P.a.q_weight) != nullptr;
+            float ss = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                ss = fmaf(x[e], x[e], ss);
+                if (kTwo) ss = fmaf(y[e], y[e], ss);
+            }
+            ss = group_sum<G>(ss);
+            if (MODE == kGather) __syncwarp();  // in place: partners are read before any is written
+            if (!mine || !col.here) continue;
+            if (normed) {
+                const float r = rsqrtf(ss / (float)a.D + P.a.eps);
+                float w[8];
+                unpack8<T>(is_k ? wk[0] : wq[0], w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] *= r * w[e];
+                if ((kTwo && col.turns) || MODE == kGather) {
+                    unpack8<T>(is_k ? wk[1] : wq[1], w);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] *= r * w[e];
+                }
+            }
+            if (!is_v) turn<MODE, false>(col, s_angles[buf][m.t - t0], pairs, x, y);
+            const bool second = kTwo && col.turns;
+            auto put16 = [&](T *dst) {
+                store8<T>(dst + col.c, x);
+                if (second) store8<T>(dst + col.d, y);
+            };
+            if (!is_k && !is_v) {
+                put16(static_cast<T *>(a.q_out) + m.t * a.q_out_token + m.h * a.q_out_head);
+                continue;
+            }
+            const int h = m.h - a.Hq - (is_v ? a.Hk : 0);
+            if (is_k && a.k_out) put16(static_cast<T *>(a.k_out) + m.t * a.k_out_token + h * a.k_out_head);
+            if (m.slot < 0 || (int64_t)m.slot >= (int64_t)a.num_blocks * a.block_size) {
+                if (m.slot != -1) set_error(err, kErrBadIndex);
+                continue;
+            }
+            const int64_t off = (int64_t)(m.slot / a.block_size) * a.cache_block +
+                                (int64_t)(m.slot % a.block_size) * a.cache_token + h * a.cache_head;
+            if (Q8) {
+                uint8_t *const dst = static_cast<uint8_t *>(is_v ? a.v_cache : a.k_cache) + off;
+                const float f = 1.f / (is_v ? P.a.v_scale : P.a.k_scale)[h];
+                *reinterpret_cast<uint2 *>(dst + col.c) = pack_e4m3(x, f);
+                if (second) *reinterpret_cast<uint2 *>(dst + col.d) = pack_e4m3(y, f);
+            } else {
+                put16(static_cast<T *>(is_v ? a.v_cache : a.k_cache) + off);
+            }
+        }
+        if (c0 + g >= c1) fetch(c1 + g, next);  // no item of this chunk was this group's
+        c0 = c1;
+    }  // the next chunk's angles go to the other buffer: one barrier per chunk
+}
+
+template <typename T, int MODE, int G>
+__global__ void __launch_bounds__(kNormThreads, kNormCtas)
+    sgmv_norm_rope_grad_kernel(const __grid_constant__ GradParams P) {
+    const sgmv_norm_rope_grad_args &a = P.a;
+    constexpr int kGroups = kNormThreads / G;
+    constexpr bool kTwo = MODE == kHalves;
+    __shared__ __align__(16) float2 s_angles[2][kChunk][kRopeMaxPairs];
+    __shared__ float s_dw[kGroups > 8 ? 8 : kGroups][kSpecMaxD];
+    const int g = threadIdx.x / G, pairs = a.pairs;
+    const Columns<MODE> col(threadIdx.x % G, P.rot, P.uph, pairs);
+    pdl_wait();
+    pdl_trigger();
+    const bool is_k = (int)blockIdx.x >= P.ctas_q;
+    const int heads = is_k ? a.Hk : a.Hq;
+    const int cta = (int)blockIdx.x - (is_k ? P.ctas_q : 0), ctas = is_k ? (int)gridDim.x - P.ctas_q : P.ctas_q;
+    const T *const X = static_cast<const T *>(is_k ? a.k : a.q);
+    const T *const DY = static_cast<const T *>(is_k ? a.dk_out : a.dq_out);
+    T *const DX = static_cast<T *>(is_k ? a.dk : a.dq);
+    const T *const W = static_cast<const T *>(is_k ? a.k_weight : a.q_weight);
+    const int64_t x_token = is_k ? a.k_token : a.q_token, x_head = is_k ? a.k_head : a.q_head;
+    const int64_t dy_token = is_k ? a.dk_out_token : a.dq_out_token, dy_head = is_k ? a.dk_out_head : a.dq_out_head;
+    const int64_t dx_token = is_k ? a.dk_token : a.dq_token, dx_head = is_k ? a.dk_head : a.dq_head;
+    const int all = a.T * heads, own = (all + ctas - 1) / ctas;
+    const int i0 = min(all, own * cta), i1 = min(all, i0 + own);
+    struct Item {
+        uint4 x, y, gx, gy;
+    };
+    auto fetch = [&](int i, Item &m) {
+        if (i >= i1 || !col.here) return;
+        const int it = i / heads;
+        const int64_t t = it, h = i - it * heads;
+        const T *const dy = DY + t * dy_token + h * dy_head, *const x = X + t * x_token + h * x_head;
+        m.gx = *reinterpret_cast<const uint4 *>(dy + col.c);
+        if (W) m.x = *reinterpret_cast<const uint4 *>(x + col.c);
+        if (kTwo && col.turns) {
+            m.gy = *reinterpret_cast<const uint4 *>(dy + col.d);
+            if (W) m.y = *reinterpret_cast<const uint4 *>(x + col.d);
+        }
+        if (MODE == kGather)
+            for (int e = 0; e < 8; ++e)
+                reinterpret_cast<T *>(&m.gy)[e] = dy[partner_of(col.c + e, pairs)];
+    };
+    float w[8], v[8], dw[8], dv[8];  // weights of the lane's columns, and their gradients
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = v[e] = 1.f, dw[e] = dv[e] = 0.f;
+    if (W && col.here) {
+        load8<T>(W + col.c, w);
+        if (kTwo && col.turns) load8<T>(W + col.d, v);
+    }
+    Item next;
+    fetch(i0 + g, next);
+    int buf = 0;
+    for (int c0 = i0; c0 < i1; buf ^= 1) {
+        const int t0 = c0 / heads, c1 = min((int64_t)i1, ((int64_t)t0 + kChunk) * heads);
+        chunk_angles(s_angles[buf], a.positions, P.turns, t0, (c1 - 1) / heads - t0 + 1, pairs, a.scale);
+        __syncthreads();
+        for (int ib = c0; ib < c1; ib += kGroups) {
+            const int i = ib + g;
+            const bool mine = i < c1;
+            Item m;
+            if (mine) {
+                m = next;
+                fetch(i + kGroups < c1 ? i + kGroups : c1 + g, next);
+            }
+            if (!__any_sync(0xffffffffu, mine)) continue;
+            const bool on = mine && col.here, second = kTwo && col.turns;
+            float gx[8], gy[8], x[8], y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) gx[e] = gy[e] = x[e] = y[e] = 0.f;
+            const int it = i / heads;
+            const int64_t t = it, h = i - it * heads;
+            if (on) {
+                unpack8<T>(m.gx, gx);
+                if (second || MODE == kGather) unpack8<T>(m.gy, gy);
+                if (W) unpack8<T>(m.x, x);
+                if (W && second) unpack8<T>(m.y, y);
+                turn<MODE, true>(col, s_angles[buf][t - t0], pairs, gx, gy);
+            }
+            if (W) {
+                // sum x^2, and sum of w g x: then mean(h * xh) = r / D times it
+                float ss = 0.f, dot = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    ss = fmaf(x[e], x[e], ss);
+                    dot = fmaf(w[e] * gx[e], x[e], dot);
+                    if (kTwo) {
+                        ss = fmaf(y[e], y[e], ss);
+                        dot = fmaf(v[e] * gy[e], y[e], dot);
+                    }
+                }
+                ss = group_sum<G>(ss);
+                dot = group_sum<G>(dot);
+                const float r = rsqrtf(ss / (float)a.D + a.eps), f = dot * r / (float)a.D * r;
+                if (on) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        dw[e] = fmaf(gx[e], x[e] * r, dw[e]);
+                        gx[e] = r * (w[e] * gx[e] - f * x[e]);
+                        if (kTwo) {
+                            dv[e] = fmaf(gy[e], y[e] * r, dv[e]);
+                            gy[e] = r * (v[e] * gy[e] - f * y[e]);
+                        }
+                    }
+                }
+            }
+            if (on) {
+                T *const dx = DX + t * dx_token + h * dx_head;
+                store8<T>(dx + col.c, gx);
+                if (second) store8<T>(dx + col.d, gy);
+            }
+        }
+        if (c0 + g >= c1) fetch(c1 + g, next);
+        c0 = c1;
+    }
+    if (!W) return;
+    // the groups' sums, in order: over the warp, then over the eight warps
+    constexpr int kWarpGroups = 32 / G;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+#pragma unroll
+        for (int o = G; o < 32; o <<= 1) {
+            dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], o);
+            if (kTwo) dv[e] += __shfl_xor_sync(0xffffffffu, dv[e], o);
+        }
+    const int warp = threadIdx.x / 32;
+    static_assert(kNormThreads / 32 <= 8 && (kGroups >= 8 || kWarpGroups == 1), "a row of sums per warp");
+    if ((threadIdx.x & 31) < G && col.here) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            s_dw[warp][col.c + e] = dw[e];
+            if (kTwo && col.turns) s_dw[warp][col.d + e] = dv[e];
+        }
+    }
+    __syncthreads();
+    for (int d = threadIdx.x; d < a.D; d += kNormThreads) {
+        float sum = 0.f;
+        for (int i = 0; i < kNormThreads / 32; ++i) sum += s_dw[i][d];
+        P.part[(int64_t)blockIdx.x * a.D + d] = sum;
+    }
+}
+
+// dw of a column of q (blockIdx.y 0) or k: the CTAs' sums added up, 32 columns and
+// 32 strands a CTA.
+__global__ void __launch_bounds__(1024) sgmv_norm_rope_dw_kernel(const float *part, float *dwq, float *dwk, int D,
+                                                                 int ctas_q, int ctas) {
+    __shared__ double s_sum[32][33];
+    pdl_wait();
+    pdl_trigger();
+    const int d = blockIdx.x * 32 + (threadIdx.x & 31), strand = threadIdx.x >> 5;
+    float *const dw = blockIdx.y ? dwk : dwq;
+    if (!dw) return;
+    double sum = 0.0;
+    if (d < D)
+        for (int i = (blockIdx.y ? ctas_q : 0) + strand; i < (blockIdx.y ? ctas : ctas_q); i += 32)
+            sum += (double)part[(int64_t)i * D + d];
+    s_sum[strand][threadIdx.x & 31] = sum;
+    __syncthreads();
+    if (strand == 0 && d < D) {
+        for (int i = 1; i < 32; ++i) sum += s_sum[i][threadIdx.x];
+        dw[d] = (float)sum;
+    }
+}
+
+// Lanes of a group: a power of two that holds the columns.
+int lanes(int uph) { return uph <= 4 ? 4 : uph <= 8 ? 8 : uph <= 16 ? 16 : 32; }
+int mode_of(int interleaved, int pairs) {
+    return interleaved ? kInterleaved : pairs % 8 == 0 ? kHalves : kGather;
+}
+void places(int mode, int D, int pairs, int32_t *rot, int32_t *uph) {
+    *rot = mode == kHalves ? pairs / 8 : D / 8;
+    *uph = mode == kHalves ? pairs / 8 + (D - 2 * pairs) / 8 : D / 8;
+}
+
+template <typename T, int MODE, int G> int launch(const NormParams &p, int nsm, int *err, cudaStream_t stream) {
+    const sgmv_rope_args &a = p.a.rope;
+    const int64_t items = (int64_t)a.T * (a.Hq + a.Hk + (a.k_cache ? a.Hk : 0)), groups = kNormThreads / G;
+    const dim3 grid((unsigned)std::min<int64_t>((items + groups - 1) / groups, (int64_t)kNormCtas * std::max(1, nsm)));
+    return p.a.k_scale
+               ? spec_launch(sgmv_norm_rope_kernel<T, MODE, G, true>, grid, kNormThreads, 0, 1, stream, p, err)
+               : spec_launch(sgmv_norm_rope_kernel<T, MODE, G, false>, grid, kNormThreads, 0, 1, stream, p, err);
+}
+template <typename T, int MODE> int launch_lanes(const NormParams &p, int nsm, int *err, cudaStream_t stream) {
+    switch (lanes(p.uph)) {
+        case 4: return launch<T, MODE, 4>(p, nsm, err, stream);
+        case 8: return launch<T, MODE, 8>(p, nsm, err, stream);
+        case 16: return launch<T, MODE, 16>(p, nsm, err, stream);
+        default: return launch<T, MODE, 32>(p, nsm, err, stream);
+    }
+}
+template <typename T> int launch_mode(const NormParams &p, int mode, int nsm, int *err, cudaStream_t stream) {
+    switch (mode) {
+        case kHalves: return launch_lanes<T, kHalves>(p, nsm, err, stream);
+        case kInterleaved: return launch_lanes<T, kInterleaved>(p, nsm, err, stream);
+        default: return launch_lanes<T, kGather>(p, nsm, err, stream);
+    }
+}
+
+template <typename T, int MODE, int G> int launch_grad(GradParams p, int nsm, cudaStream_t stream) {
+    const sgmv_norm_rope_grad_args &a = p.a;
+    // CTAs to q and k by their rows
+    const int64_t most = (int64_t)kNormCtas * std::min(std::max(1, nsm), kGradMaxSms), groups = kNormThreads / G;
+    const int64_t q = ((int64_t)a.T * a.Hq + groups - 1) / groups, k = ((int64_t)a.T * a.Hk + groups - 1) / groups;
+    int64_t nq = q, nk = k;
+    if (q + k > most) {
+        nq = q == 0 ? 0 : std::min(q, std::max<int64_t>(1, most * q / (q + k)));
+        nk = k == 0 ? 0 : std::max<int64_t>(1, most - nq);
+        if (nq + nk > most) nq = most - nk;
+    }
+    p.ctas_q = (int)nq;
+    if (nq + nk > 0) {  // (no rows: the weights' gradients are zero)
+        const int r = spec_launch(sgmv_norm_rope_grad_kernel<T, MODE, G>, dim3((unsigned)(nq + nk)), kNormThreads, 0,
+                                  1, stream, p);
+        if (r != (int)cudaSuccess) return r;
+    }
+    if (!a.dq_weight && !a.dk_weight) return (int)cudaSuccess;
+    return spec_launch(sgmv_norm_rope_dw_kernel, dim3((unsigned)((a.D + 31) / 32), 2), 1024, 0, 1, stream, p.part,
+                       a.dq_weight, a.dk_weight, (int)a.D, (int)nq, (int)(nq + nk));
+}
+template <typename T, int MODE> int launch_grad_lanes(const GradParams &p, int nsm, cudaStream_t stream) {
+    switch (lanes(p.uph)) {
+        case 4: return launch_grad<T, MODE, 4>(p, nsm, stream);
+        case 8: return launch_grad<T, MODE, 8>(p, nsm, stream);
+        case 16: return launch_grad<T, MODE, 16>(p, nsm, stream);
+        default: return launch_grad<T, MODE, 32>(p, nsm, stream);
+    }
+}
+template <typename T> int launch_grad_mode(const GradParams &p, int mode, int nsm, cudaStream_t stream) {
+    switch (mode) {
+        case kHalves: return launch_grad_lanes<T, kHalves>(p, nsm, stream);
+        case kInterleaved: return launch_grad_lanes<T, kInterleaved>(p, nsm, stream);
+        default: return launch_grad_lanes<T, kGather>(p, nsm, stream);
+    }
+}
+
+}  // namespace
+
+int norm_rope_launch(const sgmv_norm_rope_args &a, const uint64_t *turns, int nsm, int *err, cudaStream_t stream) {
+    NormParams p;
+    p.a = a;
+    for (int i = 0; i < a.rope.pairs; ++i) p.turns[i] = turns[i];
+    const int mode = mode_of(a.rope.interleaved, a.rope.pairs);
+    places(mode, a.rope.D, a.rope.pairs, &p.rot, &p.uph);
+    return a.rope.dtype == SGMV_F16 ? launch_mode<__half>(p, mode, nsm, err, stream)
+                                    : launch_mode<__nv_bfloat16>(p, mode, nsm, err, stream);
+}
+
+size_t norm_rope_grad_workspace(int32_t D) { return (size_t)kNormCtas * kGradMaxSms * (size_t)D * 4u; }
+
+int norm_rope_grad_launch(const sgmv_norm_rope_grad_args &a, const uint64_t *turns, int nsm, cudaStream_t stream) {
+    GradParams p;
+    p.a = a;
+    p.part = static_cast<float *>(a.workspace);
+    for (int i = 0; i < a.pairs; ++i) p.turns[i] = turns[i];
+    const int mode = mode_of(a.interleaved, a.pairs);
+    places(mode, a.D, a.pairs, &p.rot, &p.uph);
+    return a.dtype == SGMV_F16 ? launch_grad_mode<__half>(p, mode, nsm, stream)
+                               : launch_grad_mode<__nv_bfloat16>(p, mode, nsm, stream);
+}
+
+}  // namespace sgmv

@@ -93,11 +93,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
     load(h0, vh0);
 
     if (tid < pairs) {
-        const uint64_t turn = (uint64_t)(int64_t)pos * per_position;  // modulo one turn
-        const float half_turns = (float)(int32_t)(turn >> 32) * 0x1p-31f;
-        float sn, cs;
-        sincospif(half_turns, &sn, &cs);
-        s_angle[tid] = make_float2(cs * a.scale, (a.inverse ? -sn : sn) * a.scale);
+        const float2 u = rotary_angle(per_position, pos);
+        s_angle[tid] = make_float2(u.x * a.scale, (a.inverse ? -u.y : u.y) * a.scale);
     }
     int64_t slot_off = -1;
     if (slot >= 0 && (int64_t)slot < (int64_t)a.num_blocks * a.block_size)

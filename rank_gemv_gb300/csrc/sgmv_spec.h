@@ -1,6 +1,6 @@
-// sgmv_spec.h -- the speculative decoding operators (rotary positions, tree
-// attention, verification, commit): launchers behind the C ABI and the
-// device helpers they share.
+// sgmv_spec.h -- the decoding operators (rotary positions with or without head
+// norms, tree attention over 16-bit and e4m3 caches, sampling, verification,
+// commit): launchers behind the C ABI and the device helpers they share.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -21,6 +21,15 @@ template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) 
 template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&h);
+}
+// Cosine and sine of the angle of a pair at a position; turns: its turns per position,
+// modulo one, times 2^64 (the product wraps modulo one turn by itself).
+__device__ __forceinline__ float2 rotary_angle(uint64_t turns, int32_t position) {
+    const uint64_t turn = (uint64_t)(int64_t)position * turns;
+    const float half_turns = (float)(int32_t)(turn >> 32) * 0x1p-31f;
+    float sn, cs;
+    sincospif(half_turns, &sn, &cs);
+    return make_float2(cs, sn);
 }
 #endif
 
@@ -44,6 +53,14 @@ int tree_mma_launch(const sgmv_tree_attention_args &a, int nsm, int *err, cudaSt
 size_t tree_attention_workspace(int32_t T, int32_t Hq, int32_t Hkv, int32_t D);
 int tree_verify_launch(const sgmv_tree_verify_args &a, int nsm, int *err, cudaStream_t stream);
 int cache_commit_launch(const sgmv_cache_commit_args &a, int *err, cudaStream_t stream);
+int norm_rope_launch(const sgmv_norm_rope_args &a, const uint64_t *turns, int nsm, int *err,
+                     cudaStream_t stream);
+constexpr int kGradMaxSms = 152;  // of which the gradient's workspace holds sums
+size_t norm_rope_grad_workspace(int32_t D);
+int norm_rope_grad_launch(const sgmv_norm_rope_grad_args &a, const uint64_t *turns, int nsm,
+                          cudaStream_t stream);
+int quant_mma_launch(const sgmv_quant_attention_args &a, int nsm, int *err, cudaStream_t stream);
+int sample_launch(const sgmv_sample_args &a, int nsm, cudaStream_t stream);
 
 // Records how many kernels the calling thread's last call launched.
 void set_launch_count(int n);

@@ -18,8 +18,9 @@ import torch
 
 LIB_PATH = Path(__file__).resolve().parent / "libsgmv.so"
 
-SGMV_F16, SGMV_BF16, SGMV_F32 = 0, 1, 2
+SGMV_F16, SGMV_BF16, SGMV_F32, SGMV_E4M3 = 0, 1, 2, 3
 _DTYPES = {torch.float16: SGMV_F16, torch.bfloat16: SGMV_BF16, torch.float32: SGMV_F32}
+_CACHE_DTYPES = {**_DTYPES, torch.float8_e4m3fn: SGMV_E4M3}
 
 STATUS = {0: "SGMV_OK", 1: "SGMV_ERR_INVALID_ARG", 2: "SGMV_ERR_UNSUPPORTED",
           3: "SGMV_ERR_ALIGNMENT", 4: "SGMV_ERR_BAD_INDEX", 5: "SGMV_ERR_CUDA",
@@ -63,6 +64,12 @@ SIGNATURES = {
     "sgmv_tree_attention": (_int, [_cp, _vp]),
     "sgmv_tree_verify": (_int, [_cp, _vp]),
     "sgmv_cache_commit": (_int, [_cp, _vp]),
+    "sgmv_norm_rope": (_int, [_cp, _vp]),
+    "sgmv_norm_rope_grad_workspace_bytes": (_sz, [_i32]),
+    "sgmv_norm_rope_grad": (_int, [_cp, _vp]),
+    "sgmv_quant_attention_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32, _i32]),
+    "sgmv_quant_attention": (_int, [_cp, _vp]),
+    "sgmv_sample": (_int, [_cp, _vp]),
     "sgmv_debug_inject_wait_timeout": (_int, [_int]),
     "sgmv_get_device_error": (_int, [_vp]),
 }
@@ -383,12 +390,16 @@ def sgmv_copy_gather(dsts, srcs, stream=None, max_ctas=0):
         _check(lib.sgmv_copy_gather(n, d, s, b, int(max_ctas), st), "sgmv_copy_gather")
 
 
-# Argument structs of the speculative decoding calls (include/sgmv.h), packed
+# Argument structs of the decoding calls (include/sgmv.h), packed
 # with native sizes and alignment (0q: padded to whole 8-byte words).
 _ROPE_ARGS = struct.Struct("@10P13q10if0q")
 _ATTENTION_ARGS = struct.Struct("@10PQ8q9if0q")
 _VERIFY_ARGS = struct.Struct("@10P2q4i0q")
 _COMMIT_ARGS = struct.Struct("@6P5q9i0q")
+_NORM_ARGS = struct.Struct("@4Pf0q")       # behind _ROPE_ARGS
+_NORM_GRAD_ARGS = struct.Struct("@13PQ12q7i2f0q")
+_SCALE_ARGS = struct.Struct("@2P")         # behind _ATTENTION_ARGS
+_SAMPLE_ARGS = struct.Struct("@8P2q4i3f0q")
 
 
 def _heads(t, name, dtype, shape):
@@ -449,6 +460,17 @@ def _uniform(t, name, n):
     return t.data_ptr()
 
 
+def _vector(t, name, dtype, n):
+    """Pointer of a contiguous tensor of n entries of a type (or of None)."""
+    if t is None:
+        return 0
+    if t.dtype != dtype or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous {dtype} tensor")
+    if t.numel() != n:
+        raise ValueError(f"{name} must have {n} entries")
+    return t.data_ptr()
+
+
 def _table(block_table, B):
     if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B or (
             block_table.shape[1] > 1 and block_table.stride(1) != 1):
@@ -466,16 +488,9 @@ def sgmv_rope_frequencies(pairs, base=10000.0, factor=1.0, trained=0.0, slow=flo
     return out
 
 
-def sgmv_rope(q, k, positions, inv_freq, interleaved=False, scale=1.0, inverse=False, q_out=None,
-              k_out=None, v=None, k_cache=None, v_cache=None, slots=None):
-    """Rotary positions of q [T, Hq, D] and k [T, Hk, D] (either may be None);
-    returns (q_out, k_out).
-
-    Without q_out q is rotated in place; without k_out k is rotated in place,
-    unless caches are given: then the rotated k and the unchanged v go to the
-    cache slots `slots` only (-1: not appended).  inv_freq: float64 CPU tensor
-    of the rotated pairs (sgmv_rope_frequencies); inverse=True turns back, the
-    gradient of the rotation."""
+def _rope_args(q, k, positions, inv_freq, interleaved, scale, inverse, q_out, k_out, v, k_cache, v_cache, slots,
+               cache_dtype):
+    """(packed sgmv_rope_args, q_out, k_out, device) of the rotary calls; cache_dtype: None for q's."""
     first = q if q is not None else k
     if first is None:
         raise ValueError("q or k must be given")
@@ -514,7 +529,7 @@ def sgmv_rope(q, k, positions, inv_freq, interleaved=False, scale=1.0, inverse=F
     else:
         if k is None or v is None or v_cache is None or slots is None:
             raise ValueError("an append needs k, v, k_cache, v_cache and slots")
-        cshape, cs = _cache(k_cache, v_cache, dtype, 4)
+        cshape, cs = _cache(k_cache, v_cache, cache_dtype or dtype, 4)
         vi = _heads(v, "v", dtype, kshape)
         blocks, bs, ch, cd = cshape
         if ch != Hk or cd != D:
@@ -525,13 +540,56 @@ def sgmv_rope(q, k, positions, inv_freq, interleaved=False, scale=1.0, inverse=F
         _list(slots, "slots", T), inv_freq.data_ptr(), qo[1], qo[2], qi[1], qi[2], ko[1], ko[2],
         ki[1], ki[2], vi[1], vi[2], cs[0], cs[1], cs[2], T, Hq, Hk, D, inv_freq.numel(), blocks, bs,
         _DTYPES[dtype], interleaved, inverse, scale)
+    return args, q_out, k_out, first.device
+
+
+def sgmv_rope(q, k, positions, inv_freq, interleaved=False, scale=1.0, inverse=False, q_out=None,
+              k_out=None, v=None, k_cache=None, v_cache=None, slots=None):
+    """Rotary positions of q [T, Hq, D] and k [T, Hk, D] (either may be None);
+    returns (q_out, k_out).
+
+    Without q_out q is rotated in place; without k_out k is rotated in place,
+    unless caches are given: then the rotated k and the unchanged v go to the
+    cache slots `slots` only (-1: not appended).  inv_freq: float64 CPU tensor
+    of the rotated pairs (sgmv_rope_frequencies); inverse=True turns back, the
+    gradient of the rotation."""
+    args, q_out, k_out, device = _rope_args(q, k, positions, inv_freq, interleaved, scale, inverse, q_out, k_out,
+                                            v, k_cache, v_cache, slots, None)
     _on_gpu((q, k, q_out, k_out, v, k_cache, v_cache, positions, slots))
-    _check(load_library().sgmv_rope(args, _stream(first.device)), "sgmv_rope")
+    _check(load_library().sgmv_rope(args, _stream(device)), "sgmv_rope")
     return q_out, k_out
 
 
 def sgmv_tree_attention_workspace_bytes(T: int, B: int, Hq: int, Hkv: int, D: int) -> int:
     return int(load_library().sgmv_tree_attention_workspace_bytes(T, B, Hq, Hkv, D))
+
+
+def _attention_args(out, q, k_cache, v_cache, block_table, prefix_lens, tree_ptr, parents, scale, lse, workspace,
+                    cache_dtype, workspace_bytes):
+    """(packed sgmv_tree_attention_args, workspace) of the attention calls."""
+    qshape, dtype = q.shape, q.dtype
+    if len(qshape) != 3 or dtype not in _DTYPES:
+        raise TypeError("q must be a [T, heads, D] tensor of f16 or bf16")
+    T, Hq, D = qshape
+    B = prefix_lens.numel()
+    qi, oo = _heads(q, "q", dtype, qshape), _heads(out, "out", dtype, qshape)
+    shape, cs = _cache(k_cache, v_cache, cache_dtype, 4)
+    if shape[3] != D:
+        raise ValueError("q and the caches differ in head size")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, Hq) or not lse.is_contiguous()):
+        raise TypeError("lse must be a contiguous float32 [T, Hq] tensor")
+    table, width, row = _table(block_table, B)
+    if workspace is None:
+        workspace = torch.empty(workspace_bytes(T, B, Hq, shape[2], D),
+                                dtype=torch.uint8, device=q.device)
+    args = _ATTENTION_ARGS.pack(
+        oo[0], qi[0], k_cache.data_ptr(), v_cache.data_ptr(), 0 if lse is None else lse.data_ptr(),
+        table, _list(prefix_lens, "prefix_lens", B), _list(tree_ptr, "tree_ptr", B + 1),
+        _list(parents, "parents", T), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), oo[1], oo[2], qi[1], qi[2], cs[0], cs[1],
+        cs[2], row, T, B, Hq, shape[2], D, shape[0], shape[1], width, _DTYPES[dtype],
+        D ** -0.5 if scale is None else scale)
+    return args, workspace
 
 
 def sgmv_tree_attention(out, q, k_cache, v_cache, block_table, prefix_lens, tree_ptr, parents=None,
@@ -545,29 +603,9 @@ def sgmv_tree_attention(out, q, k_cache, v_cache, block_table, prefix_lens, tree
     the log-sum-exp.  workspace: uint8 device tensor of at least
     sgmv_tree_attention_workspace_bytes(T, B, Hq, Hkv, D) bytes (those of the
     largest T and B serve every batch); one is allocated when None."""
-    qshape, dtype = q.shape, q.dtype
-    if len(qshape) != 3 or dtype not in _DTYPES:
-        raise TypeError("q must be a [T, heads, D] tensor of f16 or bf16")
-    T, Hq, D = qshape
-    B = prefix_lens.numel()
-    qi, oo = _heads(q, "q", dtype, qshape), _heads(out, "out", dtype, qshape)
-    shape, cs = _cache(k_cache, v_cache, dtype, 4)
-    if shape[3] != D:
-        raise ValueError("q and the caches differ in head size")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, Hq) or not lse.is_contiguous()):
-        raise TypeError("lse must be a contiguous float32 [T, Hq] tensor")
-    table, width, row = _table(block_table, B)
     lib = load_library()
-    if workspace is None:
-        workspace = torch.empty(lib.sgmv_tree_attention_workspace_bytes(T, B, Hq, shape[2], D),
-                                dtype=torch.uint8, device=q.device)
-    args = _ATTENTION_ARGS.pack(
-        oo[0], qi[0], k_cache.data_ptr(), v_cache.data_ptr(), 0 if lse is None else lse.data_ptr(),
-        table, _list(prefix_lens, "prefix_lens", B), _list(tree_ptr, "tree_ptr", B + 1),
-        _list(parents, "parents", T), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), oo[1], oo[2], qi[1], qi[2], cs[0], cs[1],
-        cs[2], row, T, B, Hq, shape[2], D, shape[0], shape[1], width, _DTYPES[dtype],
-        D ** -0.5 if scale is None else scale)
+    args, workspace = _attention_args(out, q, k_cache, v_cache, block_table, prefix_lens, tree_ptr, parents, scale,
+                                      lse, workspace, q.dtype, lib.sgmv_tree_attention_workspace_bytes)
     _on_gpu((q, out, k_cache, v_cache, lse, block_table, prefix_lens, tree_ptr, parents, workspace))
     _check(lib.sgmv_tree_attention(args, _stream(q.device)), "sgmv_tree_attention")
     return out
@@ -605,8 +643,8 @@ def sgmv_cache_commit(k_cache, v_cache, block_table, prefix_lens, path, count):
     sgmv_tree_verify returns them) to their final places in the caches
     [blocks, block_size, Hkv, D] or [layers, blocks, block_size, Hkv, D], in place."""
     dtype = k_cache.dtype
-    if dtype not in _DTYPES:
-        raise TypeError("the caches must be f16 or bf16")
+    if dtype not in _CACHE_DTYPES:
+        raise TypeError("the caches must be f16, bf16 or e4m3")
     ndim = 5 if k_cache.dim() == 5 else 4
     shape, cs = _cache(k_cache, v_cache, dtype, ndim)
     layers, layer_stride = (shape[0], cs[0]) if ndim == 5 else (1, 0)
@@ -616,9 +654,148 @@ def sgmv_cache_commit(k_cache, v_cache, block_table, prefix_lens, path, count):
     args = _COMMIT_ARGS.pack(
         k_cache.data_ptr(), v_cache.data_ptr(), table, _list(prefix_lens, "prefix_lens", B),
         _list(path, "path", B * width), _list(count, "count", B), layer_stride, cs[-4], cs[-3],
-        cs[-2], row, layers, B, Hkv, D, blocks, bs, max_blocks, width, _DTYPES[dtype])
+        cs[-2], row, layers, B, Hkv, D, blocks, bs, max_blocks, width, _CACHE_DTYPES[dtype])
     _on_gpu((k_cache, v_cache, block_table, prefix_lens, path, count))
     _check(load_library().sgmv_cache_commit(args, _stream(k_cache.device)), "sgmv_cache_commit")
+
+
+def sgmv_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, scale=1.0,
+                   q_out=None, k_out=None, v=None, k_cache=None, v_cache=None, slots=None, k_scale=None, v_scale=None):
+    """RMS norms of q's and k's heads (weights [D] of their type; None: that tensor is
+    not normalised), then everything as sgmv_rope does; returns (q_out, k_out).
+
+    Caches of float8_e4m3fn take k and v in multiples of k_scale and v_scale (fp32
+    [Hk]); caches of q's type take no scales."""
+    e4m3 = k_scale is not None or v_scale is not None
+    if e4m3 and (k_scale is None or v_scale is None or k_cache is None):
+        raise ValueError("e4m3 caches need k_scale and v_scale, and these the caches")
+    args, q_out, k_out, device = _rope_args(q, k, positions, inv_freq, interleaved, scale, False, q_out, k_out, v,
+                                            k_cache, v_cache, slots, torch.float8_e4m3fn if e4m3 else None)
+    first = q if q is not None else k
+    if (q is None and q_weight is not None) or (k is None and k_weight is not None):
+        raise ValueError("a weight without its tensor")
+    D = first.shape[2]
+    args += _NORM_ARGS.pack(
+        _vector(q_weight, "q_weight", first.dtype, D), _vector(k_weight, "k_weight", first.dtype, D),
+        _vector(k_scale, "k_scale", _F32, k.shape[1] if e4m3 else 0),
+        _vector(v_scale, "v_scale", _F32, k.shape[1] if e4m3 else 0), eps)
+    _on_gpu((q, k, q_out, k_out, v, k_cache, v_cache, positions, slots, q_weight, k_weight, k_scale, v_scale))
+    _check(load_library().sgmv_norm_rope(args, _stream(device)), "sgmv_norm_rope")
+    return q_out, k_out
+
+
+def sgmv_norm_rope_grad_workspace_bytes(D: int) -> int:
+    return int(load_library().sgmv_norm_rope_grad_workspace_bytes(D))
+
+
+def sgmv_norm_rope_grad(dq_out, dk_out, q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6,
+                        interleaved=False, scale=1.0, dq=None, dk=None, dq_weight=None, dk_weight=None,
+                        workspace=None):
+    """Gradients (dq, dk, dq_weight, dk_weight) of sgmv_norm_rope's inputs from those of
+    its outputs, dq_out [T, Hq, D] and dk_out [T, Hk, D] (either may be None, with all
+    that belongs to it).  q and k, the inputs of that call, are needed with their
+    weights; the weights' gradients are fp32 [D] (None without a weight), written to
+    dq_weight and dk_weight if those are given.  workspace: uint8 device tensor of at
+    least sgmv_norm_rope_grad_workspace_bytes(D) bytes; one is allocated when None."""
+    first = dq_out if dq_out is not None else dk_out
+    if first is None:
+        raise ValueError("dq_out or dk_out must be given")
+    dtype, device = first.dtype, first.device
+    if first.dim() != 3 or dtype not in _DTYPES:
+        raise TypeError("dq_out and dk_out must be [T, heads, D] tensors of f16 or bf16")
+    T, D = first.shape[0], first.shape[2]
+    if inv_freq.dtype != torch.float64 or inv_freq.is_cuda or not inv_freq.is_contiguous():
+        raise TypeError("inv_freq must be a contiguous float64 CPU tensor")
+
+    def side(name, dy, x, dx, w, dw):
+        """Heads, the tensors' pointers and strides, and the outputs of q or k."""
+        if dy is None:
+            if any(t is not None for t in (x, dx, w, dw)):
+                raise ValueError(f"d{name}_out is not given")
+            return 0, (0, 0, 0), (0, 0, 0), (0, 0, 0), 0, 0, None, None
+        shape = (T, dy.shape[1], D) if dy.dim() == 3 else (T, 0, D)
+        dyp = _heads(dy, f"d{name}_out", dtype, shape)
+        if w is None and dw is not None:
+            raise ValueError(f"d{name}_weight without {name}_weight")
+        if w is not None and x is None:
+            raise ValueError(f"{name}_weight without {name}")
+        xp = (0, 0, 0) if w is None else _heads(x, name, dtype, shape)
+        if dx is None:
+            dx = torch.empty(shape, dtype=dtype, device=device)
+        if w is not None and dw is None:
+            dw = torch.empty(D, dtype=_F32, device=device)
+        return (shape[1], dyp, xp, _heads(dx, f"d{name}", dtype, shape), _vector(w, f"{name}_weight", dtype, D),
+                _vector(dw, f"d{name}_weight", _F32, D), dx, dw)
+
+    Hq, dyq, xq, dxq, wq, dwq, dq, dq_weight = side("q", dq_out, q, dq, q_weight, dq_weight)
+    Hk, dyk, xk, dxk, wk, dwk, dk, dk_weight = side("k", dk_out, k, dk, k_weight, dk_weight)
+    lib = load_library()
+    if workspace is None and (wq or wk):
+        workspace = torch.empty(lib.sgmv_norm_rope_grad_workspace_bytes(D), dtype=torch.uint8, device=device)
+    args = _NORM_GRAD_ARGS.pack(
+        dxq[0], dxk[0], dyq[0], dyk[0], xq[0], xk[0], wq, wk, dwq, dwk, _list(positions, "positions", T),
+        inv_freq.data_ptr(), 0 if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), dxq[1], dxq[2], dxk[1], dxk[2],
+        dyq[1], dyq[2], dyk[1], dyk[2], xq[1], xq[2], xk[1], xk[2], T, Hq, Hk, D, inv_freq.numel(), _DTYPES[dtype],
+        interleaved, scale, eps)
+    _on_gpu((dq_out, dk_out, q, k, positions, q_weight, k_weight, dq, dk, dq_weight, dk_weight, workspace))
+    _check(lib.sgmv_norm_rope_grad(args, _stream(device)), "sgmv_norm_rope_grad")
+    return dq, dk, dq_weight, dk_weight
+
+
+def sgmv_quant_attention_workspace_bytes(T: int, B: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(load_library().sgmv_quant_attention_workspace_bytes(T, B, Hq, Hkv, D))
+
+
+def sgmv_quant_attention(out, q, k_cache, v_cache, k_scale, v_scale, block_table, prefix_lens, tree_ptr, parents=None,
+                         scale=None, lse=None, workspace=None):
+    """sgmv_tree_attention over caches of float8_e4m3fn, whose values are multiples of
+    k_scale and v_scale (fp32 [Hkv]), for heads of up to 128 columns; returns out.
+    workspace: at least sgmv_quant_attention_workspace_bytes(T, B, Hq, Hkv, D) bytes."""
+    lib = load_library()
+    args, workspace = _attention_args(out, q, k_cache, v_cache, block_table, prefix_lens, tree_ptr, parents, scale,
+                                      lse, workspace, torch.float8_e4m3fn, lib.sgmv_quant_attention_workspace_bytes)
+    heads = k_cache.shape[2]
+    args += _SCALE_ARGS.pack(_vector(k_scale, "k_scale", _F32, heads), _vector(v_scale, "v_scale", _F32, heads))
+    _on_gpu((q, out, k_cache, v_cache, k_scale, v_scale, lse, block_table, prefix_lens, tree_ptr, parents, workspace))
+    _check(lib.sgmv_quant_attention(args, _stream(q.device)), "sgmv_quant_attention")
+    return out
+
+
+def _setting(x, name, dtype, T):
+    """(pointer, number) of a sampling setting: a tensor of an entry per row, or a number."""
+    if isinstance(x, torch.Tensor):
+        return _vector(x, name, dtype, T), 0
+    return 0, x
+
+
+def sgmv_sample(logits, u=None, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, token=None, probs=None):
+    """Draw a token per row of logits [T, V] (f16, bf16 or fp32) with the uniform numbers
+    u [T], by temperature, top-k, top-p and min-p (each a number, or a tensor [T]: fp32,
+    top_k int32; what each does and its value for "off": include/sgmv.h).  Returns the
+    tokens, int32 [T] (`token`: such a tensor to write into), or None without u.
+    probs: fp32 [T, V] that receives the filtered distribution, as sgmv_tree_verify
+    takes it."""
+    shape = logits.shape
+    if len(shape) != 2 or logits.dtype not in _DTYPES or (logits.stride(1) != 1 and shape[1] > 1):
+        raise TypeError("logits must be f16, bf16 or float32 [T, V] with contiguous rows")
+    T, V = shape
+    if u is None:
+        if token is not None or probs is None:
+            raise ValueError("a token needs u; without it, probs must be given")
+    elif token is None:
+        token = torch.empty(T, dtype=_I32, device=logits.device)
+    tau, tau_all = _setting(temperature, "temperature", _F32, T)
+    k, k_all = _setting(top_k, "top_k", _I32, T)
+    p, p_all = _setting(top_p, "top_p", _F32, T)
+    m, m_all = _setting(min_p, "min_p", _F32, T)
+    pp, p0 = _rows(probs, "probs", shape)
+    args = _SAMPLE_ARGS.pack(
+        logits.data_ptr(), _vector(u, "u", _F32, T), tau, k, p, m, _list(token, "token", T), pp, logits.stride(0), p0,
+        T, V, _DTYPES[logits.dtype], k_all, tau_all, p_all, m_all)
+    _on_gpu([t for t in (logits, u, token, probs, temperature, top_k, top_p, min_p) if isinstance(t, torch.Tensor)])
+    _check(load_library().sgmv_sample(args, _stream(logits.device)), "sgmv_sample")
+    return token
 
 
 def sgmv_read_floor(src, nbytes, T, L, H1, H2, r, in_dtype=torch.float16, y_dtype=None):
