@@ -35,10 +35,9 @@
 // brings Q in and says which rows see which tree nodes; two that bring K and V
 // into a ring of 32 KB stages, through the block table: by TMA, or, for pages
 // that are no multiple of 8 tokens, with cp.async, 16 bytes per lane.  A cache of
-// e4m3 is brought as it is, into a ring of its own, by four warps (two with 128 rows), each
-// of which then converts its part of the tokens to the queries' type (exactly: every e4m3
-// value is one of both types) into the stages, so that the rest of the kernel, and its
-// accuracy, are those of a 16-bit cache.
+// e4m3 is brought as it is, into a ring of its own, from which four more warps convert it
+// to the queries' type (exactly: every e4m3 value is one of both types) into the
+// stages, so that the rest of the kernel, and its accuracy, are those of a 16-bit cache.
 //
 // Values that a row does not see never reach it: scores are masked after
 // the product, and non-finite v of tree nodes are taken out of the staged
@@ -64,6 +63,7 @@ namespace {
 constexpr int kTok = 128;                // lanes: tokens per tile, at most
 constexpr uint32_t kHalf = kTok * 128u;  // bytes of 64 columns of a tile
 constexpr uint32_t kStage = 2 * kHalf;   // a K or V tile, 128 columns
+constexpr int kLoaders = 64;             // loading threads
 constexpr int kSegs = 4;                 // segments known ahead
 constexpr float kUnset = -3e38f;         // ref of a row that has seen nothing
 constexpr float kBias = 7.f;             // weights are 2^(kBias + score - ref) ...
@@ -73,13 +73,12 @@ constexpr int kSeqTable = 64;            // entries of the table that finds a ti
 constexpr int kMaxParts = 64;            // parts of an item (about)
 
 template <int RT, bool KV8> struct Shape {
-    // loading threads; those of an e4m3 cache also convert it
-    static constexpr int kLoaders = KV8 && RT <= 64 ? 128 : 64;
+    static constexpr int kConverters = KV8 ? 128 : 0;     // converting threads
     static constexpr int kGroups = RT > 32 ? RT / 32 : 1;  // softmax warpgroups
     static constexpr int kRows = RT / kGroups;            // rows per warpgroup
     static constexpr int kN = RT < 16 ? 16 : RT;          // columns of the products, the least there is
     static constexpr int kSoft = 128 * kGroups;           // softmax threads
-    static constexpr int kThreads = kSoft + 64 + kLoaders;
+    static constexpr int kThreads = kSoft + 64 + kLoaders + kConverters;
     // Two CTAs per SM where they fit: one's sums and segment changes hide behind
     // the other's loads (128 decode rows 76 us
     // with one, 67 with two).
@@ -104,7 +103,7 @@ template <int RT, bool KV8> struct Shape {
     static constexpr uint32_t kOffQ = kOffRaw + kRaw * (kStage / 2);
     static constexpr uint32_t kOffP = kOffQ + kQ * kQBytes;
     static constexpr uint32_t kOffTab = kOffP + kPBytes;            // cp.async: row offsets of 2 tiles
-    static constexpr uint32_t kOffSee = kOffTab + (KV8 ? 0u : 2u * kTok * 8u);   // who sees each node, two trees
+    static constexpr uint32_t kOffSee = kOffTab + 2u * kTok * 8u;   // who sees each node, two trees
     static constexpr uint32_t kOffRow = kOffSee + 2u * SGMV_TREE_MAX_NODES * kWords * 4u;  // rows' places
     static constexpr uint32_t kBytes = kOffRow + kSegs * RT * 8u + 1024u;  // + alignment
 };
@@ -344,21 +343,24 @@ template <typename T> __device__ __forceinline__ bool bad16(uint32_t h) {
     return (h & e) == e;
 }
 
-// 16 e4m3 values as 16-bit ones (no rounding; NaN stays NaN): the first eight, the others.
+// Four e4m3 values as 16-bit ones, exactly.  f16: the conversion instruction (its pipe takes
+// a quarter of the lanes in a cycle, but all of a tile's conversions hide behind the
+// rest: 32 trees over 4096 tokens 151 us, 148 with none at all, 200 with the integer form).
+// bf16 has no such instruction: sign, exponent and mantissa are put in their
+// places, and a product, which is exact, makes up for the other bias, subnormal values
+// too.  That takes NaN (all ones but for the sign) for 480: put_nan.
 template <typename T> __device__ __forceinline__ void widen4(uint32_t u, uint32_t &a, uint32_t &b) {
-    uint32_t x, y;
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}\n"
-        : "=r"(x), "=r"(y)
-        : "r"(u));
     if constexpr (std::is_same<T, __half>::value) {
-        a = x;
-        b = y;
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}\n"
+            : "=r"(a), "=r"(b)
+            : "r"(u));
     } else {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x));
-        const float2 g = __half22float2(*reinterpret_cast<const __half2 *>(&y));
-        a = pack2<T>(f.x, f.y);
-        b = pack2<T>(g.x, g.y);
+        const uint32_t x = __byte_perm(u, 0, 0x1404), y = __byte_perm(u, 0, 0x3424);  // to the upper bytes
+        a = (x & 0x80008000u) | (x & 0x7fff7fffu) >> 4;
+        b = (y & 0x80008000u) | (y & 0x7fff7fffu) >> 4;
+        asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(0x7B807B80u));  // 2^120
+        asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(b) : "r"(0x7B807B80u));
     }
 }
 template <typename T> __device__ __forceinline__ void widen16(const uint4 &v, uint4 &lo, uint4 &hi) {
@@ -366,6 +368,17 @@ template <typename T> __device__ __forceinline__ void widen16(const uint4 &v, ui
     widen4<T>(v.y, lo.z, lo.w);
     widen4<T>(v.z, hi.x, hi.y);
     widen4<T>(v.w, hi.z, hi.w);
+}
+__device__ __forceinline__ uint32_t e4m3_nan(uint32_t u) {  // the bytes that are no numbers: their top bits
+    return ((u & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+__device__ __forceinline__ uint32_t e4m3_nan(const uint4 &v) {
+    return e4m3_nan(v.x) | e4m3_nan(v.y) | e4m3_nan(v.z) | e4m3_nan(v.w);
+}
+__device__ __forceinline__ void put_nan(uint32_t u, uint32_t &a, uint32_t &b) {
+    const uint32_t n = e4m3_nan(u);
+    a |= ((n >> 7 & 1u) | (n >> 15 & 1u) << 16) * 0x7fffu;
+    b |= ((n >> 23 & 1u) | (n >> 31) << 16) * 0x7fffu;
 }
 
 // Row r of an item's row tile: its token (~token for a padding row) and query head.
@@ -384,15 +397,14 @@ template <typename T, int RT, bool KV8>
 __global__ void __launch_bounds__(Shape<RT, KV8>::kThreads, Shape<RT, KV8>::kPerSm)
     sgmv_tree_mma_kernel(const __grid_constant__ MmaParams P) {
     using S = Shape<RT, KV8>;
-    constexpr int kLoaders = S::kLoaders;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     const sgmv_tree_attention_args &a = P.a;
-    extern __shared__ __align__(1024) uint8_t dsm[];
+    extern __shared__ __align__(128) uint8_t dsm[];
     __shared__ __align__(8) uint64_t full[S::kStages], empty[S::kStages], q_full[S::kQ], q_empty[S::kQ];
     __shared__ __align__(8) uint64_t seg_full[kSegs], seg_empty[kSegs], aux_full[kSegs];
     __shared__ __align__(8) uint64_t p_full, pv_done, tab_ready, drained;
-    // e4m3: what has come of a loading warp's part of a stage; the scores of even and odd tiles
-    __shared__ __align__(8) uint64_t raw_full[4][4], s_done[2];
+    // e4m3: the ring of values as they come; the scores of even and odd tiles
+    __shared__ __align__(8) uint64_t raw_full[S::kRaw + 1], raw_empty[S::kRaw + 1], s_done[2];
     __shared__ uint32_t s_tmem;
     __shared__ int s_lost, s_poison, s_longest, s_known;
     __shared__ int64_t s_sum[32];
@@ -408,15 +420,18 @@ __global__ void __launch_bounds__(Shape<RT, KV8>::kThreads, Shape<RT, KV8>::kPer
     if (warp == kMmaWarp) {
         if (lane == 0) {
             for (int i = 0; i < S::kStages; ++i)
-                mbar_init(&full[i], KV8 || P.box ? kLoaders / 32 : kLoaders), mbar_init(&empty[i], 1);
+                mbar_init(&full[i], KV8 ? S::kConverters / 32 : P.box ? kLoaders / 32 : kLoaders), mbar_init(&empty[i], 1);
             for (int i = 0; i < S::kQ; ++i) mbar_init(&q_full[i], P.q_box ? 1 : 32), mbar_init(&q_empty[i], 1);
             for (int i = 0; i < kSegs; ++i) {
                 mbar_init(&seg_full[i], 1);
-                mbar_init(&seg_empty[i], 2 + kLoaders / 32);  // MMA, softmax, loaders
+                mbar_init(&seg_empty[i], 2 + (kLoaders + S::kConverters) / 32);  // MMA, softmax, loaders, converters
                 mbar_init(&aux_full[i], 1);
             }
             if (KV8) {
-                for (int i = 0; i < 16; ++i) mbar_init(&raw_full[i / 4][i % 4], P.box ? 1 : 32);
+                for (int i = 0; i < S::kRaw; ++i) {
+                    mbar_init(&raw_full[i], P.box ? kLoaders / 32 : kLoaders);
+                    mbar_init(&raw_empty[i], S::kConverters / 32);
+                }
                 mbar_init(&s_done[0], 1), mbar_init(&s_done[1], 1);
             }
             mbar_init(&p_full, S::kSoft / 32);
@@ -434,8 +449,8 @@ __global__ void __launch_bounds__(Shape<RT, KV8>::kThreads, Shape<RT, KV8>::kPer
     for (int i = tid; i < RT; i += S::kThreads) s_ref[i] = -kUnset;
     // columns past D that the products read are zero: in Q, and in K where TMA
     // does not fill them; so are the rows past a short tile
-    if (KV8 ? a.D % 64 != 0 : P.tok < kTok)
-        for (uint32_t i = tid * 16u; i < S::kStages * kStage; i += S::kThreads * 16u)
+    if (KV8 ? P.tok < kTok || a.D % 64 != 0 : P.tok < kTok)
+        for (uint32_t i = tid * 16u; i < S::kOffQ; i += S::kThreads * 16u)
             sts128(sm + i, make_uint4(0, 0, 0, 0));
     if (a.D % 64 != 0 && !(P.box && P.q_box))
         for (uint32_t i = (KV8 || P.box ? S::kOffQ : 0u) + tid * 16u; i < S::kOffP; i += S::kThreads * 16u)
@@ -496,7 +511,7 @@ __global__ void __launch_bounds__(Shape<RT, KV8>::kThreads, Shape<RT, KV8>::kPer
     }
     volatile int *const lost = &s_lost;
     const int D = a.D, group = P.group;
-    const int cpr = D / 8;  // 16-byte chunks per row
+    const int cpr = D / 8;  // 16-byte chunks per row of 16-bit values
     // a role's next segment, number i, is in s_seg[i % kSegs]
     auto segment_there = [&](int i) { return await(&seg_full[i % kSegs], (uint32_t)(i / kSegs) & 1, lost); };
     // A role takes an injected timeout as it would one of its waits.
@@ -655,176 +670,106 @@ __global__ void __launch_bounds__(Shape<RT, KV8>::kThreads, Shape<RT, KV8>::kPer
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if (warp > kWalkWarp) {
-        // ---- K and V: ring order K0, V0, K1, V1, ... ------------------------------
-        const int lt = tid - S::kSoft - 64, halves = D > 64 ? 2 : 1;
-        int st = 0;
-        uint32_t ph = 1;  // parity of the stage's release that is waited for
-        auto claim_stage = [&]() {
-            if (issued >= S::kStages && !await(&empty[st], ph, lost)) return false;
-            ++issued;
-            return true;
-        };
-        auto advance = [&]() {
-            if (++st == S::kStages) st = 0, ph ^= 1;
-        };
+    } else if (warp > kWalkWarp + kLoaders / 32) {
+        // ---- an e4m3 cache's values made 16-bit ones ------------------------------
         if constexpr (KV8) {
-            // Each warp has kOwn tokens of every tile: it requests them (operands K0, V0, K1,
-            // ..., up to kRaw of them ahead) and turns them into 16-bit values when they
-            // have come and their stage is free.  Rows lie D bytes apart as they come.
-            constexpr int kOwn = kTok / (kLoaders / 32), kChunks = 8;  // 16-byte chunks per lane and 32 rows
-            static_assert(S::kRaw <= 4 && kLoaders / 32 <= 4, "barriers");
-            const int w = lt >> 5, pieces = D / 16;
-            uint8_t *const raw = sm + S::kOffRaw + w * kOwn * D;
-            uint64_t *const come = raw_full[w];
-            // where a lane's chunks go (the first 32 rows).  The second half's go in the
-            // other order, so that eight lanes write to eight different groups of banks.
+            const int cw = warp - kWalkWarp - kLoaders / 32 - 1, pieces = D / 16;
+            constexpr int kChunks = 8;  // 16-byte chunks per lane and operand, at most
+            // a warp has 32 tokens of every tile, which lie D bytes apart; where a lane's
+            // chunks go: the second half's in the other order, so that eight lanes write
+            // to eight different groups of banks
+            const uint32_t from = S::kOffRaw + (uint32_t)(cw * 32 * pieces + lane) * 16u;
             uint32_t to[kChunks];
 #pragma unroll
             for (int i = 0; i < kChunks; ++i) {
                 const int e = lane + 32 * i, m = e / pieces, c = e - m * pieces, odd = c >> 2;
-                to[i] = (uint32_t)odd * kHalf + sw128_offset(w * kOwn + m, (2 * c + odd) & 7);
+                to[i] = (uint32_t)odd * kHalf + sw128_offset(cw * 32 + m, (2 * c + odd) & 7);
             }
-            // The tile whose place is known, and this lane's part of it: the page and row of
-            // its box, or its tokens' offsets from the cache's start (-1: none).
-            const int boxes = P.box ? kOwn / P.box : 0;
-            Segment s;
-            s.end = 0;
-            int seg = -1, tile = 0, page = 0, row = -1;
-            int64_t place[kOwn / 32];
-            bool known = false, over = false;
-            auto look = [&]() {
-                if (P.box) {
-                    const int j = tile * kTok + w * kOwn + lane * P.box;
-                    row = -1;
-                    if (lane < boxes && j < s.total) {
-                        const int pg = j / a.block_size;
-                        row = j - pg * a.block_size;
-                        page = a.block_table[s.b * a.table_row + pg];
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < kOwn / 32; ++i) {
-                        const int j = tile * kTok + w * kOwn + i * 32 + lane;
-                        place[i] = -1;
-                        if (j >= s.total) continue;
-                        const int pg = j / a.block_size;
-                        const int32_t block = a.block_table[s.b * a.table_row + pg];
-                        if (block >= 0 && block < a.num_blocks)
-                            place[i] = (int64_t)block * a.cache_block + (int64_t)(j - pg * a.block_size) * a.cache_token;
-                        else
-                            set_error(P.err, kErrBadIndex);
-                    }
-                }
-            };
-            // The next tile; waits for its segment only if told to, for what that one waits
-            // for may be held up by tiles that are still here.
-            auto next_tile = [&](bool wait) {
-                if (known || over) return;
-                if (tile + 1 < s.end) {
-                    ++tile;
-                } else {
-                    if (!wait && __shfl_sync(0xffffffffu, *(volatile int *)&s_known, 0) <= seg + 1) return;
-                    over = !segment_there(seg + 1);
-                    if (over) return;
-                    s = s_seg[++seg % kSegs];
-                    tile = s.tile;
-                    over = s.end == 0;
-                    if (over) return;
-                }
-                known = true;
-                look();
-            };
-            auto request = [&](const void *cache, const CUtensorMap *map, int slot) {
-                uint8_t *const dst = raw + slot * (int)(kStage / 2);
-                if (P.box) {
-                    // boxes past the end, and pages out of range, read as zeros
-                    int32_t pg = page;
-                    int r = row;
-                    if (r < 0 || pg < 0 || pg >= a.num_blocks) {
-                        if (r >= 0) set_error(P.err, kErrBadIndex);
-                        pg = a.num_blocks;
-                        r = 0;
-                    }
-                    if (lane == 0) mbar_arrive_expect_tx(&come[slot], (uint32_t)(kOwn * D));
-                    __syncwarp();
-                    if (lane < boxes) tma_load_4d(dst + lane * P.box * D, map, 0, r, s.h, pg, &come[slot]);
-                } else {
-                    const uint8_t *const from = static_cast<const uint8_t *>(cache) + (int64_t)s.h * a.cache_head;
-                    for (int i = 0; i < kOwn / 32 * pieces; ++i) {
-                        const int e = lane + 32 * i, m = e / pieces;
-                        int64_t off = __shfl_sync(0xffffffffu, place[0], m & 31);
-                        if (kOwn > 32) {
-                            const int64_t other = __shfl_sync(0xffffffffu, place[kOwn / 32 - 1], m & 31);
-                            if (m >= 32) off = other;
-                        }
-                        cp_async16(dst + e * 16, off >= 0 ? from + off + (e - m * pieces) * 16 : from, off >= 0 ? 16u : 0u);
-                    }
-                    cp_async_arrive(&come[slot]);
-                }
-            };
-            int asked = 0, done = 0;    // operands requested and converted
-            int ends[3] = {-1, -1, -1}; // the segments that tiles asked / 2 % 3 are the ends of, or -1
-            bool stop = injected(2);
-            while (!stop) {
-                // (K and V of a tile one after the other, from the same place)
-                while (asked < done + S::kRaw && !over) {
-                    if ((asked & 1) == 0) {
-                        next_tile(asked == done);
-                        if (!known) break;
-                        const int end = tile + 1 == s.end ? seg : -1, at = asked / 2 % 3;
-                        ends[0] = at == 0 ? end : ends[0];
-                        ends[1] = at == 1 ? end : ends[1];
-                        ends[2] = at == 2 ? end : ends[2];
-                        request(a.k_cache, &P.map_k, asked % S::kRaw);
-                    } else {
-                        request(a.v_cache, &P.map_v, asked % S::kRaw);
-                        known = false;
-                        next_tile(false);  // its place is looked up meanwhile
-                    }
-                    ++asked;
-                }
-                if (asked == done) break;
-                const int slot = done % S::kRaw;
-                if (!await(&come[slot], (uint32_t)(done / S::kRaw) & 1, lost) || !claim_stage()) break;
-                const uint8_t *const src = raw + slot * (int)(kStage / 2);
-                uint8_t *const dst = sm + (uint32_t)st * kStage;
-#pragma unroll
-                for (int sub = 0; sub < kOwn / 32; ++sub) {
-                    uint4 v[kChunks];
-#pragma unroll
-                    for (int i = 0; i < kChunks; ++i)
-                        if (i < pieces) v[i] = lds128(src + (sub * 32 * pieces + lane + 32 * i) * 16);
-#pragma unroll
-                    for (int i = 0; i < kChunks; ++i)
-                        if (i < pieces) {
-                            uint4 lo, hi;
-                            widen16<T>(v[i], lo, hi);
-                            const bool odd = to[i] >= kHalf;
-                            sts128(dst + sub * 4096 + to[i], odd ? hi : lo);
-                            sts128(dst + sub * 4096 + (to[i] ^ 16u), odd ? lo : hi);
-                        }
-                }
-                fence_proxy_async();
+            int n = 0, st = 0, slot = 0;
+            uint32_t ph = 1, raw_ph = 0;
+            for (int i = 0, stop = 0; !stop; ++i) {
+                if (!segment_there(i)) break;
+                const int tile = s_seg[i % kSegs].tile, end = s_seg[i % kSegs].end;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&full[st]);
-                advance();
-                if (++done % 2 == 0) {
-                    const int at = (done / 2 - 1) % 3, end = at == 0 ? ends[0] : at == 1 ? ends[1] : ends[2];
-                    if (end >= 0 && lane == 0) mbar_arrive(&seg_empty[end % kSegs]);
+                if (end == 0) break;
+                if (lane == 0) mbar_arrive(&seg_empty[i % kSegs]);
+                for (int left = 2 * (end - tile); left > 0; --left, ++n) {
+                    if (!await(&raw_full[slot], raw_ph, lost) || (n >= S::kStages && !await(&empty[st], ph, lost))) {
+                        stop = 1;
+                        break;
+                    }
+                    const uint8_t *const src = sm + from + (uint32_t)slot * (kStage / 2);
+                    uint8_t *const dst = sm + (uint32_t)st * kStage;
+                    uint4 v[kChunks];
+                    uint32_t nan = 0;
+#pragma unroll
+                    for (int e = 0; e < kChunks; ++e)
+                        if (e < pieces) v[e] = lds128(src + e * 512);
+#pragma unroll
+                    for (int e = 0; e < kChunks; ++e)
+                        if (e < pieces) {
+                            uint4 lo, hi;
+                            widen16<T>(v[e], lo, hi);
+                            if (!std::is_same<T, __half>::value) nan |= e4m3_nan(v[e]);
+                            const bool odd = to[e] >= kHalf;
+                            sts128(dst + to[e], odd ? hi : lo);
+                            sts128(dst + (to[e] ^ 16u), odd ? lo : hi);
+                        }
+                    // (once per operand: a branch per chunk cost 64 heads over 32768
+                    // tokens 150 of 580 us)
+                    if (nan) {
+#pragma unroll 1
+                        for (int e = 0; e < pieces; ++e) {
+                            const uint4 u = lds128(src + e * 512);
+                            if (!e4m3_nan(u)) continue;
+                            uint4 lo, hi;
+                            widen16<T>(u, lo, hi);
+                            put_nan(u.x, lo.x, lo.y);
+                            put_nan(u.y, lo.z, lo.w);
+                            put_nan(u.z, hi.x, hi.y);
+                            put_nan(u.w, hi.z, hi.w);
+                            const int k = lane + 32 * e, m = k / pieces, c = k - m * pieces;
+                            uint8_t *const half = dst + (uint32_t)(c >> 2) * kHalf;
+                            sts128(half + sw128_offset(cw * 32 + m, (2 * c) & 7), lo);
+                            sts128(half + sw128_offset(cw * 32 + m, (2 * c + 1) & 7), hi);
+                        }
+                    }
+                    fence_proxy_async();
                     __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&raw_empty[slot]);
+                        mbar_arrive(&full[st]);
+                    }
+                    if (++slot == S::kRaw) slot = 0, raw_ph ^= 1;
+                    if (++st == S::kStages) st = 0, ph ^= 1;
                 }
             }
-            // what is still on its way lands while this shared memory is the CTA's
-            for (; done < asked; ++done)
-                if (!mbar_wait(&come[done % S::kRaw], (uint32_t)(done / S::kRaw) & 1)) break;
-        } else if (P.box) {
+        }
+    } else if (warp > kWalkWarp) {
+        // ---- K and V: ring order K0, V0, K1, V1, ... ------------------------------
+        const int lt = tid - S::kSoft - 64, halves = !KV8 && D > 64 ? 2 : 1;
+        constexpr int kRing = KV8 ? S::kRaw : S::kStages;
+        constexpr uint32_t kSlot = KV8 ? kStage / 2 : kStage;
+        uint8_t *const ring = sm + (KV8 ? S::kOffRaw : 0u);
+        uint64_t *const come = KV8 ? raw_full : full, *const gone = KV8 ? raw_empty : empty;
+        int st = 0;
+        uint32_t ph = 1;  // parity of the stage's release that is waited for
+        auto claim_stage = [&]() {
+            if (issued >= kRing && !await(&gone[st], ph, lost)) return false;
+            ++issued;
+            return true;
+        };
+        auto advance = [&]() {
+            if (++st == kRing) st = 0, ph ^= 1;
+        };
+        if (P.box) {
             // TMA: a box (tokens x 64 columns) per lane, dealt to the two warps
             const int box = P.box, nbox = P.tok / box, op = lane * (kLoaders / 32) + lt / 32;
             const int mine = op % nbox, half = op / nbox;
             const bool busy = half < halves;
-            const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, busy)) * (uint32_t)box * 128u;
-            const uint32_t at = (uint32_t)half * kHalf + (uint32_t)(mine * box) * 128u;
+            const uint32_t wide = KV8 ? (uint32_t)D : 128u;  // bytes of a box's row
+            const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, busy)) * (uint32_t)box * wide;
+            const uint32_t at = (uint32_t)half * kHalf + (uint32_t)(mine * box) * wide;
             int32_t page = 0;
             int in = -1;
             // page and place of this lane's box of a tile
@@ -839,9 +784,9 @@ __global__ void __launch_bounds__(Shape<RT, KV8>::kThreads, Shape<RT, KV8>::kPer
             };
             auto copy_boxes = [&](const CUtensorMap *map, int32_t pg, int row, int head) {
                 if (!claim_stage()) return false;
-                if (lane == 0) mbar_arrive_expect_tx(&full[st], bytes);
+                if (lane == 0) mbar_arrive_expect_tx(&come[st], bytes);
                 __syncwarp();
-                if (busy) tma_load_4d(sm + (uint32_t)st * kStage + at, map, half * 64, row, head, pg, &full[st]);
+                if (busy) tma_load_4d(ring + (uint32_t)st * kSlot + at, map, half * 64, row, head, pg, &come[st]);
                 advance();
                 return true;
             };
@@ -878,16 +823,18 @@ __global__ void __launch_bounds__(Shape<RT, KV8>::kThreads, Shape<RT, KV8>::kPer
             }
         } else {
             int64_t *const tab = reinterpret_cast<int64_t *>(sm + S::kOffTab);
-            const int dm = kLoaders / cpr, dc = kLoaders - dm * cpr;
+            using Cache = std::conditional_t<KV8, uint8_t, T>;
+            constexpr int kElems = 16 / (int)sizeof(Cache);
+            const int per = D / kElems, dm = kLoaders / per, dc = kLoaders - dm * per;  // 16-byte chunks per row
             constexpr int kBatch = 8;
             int g = 0;
             auto copy_tile = [&](const void *cache, int64_t off) {
                 if (!claim_stage()) return false;
-                const T *const from = static_cast<const T *>(cache) + off;
+                const Cache *const from = static_cast<const Cache *>(cache) + off;
                 const int64_t *const rows = tab + (g & 1) * kTok;
-                uint8_t *const dst = sm + (uint32_t)st * kStage;
+                uint8_t *const dst = ring + (uint32_t)st * kSlot;
                 // eight copies' row offsets are read before the first is used
-                int m = lt / cpr, c = lt - m * cpr;
+                int m = lt / per, c = lt - m * per;
                 while (m < kTok) {
                     int64_t o[kBatch];
                     uint32_t to[kBatch];
@@ -897,19 +844,19 @@ __global__ void __launch_bounds__(Shape<RT, KV8>::kThreads, Shape<RT, KV8>::kPer
                         o[i] = -2;
                         if (m < kTok) {
                             o[i] = rows[m];
-                            to[i] = (uint32_t)(c >> 3) * kHalf + sw128_offset(m, c & 7);
-                            cc[i] = c * 8;
+                            to[i] = KV8 ? (uint32_t)(m * per + c) * 16u : (uint32_t)(c >> 3) * kHalf + sw128_offset(m, c & 7);
+                            cc[i] = c * kElems;
                         }
                         m += dm;
                         c += dc;
-                        if (c >= cpr) c -= cpr, ++m;
+                        if (c >= per) c -= per, ++m;
                     }
 #pragma unroll
                     for (int i = 0; i < kBatch; ++i)
                         if (o[i] != -2)
                             cp_async16(dst + to[i], o[i] >= 0 ? from + o[i] + cc[i] : from, o[i] >= 0 ? 16u : 0u);
                 }
-                cp_async_arrive(&full[st]);
+                cp_async_arrive(&come[st]);
                 advance();
                 return true;
             };
@@ -1320,9 +1267,10 @@ __global__ void __launch_bounds__(Shape<RT, KV8>::kThreads, Shape<RT, KV8>::kPer
         if (P.q_box && warp == kWalkWarp)
             for (int i = max(0, issued - S::kQ); i < issued; ++i)
                 if (!mbar_wait(&q_full[i % S::kQ], (uint32_t)(i / S::kQ) & 1)) break;
-        if (!KV8 && P.box && warp > kWalkWarp)
-            for (int i = max(0, issued - S::kStages); i < issued; ++i)
-                if (!mbar_wait(&full[i % S::kStages], (uint32_t)(i / S::kStages) & 1)) break;
+        constexpr int kRing = KV8 ? S::kRaw : S::kStages;
+        if (P.box && warp > kWalkWarp && warp <= kWalkWarp + kLoaders / 32)
+            for (int i = max(0, issued - kRing); i < issued; ++i)
+                if (!mbar_wait(KV8 ? &raw_full[i % kRing] : &full[i % kRing], (uint32_t)(i / kRing) & 1)) break;
     }
 }
 
@@ -1433,6 +1381,39 @@ constexpr size_t kHeadBytes = 256;
 
 // CTAs, and so shares, at most.
 int max_ctas(int rt) { return kMaxSms * (rt <= 16 ? Shape<16, false>::kPerSm : 1); }
+
+// The caches' tensor maps: values of `bytes` bytes, in rows of `columns` 16-bit elements,
+// of which a box has box_columns.  No boxes where pages or strides do not allow them.
+// Boxes are as high as pages allow, for TMA's cost here is per box: at pages of
+// 24 tokens, boxes of 8 filling every tile took 115 us, boxes of 24 and tiles of
+// 120 tokens 109 us (128 sequences of up to 2100 tokens, 4 heads of 80).
+inline void map_cache(MmaParams &p, bool bf16, int columns, int box_columns, int bytes, bool swizzle) {
+    const sgmv_tree_attention_args &a = p.a;
+    p.tok = tree_tile(a.block_size);
+    p.box = p.tok < kTok ? a.block_size : std::gcd(a.block_size, kTok);
+    if (p.box < 8) {
+        p.box = 0;
+        return;
+    }
+    const cuuint64_t dims[4] = {(cuuint64_t)columns, (cuuint64_t)a.block_size, (cuuint64_t)a.Hkv,
+                                (cuuint64_t)a.num_blocks};
+    const cuuint64_t strides[3] = {(cuuint64_t)a.cache_token * bytes, (cuuint64_t)a.cache_head * bytes,
+                                   (cuuint64_t)a.cache_block * bytes};
+    const cuuint32_t box[4] = {(cuuint32_t)box_columns, (cuuint32_t)p.box, 1, 1};
+    // What L2 fetches around a row of a box is this head's only if the rows of
+    // a head are contiguous or as wide; else it is another CTA's (32 x 4 rows over up
+    // to 4096 tokens, 32 heads side by side: of 64 columns 142 us with 256 bytes,
+    // 122 with 128; of 96 columns 220 with 256, 167 with 64)
+    const int row = a.D * bytes;
+    const CUtensorMapL2promotion fetch =
+        a.cache_token == a.D || row % 256 == 0 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+        : row % 128 == 0                       ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+        : row % 64 == 0                        ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B
+                                               : CU_TENSOR_MAP_L2_PROMOTION_NONE;
+    if (!tmap_encode(&p.map_k, bf16, 4, a.k_cache, dims, strides, box, swizzle, fetch) ||
+        !tmap_encode(&p.map_v, bf16, 4, a.v_cache, dims, strides, box, swizzle, fetch))
+        p.box = 0, p.tok = kTok;  // strides that a tensor map cannot hold
+}
 
 // Parameters that both kinds of cache share; the row tile and its CTAs.
 inline MmaParams plan_launch(const sgmv_tree_attention_args &a, int nsm, int *err, int *rt, int *ctas) {
