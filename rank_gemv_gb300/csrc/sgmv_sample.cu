@@ -9,11 +9,13 @@
 // A cluster of CTAs has a row, each warp one contiguous range of it, staged in
 // shared memory as fp32 once; everything else happens on chip.  The filters keep
 // the first tokens in order of (logit, index), and what cuts there is found without a
-// sort: a histogram of 2048 bins over the logits counts the tokens; the bin where the
-// k-th falls, or the bins where the running weight can pass p of the total (the
-// weights at a bin's edges bound it from both sides), are looked at again, finer,
-// until few tokens are left, which are ranked one against all, or one value, whose
-// tokens are counted off by index.  Sums above the cut are exact at every step.
+// sort.  A histogram over the logits counts the tokens; top-k bounds the bins that can
+// matter, or top-p does (the weights at a bin's edges bound the running weight from both
+// sides).  If they hold few tokens, as they mostly do, one CTA collects them, ranks them
+// one against all and draws.  If not, each thread notes which of its tokens they are,
+// and only those are looked at again: the bins around the cut are divided finer, until
+// few tokens are left, or one value, whose tokens are counted off by index; the sums
+// above the cut are exact at every step.
 #include <algorithm>
 
 #include "sgmv_device.cuh"
@@ -25,11 +27,13 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kBins = 4 * kThreads;
+constexpr int kBins = 2 * kThreads;
 constexpr int kFew = 256;               // tokens that are ranked one against all
+constexpr int kLong = 512;              // entries of a warp's range from which on its threads' largest are counted
+constexpr float kDeep = 18.f;            // octaves below the largest weight from which on fp32 is exact enough
 constexpr float kOctaves = 39.f;        // weights below 2^-39 of the largest are zero
 constexpr float kSlack = 3e-5f;         // rounding of the weights at bins' edges and of their sums
-constexpr int64_t kOne = 1ll << 38, kUnit = 1ll << 24;
+constexpr int64_t kUnit = 1ll << 24;
 
 // 2^38 2^(j / 128), j = -64 ... 64
 __device__ const int64_t kExp2[129] = {
@@ -58,26 +62,28 @@ __device__ const int64_t kExp2[129] = {
 };
 
 struct SampleShared {
-    uint32_t hist[kBins];
+    __align__(16) uint32_t hist[kBins];
+    __align__(16) uint4 list[kFew];         // logit, token, weight
     int64_t exp2[129];
-    int64_t part[2][3][kWarps], mine[2][3];
+    int64_t part[2][4][kWarps];         // a sum of every warp,
+    int64_t every[2][4][kMaxCluster];   // and of every CTA
     int64_t scan[kWarps];
     float scan_lo[kWarps], scan_hi[kWarps];
     uint32_t scan_n[kWarps];
-    float list_l[kFew];
-    int32_t list_v[kFew];
-    int64_t list_w[kFew];
     uint32_t listed;
     int bin0, bin1;
     uint32_t rank, count;
     float cut_l;
     int32_t cut_v, found;
 };
+static_assert(kFew * 16 >= kWarps * 64 * 4, "the warps' queues in the list");
+static_assert(2 * (sizeof(SampleShared) + 1024 + 100 * 1024) <= 228 * 1024, "two CTAs per SM");
 
 struct SampleParams {
     sgmv_sample_args a;
     int32_t share;   // entries of a warp's range
     int32_t staged;  // the ranges are in shared memory
+    int32_t noted;   // a thread's entries of a range have a bit each
 };
 
 // One zero; finite logits and +inf within +-2^126, so that differences are finite; NaN as -inf.
@@ -95,11 +101,21 @@ struct Weigh {
 
     // fp32 exponent, never above zero, descending with l
     __device__ __forceinline__ float rough(float l) const { return (l - m) * ch; }
+    // 38 above the exponent; of one below -kDeep the weight, which is less than 2^20,
+    // so that its rounding is a unit or so
+    __device__ __forceinline__ float raised(float l) const { return fmaf(l - m, ch, 38.f); }
+    static __device__ __forceinline__ uint32_t deep(float raised) {
+        float w;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(raised));
+        return __float2uint_rz(w);
+    }
     __device__ __forceinline__ int64_t operator()(float l) const {
         // l - m = d + e exactly; times log2(e) / temperature: p + q
-        const float d = l - m, b = d - l, e = (l - (d - b)) + (-m - b);
+        const float d = l - m;
+        const float up = fmaf(d, ch, 38.f);
+        if (!(up >= 38.f - kDeep)) return deep(up);
+        const float b = d - l, e = (l - (d - b)) + (-m - b);
         const float p = d * ch;
-        if (!(p > -kOctaves)) return 0;
         const float q = fmaf(d, ch, -p) + fmaf(d, cl, e * ch);
         // p = n + j / 128 + g; the magic sums leave whole numbers in the low bits
         const float nm = p + 12582912.f, f = p - (nm - 12582912.f);
@@ -147,8 +163,26 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
     auto get1 = [&](int w, int i) {
         return P.staged ? ldsf(staged + w * share + i) : read1((rank * kWarps + w) * share + i);
     };
-    // every entry of this warp, f(logit, token)
+    // the entries of this thread that a pass looks at: all of them, or those noted (bit 4 j + e:
+    // entry 128 j + 4 lane + e of the warp's range); inside: those that the last span() counted
+    uint64_t noted = 0, inside = 0;
+    bool by_note = false;
+    uint64_t at_bit = 0;  // of the entry that f is given
+    // f(logit, token) of them
     auto each = [&](auto f) {
+        if (by_note) {
+            // (the warp's lanes together: left to themselves they drift apart at f's
+            // branches and run one by one, which took four times as long)
+            for (uint64_t left = noted; __any_sync(0xffffffffu, left != 0); left &= left - 1) {
+                if (left) {
+                    const int k = __ffsll((long long)left) - 1, i = (k >> 2) * 128 + lane * 4 + (k & 3);
+                    at_bit = left & -left;
+                    f(ldsf(mine + i), u0 + i - skew);
+                }
+                __syncwarp();
+            }
+            return;
+        }
         for (int i = lane * 4; i < share; i += 128) {
             const float4 x = get4(i);
             const int v = u0 + i - skew;
@@ -162,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
     // ---- the cluster's sums ----------------------------------------------------
     int turn = 0;
     // Joins N values of all threads by op(n, x, y); everyone gets the result.  The warps'
-    // values stay in part[], the CTAs' in mine[], of the turn before.
+    // values stay in part[], the CTAs' in every[], of the turn before.
     auto join = [&](auto &v, auto op) {
         constexpr int N = sizeof(v) / sizeof(v[0]);
         const int at = turn;
@@ -173,24 +207,21 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
             if (lane == 0) s.part[at][n][warp] = v[n];
         }
         __syncthreads();
+        if (warp < N) {  // warp n joins value n and hands it to every CTA
+            int64_t x = s.part[at][warp][lane % kWarps];
+            for (int o = kWarps / 2; o > 0; o >>= 1) x = op(warp, x, (int64_t)__shfl_xor_sync(0xffffffffu, x, o));
+            if (lane < cl)
+                asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(
+                                 peer_addr(&s.every[at][warp][rank], (uint32_t)lane)),
+                             "l"(x)
+                             : "memory");
+        }
+        if (cl > 1) cluster_sync();
+        else __syncthreads();
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-            v[n] = s.part[at][n][0];
-            for (int w = 1; w < kWarps; ++w) v[n] = op(n, v[n], s.part[at][n][w]);
-            if (tid == 0) s.mine[at][n] = v[n];
-        }
-        if (cl > 1) {
-            cluster_sync();
-#pragma unroll
-            for (int n = 0; n < N; ++n)
-                for (int r = 0; r < cl; ++r) {
-                    uint64_t x;
-                    asm volatile("ld.shared::cluster.u64 %0, [%1];"
-                                 : "=l"(x)
-                                 : "r"(peer_addr(&s.mine[at][n], (uint32_t)r))
-                                 : "memory");
-                    v[n] = r == 0 ? (int64_t)x : op(n, v[n], (int64_t)x);
-                }
+            v[n] = s.every[at][n][0];
+            for (int r = 1; r < cl; ++r) v[n] = op(n, v[n], s.every[at][n][r]);
         }
     };
     auto plus = [](int, int64_t x, int64_t y) { return x + y; };
@@ -198,44 +229,34 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
     // f's sums alone (found: it, in every CTA).
     auto locate = [&](auto f, int64_t mark) {
         const int at = turn ^ 1;
-        int64_t before = 0, all = 0;
-        if (cl > 1) {
-            for (int r = 0; r <= rank; ++r) {
-                uint64_t x;
-                asm volatile("ld.shared::cluster.u64 %0, [%1];"
-                             : "=l"(x)
-                             : "r"(peer_addr(&s.mine[at][0], (uint32_t)r))
-                             : "memory");
-                if (r < rank) before += (int64_t)x;
-                else all = (int64_t)x;
-            }
-        } else {
-            for (int w = 0; w < kWarps; ++w) all += s.part[at][0][w];
-        }
+        int64_t before = 0;
+        const int64_t all = s.every[at][0][rank];
+        for (int r = 0; r < rank; ++r) before += s.every[at][0][r];
         if (before <= mark && mark < before + all) {  // it is this CTA's
             int w = 0;
             while (w < kWarps - 1 && mark >= before + s.part[at][0][w]) before += s.part[at][0][w++];
-            for (int i0 = 0; i0 < share; i0 += kThreads) {
-                const int i = i0 + tid, v = (rank * kWarps + w) * share + i - skew;
-                int64_t run = i < share ? f(get1(w, i), v) : 0;
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int64_t up = __shfl_up_sync(0xffffffffu, run, o);
-                    if (lane >= o) run += up;
-                }
-                if (lane == 31) s.scan[warp] = run;
-                __syncthreads();
-                int64_t here = before, sum = 0;
-                for (int e = 0; e < kWarps; ++e) {
-                    if (e < warp) here += s.scan[e];
-                    sum += s.scan[e];
-                }
-                const unsigned over = __ballot_sync(0xffffffffu, here + run > mark);
-                if (here <= mark && over && lane == __ffs(over) - 1)
-                    for (int r = 0; r < cl; ++r) st_peer32(peer_addr(&s.found, (uint32_t)r), (uint32_t)v);
-                before += sum;
-                if (before > mark) break;
-                __syncthreads();
+            // each thread's part of the warp's range, then the thread's entries one by one
+            const int each_has = (share + kThreads - 1) / kThreads, i0 = min(share, tid * each_has);
+            const int i1 = min(share, i0 + each_has), v0 = (rank * kWarps + w) * share - skew;
+            int64_t own = 0;
+            for (int i = i0; i < i1; ++i) own += f(get1(w, i), v0 + i);
+            int64_t run = own;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t up = __shfl_up_sync(0xffffffffu, run, o);
+                if (lane >= o) run += up;
             }
+            if (lane == 31) s.scan[warp] = run;
+            __syncthreads();
+            run += before - own;
+            for (int e = 0; e < warp; ++e) run += s.scan[e];
+            if (run <= mark && mark < run + own)
+                for (int i = i0; i < i1; ++i) {
+                    run += f(get1(w, i), v0 + i);
+                    if (mark < run) {
+                        for (int r = 0; r < cl; ++r) st_peer32(peer_addr(&s.found, (uint32_t)r), (uint32_t)(v0 + i));
+                        break;
+                    }
+                }
         }
         if (cl > 1) cluster_sync();
         else __syncthreads();
@@ -273,6 +294,7 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
     for (int i = tid; i < 129; i += kThreads) s.exp2[i] = kExp2[i];
     for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0;
     if (tid == 0) s.listed = 0;
+    const float largest = m;  // this thread's
     {
         // (floats in the order of whole numbers)
         auto key = [](float x) { return (int64_t)(__float_as_int(x) ^ (__float_as_int(x) < 0 ? 0x7fffffff : 0)); };
@@ -333,27 +355,72 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
         }
         return l > hi ? -1 : l < lo ? kBins : (int)((hi - l) / (hi - lo) * (kBins - 1));
     };
-    uint32_t n4[4];  // tokens in this thread's bins
+    uint32_t n2[2];  // tokens in this thread's bins
     uint32_t n_before, n_all;
-    // Counts the kept tokens; the whole cluster's counts in n4, those before them in n_before.
-    auto count_bins = [&]() {
+    auto count = [&](float l) {
+        const int b = bin_of(l);
+        if (b >= 0 && b < kBins) atomicAdd(&s.hist[b], 1u);
+    };
+    // The sum of all entries' kept weights, with take(logit) for those that are not deep.
+    // Deep ones, mostly the most, are done at once; the others, whose weights take ten times the
+    // instructions, wait in a queue of the warp's until all of its lanes have one.
+    auto sum_weights = [&](auto take) {
+        const bool all = cut_l == -INFINITY;
+        float *const queue = reinterpret_cast<float *>(s.list) + warp * 64;
+        int64_t sum = 0;
+        int waiting = 0;
+        auto weigh_one = [&](float l) {
+            sum += weigh(l);
+            take(l);
+        };
+        for (int j = 0; 128 * j < share; ++j) {
+            const int i = 128 * j + lane * 4;
+            const float4 x4 = i < share ? get4(i) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            const float x[4] = {x4.x, x4.y, x4.z, x4.w};
+            uint32_t w = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float up = weigh.raised(x[e]);
+                const bool on = all || kept(x[e], u0 + i + e - skew), full = on && up >= 38.f - kDeep;
+                if (on && !full) w += Weigh::deep(up);
+                const unsigned who = __ballot_sync(0xffffffffu, full);
+                if (full) queue[waiting + __popc(who & ((1u << lane) - 1))] = x[e];
+                waiting += __popc(who);
+                if (waiting >= 32) {
+                    __syncwarp();
+                    weigh_one(queue[lane]);
+                    waiting -= 32;
+                    const float rest = queue[32 + lane];
+                    __syncwarp();
+                    queue[lane] = rest;
+                    __syncwarp();
+                }
+            }
+            sum += w;
+        }
+        __syncwarp();
+        if (lane < waiting) weigh_one(queue[lane]);
+        __syncwarp();
+        return sum;
+    };
+    // Counts what the pass counts; the whole cluster's counts in n2, those before them in n_before.
+    auto count_bins = [&](auto pass) {
         __syncthreads();
-        each([&](float l, int v) {
-            const int b = bin_of(l);
-            if (b >= 0 && b < kBins && kept(l, v)) atomicAdd(&s.hist[b], 1u);
-        });
+        pass();
         if (cl > 1) cluster_sync();
         else __syncthreads();
-        n4[0] = n4[1] = n4[2] = n4[3] = 0;
-        for (int r = 0; r < cl; ++r) {
-            uint32_t x, y, z, w;
-            asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(x), "=r"(y), "=r"(z), "=r"(w)
-                         : "r"(peer_addr(&s.hist[4 * tid], (uint32_t)r))
+        uint32_t x[kMaxCluster], y[kMaxCluster];
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)  // all under way at once
+            asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];"
+                         : "=r"(x[r]), "=r"(y[r])
+                         : "r"(peer_addr(&s.hist[2 * tid], (uint32_t)min(r, cl - 1)))
                          : "memory");
-            n4[0] += x, n4[1] += y, n4[2] += z, n4[3] += w;
-        }
-        uint32_t run = n4[0] + n4[1] + n4[2] + n4[3];
+        n2[0] = n2[1] = 0;
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)
+            if (r < cl) n2[0] += x[r], n2[1] += y[r];
+        uint32_t run = n2[0] + n2[1];
         const uint32_t own = run;
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t up = __shfl_up_sync(0xffffffffu, run, o);
@@ -367,6 +434,11 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
             if (e < warp) n_before += s.scan_n[e];
             n_all += s.scan_n[e];
         }
+    };
+    auto count_kept = [&]() {
+        each([&](float l, int v) {
+            if (kept(l, v)) count(l);
+        });
     };
     // (after a join: every CTA has read the counts)
     auto clear_bins = [&]() {
@@ -384,40 +456,61 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
                              : "r"(peer_addr(&s.listed, 0))
                              : "memory");
                 if (at < kFew) {
-                    st_peer(peer_addr(&s.list_l[at], 0), l);
-                    st_peer32(peer_addr(&s.list_v[at], 0), (uint32_t)v);
+                    st_peer(peer_addr(&s.list[at].x, 0), l);
+                    st_peer32(peer_addr(&s.list[at].y, 0), (uint32_t)v);
                 }
             }
         });
         if (cl > 1) cluster_sync();
         else __syncthreads();
     };
-    // Ranks the list; where yes(rank, weight before, weight, last), the cut is.
-    auto rank_list = [&](bool weights, auto yes) {
+    // In the first CTA: entry tid (of n) of the list, the number of entries ranked before it
+    // and their weight.  Two threads per entry go through half the list each.
+    struct Entry {
+        float l;
+        int v, place;
+        int64_t w, before;
+    };
+    auto entry = [&](int n) {
+        Entry x = {};
+        const int at = tid % kFew;
+        if (at < n) {
+            x.l = __uint_as_float(s.list[at].x);
+            x.v = (int)s.list[at].y;
+            x.w = weigh(x.l);
+            if (tid < n) *reinterpret_cast<int64_t *>(&s.list[at].z) = x.w;
+        }
+        __syncthreads();
+        const int e0 = tid < kFew ? 0 : n / 2, e1 = tid < kFew ? n / 2 : n;
+#pragma unroll 4
+        for (int e = e0; e < e1; ++e) {
+            const uint4 y = lds128(&s.list[e]);
+            const float l = __uint_as_float(y.x);
+            const bool ahead = l > x.l || (l == x.l && (int)y.y < x.v);
+            x.place += ahead;
+            x.before += ahead ? (int64_t)((uint64_t)y.w << 32 | y.z) : 0;
+        }
+        static_assert(kThreads == 2 * kFew && sizeof(s.hist) >= kFew * 16, "two halves of the list");
+        uint4 *const half = reinterpret_cast<uint4 *>(s.hist);  // (the bins are done with, or cleared before the next use)
+        if (tid >= kFew) half[at] = make_uint4((uint32_t)x.place, 0, (uint32_t)x.before, (uint32_t)(x.before >> 32));
+        __syncthreads();
+        if (tid < kFew) {
+            const uint4 y = half[at];
+            x.place += (int)y.x;
+            x.before += (int64_t)((uint64_t)y.w << 32 | y.z);
+        }
+        return x;
+    };
+    // Ranks the list; where yes(entry, last), the cut is.
+    auto rank_list = [&](auto yes) {
         if (rank == 0) {
             const int n = min((int)s.listed, kFew);
-            if (weights) {
-                if (tid < n) s.list_w[tid] = weigh(s.list_l[tid]);
-                __syncthreads();
-            }
-            if (tid < n) {
-                const float l = s.list_l[tid];
-                const int v = s.list_v[tid];
-                int place = 0;
-                int64_t before = 0;
-                for (int i = 0; i < n; ++i) {
-                    const float x = s.list_l[i];
-                    if (x > l || (x == l && s.list_v[i] < v)) {
-                        ++place;
-                        if (weights) before += s.list_w[i];
-                    }
+            const Entry x = entry(n);
+            if (tid < n && yes(x, x.place == n - 1))
+                for (int r = 0; r < cl; ++r) {
+                    st_peer(peer_addr(&s.cut_l, (uint32_t)r), x.l);
+                    st_peer32(peer_addr(&s.cut_v, (uint32_t)r), (uint32_t)x.v);
                 }
-                if (yes(place, before, weights ? s.list_w[tid] : 0, place == n - 1))
-                    for (int r = 0; r < cl; ++r) {
-                        st_peer(peer_addr(&s.cut_l, (uint32_t)r), l);
-                        st_peer32(peer_addr(&s.cut_v, (uint32_t)r), (uint32_t)v);
-                    }
-            }
             __syncthreads();
             if (tid == 0) s.listed = 0;
         }
@@ -440,53 +533,214 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
         float lo, hi;
     };
     auto span = [&](int b0, int b1, bool weights) {
-        int64_t v[3] = {0, 0, 0};
+        int64_t v[4] = {0, 0, 0, 0};
         float small = INFINITY, large = -INFINITY;
+        inside = 0;
         each([&](float l, int i) {
             const int b = bin_of(l);
             if (b < 0 || b > b1 || !kept(l, i)) return;
             if (b >= b0) {
                 ++v[1];
+                inside |= at_bit;
                 small = fminf(small, l);
                 large = fmaxf(large, l);
             } else if (weights) {
                 v[0] += weigh(l);
             }
         });
-        // both ends as one: order-preserving whole numbers, each 32 bits
+        // (floats in the order of whole numbers)
         auto key = [](float x) { return (int64_t)(__float_as_int(x) ^ (__float_as_int(x) < 0 ? 0x7fffffff : 0)); };
         auto back = [](int64_t x) { return __int_as_float((int)x ^ ((int)x < 0 ? 0x7fffffff : 0)); };
-        join(v, plus);
-        int64_t e[2] = {key(small), key(large)};
-        join(e, [](int n, int64_t x, int64_t y) { return (n == 0) == (x < y) ? x : y; });
-        return Span{v[0], v[1], back(e[0]), back(e[1])};
+        v[2] = -key(small);
+        v[3] = key(large);
+        join(v, [](int n, int64_t x, int64_t y) { return n < 2 ? x + y : x > y ? x : y; });
+        return Span{v[0], v[1], back(-v[2]), back(v[3])};
     };
 
     const bool by_k = k > 0 && k < a.V, by_p = part_p < kUnit;
-    int64_t total = 0;  // of the tokens that top-k keeps
-    if (by_k || by_p) count_bins();
-    if (by_k && n_all > (uint32_t)k) {
-        // ---- the k-th token ---------------------------------------------------------
-        uint32_t want = (uint32_t)k;
-        uint32_t kn[4], kb = n_before;
-        for (int e = 0; e < 4; ++e) kn[e] = n4[e];
-        for (;;) {
-            uint32_t run = kb;
+    const int64_t least = (int64_t)(fminf(fmaxf(min_p, 0.f), 1.f) * 0x1p38f);
+    int64_t target = 0;  // top-p's part of the weights
+    // Bounds of the running weight at the ends of this thread's bins, over `above`; then the
+    // first bin that can reach the target, and the first that must, to bin0 and bin1.
+    auto bound_bins = [&](int64_t above) {
+        float wl[2], wh[2], sl = 0.f, sh = 0.f;
+        auto edge = [&](int b) {
+            return first ? b * (-kOctaves / kBins) : (hi - (hi - lo) * ((float)b / (kBins - 1)) - m) * weigh.ch;
+        };
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (run < want && want <= run + kn[e]) {
-                    s.bin0 = 4 * tid + e;
-                    s.rank = want - run;
-                    s.count = kn[e];
-                }
-                run += kn[e];
+        for (int e = 0; e < 2; ++e) {
+            wh[e] = sh += (float)n2[e] * exp2f(edge(2 * tid + e) + 38.f);
+            wl[e] = sl += (float)n2[e] * exp2f(edge(2 * tid + e + 1) + 38.f);
+        }
+        const float own_l = sl, own_h = sh;
+        for (int o = 1; o < 32; o <<= 1) {
+            const float ul = __shfl_up_sync(0xffffffffu, sl, o), uh = __shfl_up_sync(0xffffffffu, sh, o);
+            if (lane >= o) sl += ul, sh += uh;
+        }
+        if (lane == 31) s.scan_lo[warp] = sl, s.scan_hi[warp] = sh;
+        if (tid == 0) s.bin0 = s.bin1 = kBins - 1;
+        __syncthreads();
+        sl -= own_l, sh -= own_h;
+        for (int e = 0; e < warp; ++e) sl += s.scan_lo[e], sh += s.scan_hi[e];
+        const float need = (float)(target - above);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            if ((sh + wh[e]) * (1.f + kSlack) >= need) atomicMin(&s.bin0, 2 * tid + e);
+            if ((sl + wl[e]) * (1.f - kSlack) >= need) atomicMin(&s.bin1, 2 * tid + e);
+        }
+        __syncthreads();
+    };
+    // The bin where the want-th token falls: bin0, with its rank there and the bin's count.
+    auto find_bin = [&](uint32_t want) {
+        uint32_t run = n_before;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            if (run < want && want <= run + n2[e]) {
+                s.bin0 = 2 * tid + e;
+                s.rank = want - run;
+                s.count = n2[e];
             }
+            run += n2[e];
+        }
+        __syncthreads();
+    };
+    int64_t total = 0;  // of the tokens that top-k keeps
+    bool cut_k = false;
+    // Notes this thread's tokens in bins up to `last`.
+    auto note = [&](int last) {
+        noted = 0;
+        for (int j = 0; 128 * j + lane * 4 < share; ++j) {
+            const float4 x = get4(128 * j + lane * 4);
+            const uint32_t bits = (bin_of(x.x) <= last) | (bin_of(x.y) <= last) << 1 | (bin_of(x.z) <= last) << 2 |
+                                  (bin_of(x.w) <= last) << 3;
+            noted |= (uint64_t)bits << (4 * j);
+        }
+        by_note = true;
+    };
+    if (by_k || by_p) {
+        // the last bin that matters, and the tokens up to it
+        int last = kBins - 1;
+        uint32_t few = 0;
+        bool bounded = false;
+        if (by_k && P.noted && share >= kLong) {
+            // In long ranges the threads' largest logits are counted first, which are few:
+            // the k-th of them is no larger than the k-th of all.
+            count_bins([&]() { count(largest); });
+            if (n_all >= (uint32_t)k) {
+                find_bin((uint32_t)k);
+                last = s.bin0;
+                bounded = true;
+            }
+            note(last);
+            int64_t v[1] = {__popcll(noted)};
+            join(v, plus);
+            few = (uint32_t)v[0];
+            cut_k = bounded || few > (uint32_t)k;
+            clear_bins();
+        }
+        if (!by_note || few > kFew) {
+            int64_t v[1] = {0};
+            const bool sums = by_p && !by_k;
+            count_bins([&]() {
+                if (sums && P.noted) v[0] = sum_weights(count);  // (deep ones are not counted)
+                else each([&](float l, int) {
+                    count(l);
+                    if (sums) v[0] += weigh(l);
+                });
+            });
+            cut_k = by_k && (bounded || n_all > (uint32_t)k);
+            if (cut_k) {
+                find_bin((uint32_t)k);
+                last = s.bin0;
+                few = (uint32_t)k - s.rank + s.count;
+            } else {
+                few = n_all;
+                if (by_p) {
+                    if (by_k) each([&](float l, int) { v[0] += weigh(l); });
+                    join(v, plus);
+                    total = v[0];
+                    target = part(total, part_p);
+                    bound_bins(0);
+                    last = s.bin1;
+                    if (sums && P.noted && last >= (int)(kDeep * (kBins / kOctaves)) - 1) {
+                        // the cut may be among the deep ones: with them
+                        clear_bins();
+                        count_bins(count_kept);
+                        bound_bins(0);
+                        last = s.bin1;
+                        few = n_all;
+                    }
+                    if (tid == last / 2) s.count = n_before + n2[0] + (last & 1 ? n2[1] : 0);
+                    __syncthreads();
+                    few = s.count;
+                }
+            }
+        }
+        if (few <= kFew) {
+            // ---- one CTA has them all -------------------------------------------------
+            collect(0, last);
+            if (rank != 0) {
+                if (probs) write_probs([](float, int) { return 0.f; });
+                if (probs && cl > 1) cluster_sync();
+                return;
+            }
+            const int n = (int)few;
+            const Entry x = entry(n);
+            int64_t w = tid < n ? x.w : 0;
+            // sum over the list, for all
+            auto sum = [&](int64_t x) {
+                for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+                __syncthreads();
+                if (lane == 0) s.scan[warp] = x;
+                __syncthreads();
+                x = 0;
+                for (int e = 0; e < kFew / 32; ++e) x += s.scan[e];
+                return x;
+            };
+            bool on = tid < n && (!cut_k || x.place < k);
+            if (by_p) {
+                if (target == 0) target = part(sum(on ? w : 0), part_p);  // the list has all that top-k keeps
+                on = on && (x.place == 0 || x.before < target);
+            }
+            if (!on || w < least) w = 0;
+            total = sum(w);
+            if (tid < n) *reinterpret_cast<int64_t *>(&s.list[tid].z) = w;
             __syncthreads();
+            if (a.token) {
+                int64_t u = (int64_t)(a.u[t] * 0x1p24f);
+                u = u < 0 ? 0 : u >= kUnit ? kUnit - 1 : u;
+                const int64_t mark = part(total, u);
+                // the weight of kept tokens before this one by index
+                int64_t run = 0;
+                if (tid < kFew)
+#pragma unroll 4
+                    for (int e = 0; e < n; ++e) {
+                        const uint4 y = lds128(&s.list[e]);
+                        run += (int)y.y < x.v ? (int64_t)((uint64_t)y.w << 32 | y.z) : 0;
+                    }
+                if (w > 0 && run <= mark && mark < run + w) a.token[t] = x.v;
+            }
+            if (probs) {
+                write_probs([](float, int) { return 0.f; });
+                if (cl > 1) cluster_sync();
+                else __syncthreads();
+                if (w > 0) probs[x.v] = (float)w * (1.f / (float)total);
+            }
+            return;
+        }
+        if (P.noted && few <= (uint32_t)a.V / 2) note(last);
+    }
+    const uint64_t candidates = noted;
+    if (cut_k) {
+        // ---- the k-th token ---------------------------------------------------------
+        const uint32_t n2_0 = n2[0], n2_1 = n2[1], n_before_0 = n_before;
+        for (uint32_t want = (uint32_t)k;;) {
+            if (!first) find_bin(want);
             const int b = s.bin0;
             want = s.rank;
             if (s.count <= kFew) {
                 collect(b, b);
-                rank_list(false, [&](int place, int64_t, int64_t, bool) { return place == (int)want - 1; });
+                rank_list([&](const Entry &x, bool) { return x.place == (int)want - 1; });
                 break;
             }
             const Span e = span(b, b, false);
@@ -497,58 +751,31 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
             first = false;
             hi = e.hi;
             lo = e.lo;
+            noted = inside;  // only these are looked at from here on
             clear_bins();
-            count_bins();
-            for (int i = 0; i < 4; ++i) kn[i] = n4[i];
-            kb = n_before;
+            count_bins(count_kept);
         }
-    }
-    if (by_p) {
-        // ---- where the running weight reaches p of the total ------------------------------
-        {
+        // the first bins' counts of what is left
+        first = true;
+        noted = candidates;
+        const uint32_t room = (uint32_t)k > n_before_0 ? (uint32_t)k - n_before_0 : 0;
+        n2[0] = min(n2_0, room);
+        n2[1] = min(n2_1, room - n2[0]);
+        if (by_p) {
             int64_t v[1] = {0};
             each([&](float l, int i) {
                 if (kept(l, i)) v[0] += weigh(l);
             });
             join(v, plus);
             total = v[0];
+            target = part(total, part_p);
         }
-        const int64_t target = part(total, part_p);
+    }
+    if (by_p) {
+        // ---- where the running weight reaches p of the total ------------------------------
         int64_t above = 0;
-        // the first histogram again, of the tokens that are left
-        if (!first || cut_l > -INFINITY) {
-            first = true;
-            clear_bins();
-            count_bins();
-        }
         for (;;) {
-            // bounds of the running weight behind each of this thread's bins
-            float wl[4], wh[4], sl = 0.f, sh = 0.f;
-            auto edge = [&](int b) {
-                return first ? b * (-kOctaves / kBins) : (hi - (hi - lo) * ((float)b / (kBins - 1)) - m) * weigh.ch;
-            };
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                wh[e] = sh += (float)n4[e] * exp2f(edge(4 * tid + e) + 38.f);
-                wl[e] = sl += (float)n4[e] * exp2f(edge(4 * tid + e + 1) + 38.f);
-            }
-            const float own_l = sl, own_h = sh;
-            for (int o = 1; o < 32; o <<= 1) {
-                const float ul = __shfl_up_sync(0xffffffffu, sl, o), uh = __shfl_up_sync(0xffffffffu, sh, o);
-                if (lane >= o) sl += ul, sh += uh;
-            }
-            if (lane == 31) s.scan_lo[warp] = sl, s.scan_hi[warp] = sh;
-            if (tid == 0) s.bin0 = s.bin1 = kBins - 1;
-            __syncthreads();
-            sl -= own_l, sh -= own_h;
-            for (int e = 0; e < warp; ++e) sl += s.scan_lo[e], sh += s.scan_hi[e];
-            const float need = (float)(target - above);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if ((sh + wh[e]) * (1.f + kSlack) >= need) atomicMin(&s.bin0, 4 * tid + e);
-                if ((sl + wl[e]) * (1.f - kSlack) >= need) atomicMin(&s.bin1, 4 * tid + e);
-            }
-            __syncthreads();
+            bound_bins(above);
             int b0 = s.bin0, b1 = s.bin1;
             Span e = span(b0, b1, true);
             if (!first && e.count > kFew && e.lo < e.hi && e.lo == lo && e.hi == hi) {
@@ -565,8 +792,8 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
             above += e.above;
             if (e.count <= kFew) {
                 collect(b0, b1);
-                rank_list(true, [&](int, int64_t before, int64_t w, bool last) {
-                    return above + before < target && (above + before + w >= target || last);
+                rank_list([&](const Entry &x, bool last) {
+                    return above + x.before < target && (above + x.before + x.w >= target || last);
                 });
                 break;
             }
@@ -578,20 +805,24 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
             first = false;
             hi = e.hi;
             lo = e.lo;
+            noted = inside;  // only these are looked at from here on
             clear_bins();
-            count_bins();
+            count_bins(count_kept);
         }
     }
 
+    noted = candidates;
     // ---- the token ---------------------------------------------------------------------
-    const int64_t least = (int64_t)(fminf(fmaxf(min_p, 0.f), 1.f) * 0x1p38f);
+    // (a logit whose weight cannot reach min_p's needs no weight)
+    const float floor_l = least > 0 ? log2f((float)least) - 38.01f : -INFINITY;
     auto final_weight = [&](float l, int v) -> int64_t {
-        if (!kept(l, v)) return 0;
+        if (!kept(l, v) || weigh.rough(l) < floor_l) return 0;
         const int64_t w = weigh(l);
         return w >= least ? w : 0;
     };
     int64_t v[1] = {0};
-    each([&](float l, int i) { v[0] += final_weight(l, i); });
+    if (by_note || !P.noted || least > 0) each([&](float l, int i) { v[0] += final_weight(l, i); });
+    else v[0] = sum_weights([](float) {});
     join(v, plus);
     if (a.token) {
         int64_t u = (int64_t)(a.u[t] * 0x1p24f);
@@ -628,6 +859,7 @@ int sample_launch(const sgmv_sample_args &a, int nsm, cudaStream_t stream) {
     p.share = ((a.V + 7 + cl * kWarps - 1) / (cl * kWarps) + 7) / 8 * 8;
     const size_t bytes = (size_t)p.share * kWarps * 4;
     p.staged = bytes <= 200 * 1024;
+    p.noted = p.staged && p.share <= 64 / 4 * 128;
     const size_t smem = p.staged ? bytes : 0;
     switch (a.dtype) {
         case SGMV_F16: return launch<__half>(p, cl, smem, stream);
