@@ -27,11 +27,12 @@ namespace {
 
 constexpr int kNormThreads = 256;
 constexpr int kNormCtas = 3;  // per SM
+constexpr int kGradCtas = 2;  // the gradient's, which holds more
 constexpr int kChunk = 8;     // tokens whose angles are held
 
 enum NormMode : int {
     kHalves = 0,       // pairs (i, i + pairs), pairs a multiple of 8: a lane has two vectors
-    kInterleaved = 1,  // pairs (2i, 2i + 1): one vector
+    kInterleaved = 1,  // pairs (2i, 2i + 1): a lane has two vectors side by side
     kGather = 2,       // pairs (i, i + pairs) of any number: one vector, partners read singly
 };
 
@@ -48,15 +49,35 @@ struct GradParams {
     float *part;     // [CTA][D]
 };
 
-// Where a lane's columns are: [c, c + 8), and with kHalves [c + pairs, ...) if they turn.
+// Where a lane's columns are: [c, c + 8), and [d, d + 8) if it has a second vector.
 template <int MODE> struct Columns {
-    int c, d;    // d: second vector's first column (kHalves, turning lanes)
-    bool here, turns;
-    __device__ __forceinline__ Columns(int w, int rot, int uph, int pairs) {
+    int c, d;
+    bool here, turns, second;
+    __device__ __forceinline__ Columns(int w, int rot, int uph, int pairs, int D) {
         here = w < uph;
-        turns = MODE == kHalves ? w < rot : here;
-        c = MODE == kHalves && !turns ? (w - rot) * 8 + 2 * pairs : w * 8;
-        d = c + pairs;
+        turns = w < rot;
+        c = MODE == kInterleaved ? w * 16 : MODE == kHalves && !turns ? (w - rot) * 8 + 2 * pairs : w * 8;
+        d = MODE == kInterleaved ? c + 8 : c + pairs;
+        second = here && (MODE == kInterleaved ? d < D : MODE == kHalves && turns);
+    }
+};
+
+// Token and head of an item, and of the one `by` items on, without a division each time.
+struct Walk {
+    int t, h, heads, dt, dh;
+    __device__ __forceinline__ Walk(int i, int heads_, int by) : heads(heads_) {
+        dt = by / heads;
+        dh = by - dt * heads;
+        to(i);
+    }
+    __device__ __forceinline__ void to(int i) {
+        t = i / heads;
+        h = i - t * heads;
+    }
+    __device__ __forceinline__ void step() {
+        t += dt;
+        h += dh;
+        if (h >= heads) h -= heads, ++t;
     }
 };
 
@@ -95,13 +116,26 @@ __device__ __forceinline__ void turn(const Columns<MODE> &col, const float2 *ang
             y[2 * i + 1] = b * s1 + y[2 * i + 1] * c1;
         }
     } else if (MODE == kInterleaved) {
+        const float4 *const at = reinterpret_cast<const float4 *>(angle + col.c / 2);
+        auto two = [](float4 u, float (&z)[8], int i, bool last) {
+            const float s0 = BACK ? -u.y : u.y, s1 = BACK ? -u.w : u.w;
+            const float a = z[4 * i], b = z[4 * i + 2];
+            z[4 * i] = a * u.x - z[4 * i + 1] * s0;
+            z[4 * i + 1] = a * s0 + z[4 * i + 1] * u.x;
+            if (last) return;
+            z[4 * i + 2] = b * u.z - z[4 * i + 3] * s1;
+            z[4 * i + 3] = b * s1 + z[4 * i + 3] * u.z;
+        };
+        if (col.c / 2 + 8 <= pairs) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (col.c / 2 + i >= pairs) break;  // columns behind the last pair stay
-            const float2 u = angle[col.c / 2 + i];
-            const float s = BACK ? -u.y : u.y, a = x[2 * i], b = x[2 * i + 1];
-            x[2 * i] = a * u.x - b * s;
-            x[2 * i + 1] = a * s + b * u.x;
+            for (int i = 0; i < 2; ++i) two(at[i], x, i, false), two(at[2 + i], y, i, false);
+        } else {  // columns behind the last pair stay
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int left = pairs - (col.c / 2 + 2 * i);
+                if (left > 0) two(at[i], x, i, left == 1);
+                if (left > 4) two(at[2 + i], y, i, left == 5);
+            }
         }
     } else {  // y: the partners
 #pragma unroll
@@ -134,43 +168,45 @@ __global__ void __launch_bounds__(kNormThreads, kNormCtas)
     sgmv_norm_rope_kernel(const __grid_constant__ NormParams P, int *err) {
     const sgmv_rope_args &a = P.a.rope;
     constexpr int kGroups = kNormThreads / G;
-    constexpr bool kTwo = MODE == kHalves;
+    constexpr bool kTwo = MODE != kGather;
     __shared__ __align__(16) float2 s_angles[2][kChunk][kRopeMaxPairs];
     const int g = threadIdx.x / G, pairs = a.pairs;
-    const Columns<MODE> col(threadIdx.x % G, P.rot, P.uph, pairs);
+    const Columns<MODE> col(threadIdx.x % G, P.rot, P.uph, pairs, a.D);
     const bool append = a.k_cache != nullptr;
     const int heads = a.Hq + a.Hk + (append ? a.Hk : 0);
     pdl_wait();
     pdl_trigger();
     const int all = a.T * heads, own = (all + (int)gridDim.x - 1) / (int)gridDim.x;
     const int i0 = min(all, own * (int)blockIdx.x), i1 = min(all, i0 + own);
-    // an item's rows, and what is read of them
+    // An item's rows, and what is read of them.  No load stands under a condition (behind the
+    // last item its rows are read again, lanes without columns read others'): its
+    // answer would be waited for where the branches meet.
     struct Item {
         int64_t t;
         int h;
         uint4 x, y;
         int32_t slot;
     };
+    const int c_at = col.here ? col.c : 0, d_at = col.second ? col.d : c_at;
+    const int32_t *const slots = append ? a.slots : a.positions;
+    Walk walk(i0 + g, heads, kGroups), end(i1 - 1, heads, kGroups);
     auto fetch = [&](int i, Item &m) {
-        const int it = i / heads;
-        m.t = it;
-        m.h = i - it * heads;
-        m.slot = -1;
-        if (i >= i1) return;
-        const T *src = m.h < a.Hq ? static_cast<const T *>(a.q) + m.t * a.q_token + m.h * a.q_head
-                       : m.h < a.Hq + a.Hk
-                           ? static_cast<const T *>(a.k) + m.t * a.k_token + (m.h - a.Hq) * a.k_head
-                           : static_cast<const T *>(a.v) + m.t * a.v_token + (m.h - a.Hq - a.Hk) * a.v_head;
-        if (col.here) {
-            m.x = *reinterpret_cast<const uint4 *>(src + col.c);
-            if (kTwo && col.turns) m.y = *reinterpret_cast<const uint4 *>(src + col.d);
-            if (MODE == kGather && m.h < a.Hq + a.Hk) {
-                uint16_t *const p = reinterpret_cast<uint16_t *>(&m.y);
-                for (int e = 0; e < 8; ++e)
-                    p[e] = reinterpret_cast<const uint16_t *>(src)[partner_of(col.c + e, pairs)];
-            }
+        m.t = i < i1 ? walk.t : end.t;
+        m.h = i < i1 ? walk.h : end.h;
+        const bool is_q = m.h < a.Hq, is_v = m.h >= a.Hq + a.Hk;
+        const int h = m.h - (is_q ? 0 : is_v ? a.Hq + a.Hk : a.Hq);
+        const T *const src = static_cast<const T *>(is_q ? a.q : is_v ? a.v : a.k) +
+                             m.t * (is_q ? a.q_token : is_v ? a.v_token : a.k_token) +
+                             h * (is_q ? a.q_head : is_v ? a.v_head : a.k_head);
+        m.x = *reinterpret_cast<const uint4 *>(src + c_at);
+        if (kTwo) m.y = *reinterpret_cast<const uint4 *>(src + d_at);
+        if (MODE == kGather) {
+            uint16_t p[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[e] = reinterpret_cast<const uint16_t *>(src)[partner_of(c_at + e, pairs)];
+            m.y = make_uint4(p[0] | p[1] << 16, p[2] | p[3] << 16, p[4] | p[5] << 16, p[6] | p[7] << 16);
         }
-        if (append && m.h >= a.Hq) m.slot = a.slots[m.t];
+        m.slot = slots[m.t];
     };
     // the weights of this lane's columns
     uint4 wq[2], wk[2];
@@ -178,11 +214,12 @@ __global__ void __launch_bounds__(kNormThreads, kNormCtas)
         if (!w || !col.here) return;
         const T *const src = static_cast<const T *>(w);
         to[0] = *reinterpret_cast<const uint4 *>(src + col.c);
-        if (kTwo && col.turns) to[1] = *reinterpret_cast<const uint4 *>(src + col.d);
+        if (col.second) to[1] = *reinterpret_cast<const uint4 *>(src + col.d);
         if (MODE == kGather)
             for (int e = 0; e < 8; ++e)
                 reinterpret_cast<T *>(&to[1])[e] = src[partner_of(col.c + e, pairs)];
     };
+    if (i0 >= i1) return;
     Item next;
     fetch(i0 + g, next);
     weights(P.a.q_weight, wq);
@@ -195,13 +232,12 @@ __global__ void __launch_bounds__(kNormThreads, kNormCtas)
         // (whole warps together: the sums are shuffled)
         for (int ib = c0; ib < c1; ib += kGroups) {
             const bool mine = ib + g < c1;
-            Item m;
-            if (mine) {
-                m = next;
-                // the group's next item, in this chunk or the next one
-                const int after = ib + g + kGroups;
-                fetch(after < c1 ? after : c1 + g, next);
-            }
+            const Item m = next;
+            // the group's next item, in this chunk or the next one
+            const int after = ib + g + kGroups;
+            if (after < c1) walk.step();
+            else walk.to(c1 + g);
+            fetch(after < c1 ? after : c1 + g, next);
             if (!__any_sync(0xffffffffu, mine)) continue;
             const bool is_v = mine && m.h >= a.Hq + a.Hk, is_k = mine && m.h >= a.Hq && !is_v;
             float x[8], y[8];
@@ -209,7 +245,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormCtas)
             for (int e = 0; e < 8; ++e) x[e] = y[e] = 0.f;
             if (mine && col.here) {
                 unpack8<T>(m.x, x);
-                if ((kTwo && col.turns) || (MODE == kGather && !is_v)) unpack8<T>(m.y, y);
+                if (col.second || (MODE == kGather && !is_v)) unpack8<T>(m.y, y);
             }
             const bool normed = mine && !is_v && (is_k ? P.a.k_weight : P.a.q_weight) != nullptr;
             float ss = 0.f;
@@ -227,14 +263,14 @@ __global__ void __launch_bounds__(kNormThreads, kNormCtas)
                 unpack8<T>(is_k ? wk[0] : wq[0], w);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[e] *= r * w[e];
-                if ((kTwo && col.turns) || MODE == kGather) {
+                if (col.second || MODE == kGather) {
                     unpack8<T>(is_k ? wk[1] : wq[1], w);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) y[e] *= r * w[e];
                 }
             }
             if (!is_v) turn<MODE, false>(col, s_angles[buf][m.t - t0], pairs, x, y);
-            const bool second = kTwo && col.turns;
+            const bool second = col.second;
             auto put16 = [&](T *dst) {
                 store8<T>(dst + col.c, x);
                 if (second) store8<T>(dst + col.d, y);
@@ -245,6 +281,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormCtas)
             }
             const int h = m.h - a.Hq - (is_v ? a.Hk : 0);
             if (is_k && a.k_out) put16(static_cast<T *>(a.k_out) + m.t * a.k_out_token + h * a.k_out_head);
+            if (!append) continue;
             if (m.slot < 0 || (int64_t)m.slot >= (int64_t)a.num_blocks * a.block_size) {
                 if (m.slot != -1) set_error(err, kErrBadIndex);
                 continue;
@@ -260,21 +297,20 @@ __global__ void __launch_bounds__(kNormThreads, kNormCtas)
                 put16(static_cast<T *>(is_v ? a.v_cache : a.k_cache) + off);
             }
         }
-        if (c0 + g >= c1) fetch(c1 + g, next);  // no item of this chunk was this group's
         c0 = c1;
     }  // the next chunk's angles go to the other buffer: one barrier per chunk
 }
 
 template <typename T, int MODE, int G>
-__global__ void __launch_bounds__(kNormThreads, kNormCtas)
+__global__ void __launch_bounds__(kNormThreads, kGradCtas)
     sgmv_norm_rope_grad_kernel(const __grid_constant__ GradParams P) {
     const sgmv_norm_rope_grad_args &a = P.a;
     constexpr int kGroups = kNormThreads / G;
-    constexpr bool kTwo = MODE == kHalves;
+    constexpr bool kTwo = MODE != kGather;
     __shared__ __align__(16) float2 s_angles[2][kChunk][kRopeMaxPairs];
     __shared__ float s_dw[kGroups > 8 ? 8 : kGroups][kSpecMaxD];
     const int g = threadIdx.x / G, pairs = a.pairs;
-    const Columns<MODE> col(threadIdx.x % G, P.rot, P.uph, pairs);
+    const Columns<MODE> col(threadIdx.x % G, P.rot, P.uph, pairs, a.D);
     pdl_wait();
     pdl_trigger();
     const bool is_k = (int)blockIdx.x >= P.ctas_q;
@@ -290,32 +326,40 @@ __global__ void __launch_bounds__(kNormThreads, kNormCtas)
     const int all = a.T * heads, own = (all + ctas - 1) / ctas;
     const int i0 = min(all, own * cta), i1 = min(all, i0 + own);
     struct Item {
+        int t, h;
         uint4 x, y, gx, gy;
     };
+    // (no load under a condition, as above)
+    const int c_at = col.here ? col.c : 0, d_at = col.second ? col.d : c_at;
+    const T *const X0 = W ? X : DY;  // x is not read without its weight
+    const int64_t x0_token = W ? x_token : dy_token, x0_head = W ? x_head : dy_head;
+    Walk walk(i0 + g, heads, kGroups), end(max(i1 - 1, 0), heads, kGroups);
     auto fetch = [&](int i, Item &m) {
-        if (i >= i1 || !col.here) return;
-        const int it = i / heads;
-        const int64_t t = it, h = i - it * heads;
-        const T *const dy = DY + t * dy_token + h * dy_head, *const x = X + t * x_token + h * x_head;
-        m.gx = *reinterpret_cast<const uint4 *>(dy + col.c);
-        if (W) m.x = *reinterpret_cast<const uint4 *>(x + col.c);
-        if (kTwo && col.turns) {
-            m.gy = *reinterpret_cast<const uint4 *>(dy + col.d);
-            if (W) m.y = *reinterpret_cast<const uint4 *>(x + col.d);
+        m.t = i < i1 ? walk.t : end.t;
+        m.h = i < i1 ? walk.h : end.h;
+        const T *const dy = DY + m.t * dy_token + m.h * dy_head, *const x = X0 + m.t * x0_token + m.h * x0_head;
+        m.gx = *reinterpret_cast<const uint4 *>(dy + c_at);
+        m.x = *reinterpret_cast<const uint4 *>(x + c_at);
+        if (kTwo) {
+            m.gy = *reinterpret_cast<const uint4 *>(dy + d_at);
+            m.y = *reinterpret_cast<const uint4 *>(x + d_at);
         }
-        if (MODE == kGather)
-            for (int e = 0; e < 8; ++e)
-                reinterpret_cast<T *>(&m.gy)[e] = dy[partner_of(col.c + e, pairs)];
+        if (MODE == kGather) {
+            uint16_t p[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[e] = reinterpret_cast<const uint16_t *>(dy)[partner_of(c_at + e, pairs)];
+            m.gy = make_uint4(p[0] | p[1] << 16, p[2] | p[3] << 16, p[4] | p[5] << 16, p[6] | p[7] << 16);
+        }
     };
     float w[8], v[8], dw[8], dv[8];  // weights of the lane's columns, and their gradients
 #pragma unroll
     for (int e = 0; e < 8; ++e) w[e] = v[e] = 1.f, dw[e] = dv[e] = 0.f;
     if (W && col.here) {
         load8<T>(W + col.c, w);
-        if (kTwo && col.turns) load8<T>(W + col.d, v);
+        if (col.second) load8<T>(W + col.d, v);
     }
-    Item next;
-    fetch(i0 + g, next);
+    Item next = {};
+    if (i0 < i1) fetch(i0 + g, next);
     int buf = 0;
     for (int c0 = i0; c0 < i1; buf ^= 1) {
         const int t0 = c0 / heads, c1 = min((int64_t)i1, ((int64_t)t0 + kChunk) * heads);
@@ -324,18 +368,16 @@ __global__ void __launch_bounds__(kNormThreads, kNormCtas)
         for (int ib = c0; ib < c1; ib += kGroups) {
             const int i = ib + g;
             const bool mine = i < c1;
-            Item m;
-            if (mine) {
-                m = next;
-                fetch(i + kGroups < c1 ? i + kGroups : c1 + g, next);
-            }
+            const Item m = next;
+            if (i + kGroups < c1) walk.step();
+            else walk.to(c1 + g);
+            fetch(i + kGroups < c1 ? i + kGroups : c1 + g, next);
             if (!__any_sync(0xffffffffu, mine)) continue;
-            const bool on = mine && col.here, second = kTwo && col.turns;
+            const bool on = mine && col.here, second = col.second;
             float gx[8], gy[8], x[8], y[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) gx[e] = gy[e] = x[e] = y[e] = 0.f;
-            const int it = i / heads;
-            const int64_t t = it, h = i - it * heads;
+            const int64_t t = mine ? m.t : t0, h = mine ? m.h : 0;
             if (on) {
                 unpack8<T>(m.gx, gx);
                 if (second || MODE == kGather) unpack8<T>(m.gy, gy);
@@ -376,7 +418,6 @@ __global__ void __launch_bounds__(kNormThreads, kNormCtas)
                 if (second) store8<T>(dx + col.d, gy);
             }
         }
-        if (c0 + g >= c1) fetch(c1 + g, next);
         c0 = c1;
     }
     if (!W) return;
@@ -395,7 +436,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormCtas)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             s_dw[warp][col.c + e] = dw[e];
-            if (kTwo && col.turns) s_dw[warp][col.d + e] = dv[e];
+            if (col.second) s_dw[warp][col.d + e] = dv[e];
         }
     }
     __syncthreads();
@@ -434,8 +475,8 @@ int mode_of(int interleaved, int pairs) {
     return interleaved ? kInterleaved : pairs % 8 == 0 ? kHalves : kGather;
 }
 void places(int mode, int D, int pairs, int32_t *rot, int32_t *uph) {
-    *rot = mode == kHalves ? pairs / 8 : D / 8;
-    *uph = mode == kHalves ? pairs / 8 + (D - 2 * pairs) / 8 : D / 8;
+    *uph = mode == kHalves ? pairs / 8 + (D - 2 * pairs) / 8 : mode == kInterleaved ? (D + 15) / 16 : D / 8;
+    *rot = mode == kHalves ? pairs / 8 : *uph;
 }
 
 template <typename T, int MODE, int G> int launch(const NormParams &p, int nsm, int *err, cudaStream_t stream) {
@@ -465,7 +506,7 @@ template <typename T> int launch_mode(const NormParams &p, int mode, int nsm, in
 template <typename T, int MODE, int G> int launch_grad(GradParams p, int nsm, cudaStream_t stream) {
     const sgmv_norm_rope_grad_args &a = p.a;
     // CTAs to q and k by their rows
-    const int64_t most = (int64_t)kNormCtas * std::min(std::max(1, nsm), kGradMaxSms), groups = kNormThreads / G;
+    const int64_t most = (int64_t)kGradCtas * std::min(std::max(1, nsm), kGradMaxSms), groups = kNormThreads / G;
     const int64_t q = ((int64_t)a.T * a.Hq + groups - 1) / groups, k = ((int64_t)a.T * a.Hk + groups - 1) / groups;
     int64_t nq = q, nk = k;
     if (q + k > most) {
@@ -511,7 +552,7 @@ int norm_rope_launch(const sgmv_norm_rope_args &a, const uint64_t *turns, int ns
                                     : launch_mode<__nv_bfloat16>(p, mode, nsm, err, stream);
 }
 
-size_t norm_rope_grad_workspace(int32_t D) { return (size_t)kNormCtas * kGradMaxSms * (size_t)D * 4u; }
+size_t norm_rope_grad_workspace(int32_t D) { return (size_t)kGradCtas * kGradMaxSms * (size_t)D * 4u; }
 
 int norm_rope_grad_launch(const sgmv_norm_rope_grad_args &a, const uint64_t *turns, int nsm, cudaStream_t stream) {
     GradParams p;
