@@ -269,22 +269,35 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
     const float top_p = a.top_p ? a.top_p[t] : a.top_p_all, min_p = a.min_p ? a.min_p[t] : a.min_p_all;
     float m = -INFINITY;
     if (P.staged) {
-        for (int i = lane * kVec; i < share; i += 32 * kVec) {
-            const int u = u0 + i;
-            float x[kVec];
-            if (u >= skew && u + kVec <= u_end) {
-                const uint4 raw = __ldcs(reinterpret_cast<const uint4 *>(row + (u - skew)));
+        // Four vectors under way at a time, none of them under a condition (their answers would be
+        // waited for one by one): a vector that is not whole within the row reads another, and
+        // its entries singly.
+        const int whole0 = (skew + kVec - 1) / kVec * kVec, whole1 = u_end / kVec * kVec - kVec;
+        for (int i0 = lane * kVec; i0 < share; i0 += 4 * 32 * kVec) {
+            uint4 raw[4];
+            if (whole0 <= whole1) {
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) x[e] = canonical(to_f<T>(reinterpret_cast<const T *>(&raw)[e]));
-            } else {
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) x[e] = read1(u + e);
+                for (int b = 0; b < 4; ++b)
+                    raw[b] = __ldcs(reinterpret_cast<const uint4 *>(
+                        row + (max(whole0, min(whole1, u0 + i0 + b * 32 * kVec)) - skew)));
             }
 #pragma unroll
-            for (int e = 0; e < kVec; e += 4) {
-                sts128(mine + i + e, make_uint4(__float_as_uint(x[e]), __float_as_uint(x[e + 1]),
-                                                __float_as_uint(x[e + 2]), __float_as_uint(x[e + 3])));
-                m = fmaxf(m, fmaxf(fmaxf(x[e], x[e + 1]), fmaxf(x[e + 2], x[e + 3])));
+            for (int b = 0; b < 4; ++b) {
+                const int i = i0 + b * 32 * kVec, u = u0 + i;
+                if (i >= share) break;
+                float x[kVec];
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) x[e] = canonical(to_f<T>(reinterpret_cast<const T *>(&raw[b])[e]));
+                if (u < whole0 || u > whole1) {
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e) x[e] = read1(u + e);
+                }
+#pragma unroll
+                for (int e = 0; e < kVec; e += 4) {
+                    sts128(mine + i + e, make_uint4(__float_as_uint(x[e]), __float_as_uint(x[e + 1]),
+                                                    __float_as_uint(x[e + 2]), __float_as_uint(x[e + 3])));
+                    m = fmaxf(m, fmaxf(fmaxf(x[e], x[e + 1]), fmaxf(x[e + 2], x[e + 3])));
+                }
             }
         }
         __syncwarp();
