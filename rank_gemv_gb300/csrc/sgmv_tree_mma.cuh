@@ -36,8 +36,11 @@
 // into a ring of 32 KB stages, through the block table: by TMA, or, for pages
 // that are no multiple of 8 tokens, with cp.async, 16 bytes per lane.  A cache of
 // e4m3 is brought as it is, into a ring of its own, from which four more warps convert it
-// to the queries' type (exactly: every e4m3 value is one of both types) into the
-// stages, so that the rest of the kernel, and its accuracy, are those of a 16-bit cache.
+// to f16 (exactly) into the stages, so that the rest of the kernel is that of a 16-bit
+// cache.  Queries of bf16 become f16 too, each row times a power of two that brings its
+// largest value near f16's: what the smallest lose is 2^-39 of that.  (Converted to bf16,
+// for which there is no instruction, K and V cost 8 trees of 4 nodes, 64 heads on 8 over 32768
+// tokens, 153 us in place of 104.)
 //
 // Values that a row does not see never reach it: scores are masked after
 // the product, and non-finite v of tree nodes are taken out of the staged
@@ -88,6 +91,12 @@ template <int RT, bool KV8> struct Shape {
     // an e4m3 cache: stages of 16 KB that hold it as it is, in place of one or two others
     static constexpr int kRaw = !KV8 ? 0 : kAll > 4 ? 4 : 2;
     static constexpr int kStages = kAll - kRaw / 2;
+    // The next tile's scores are asked for before this tile's last product, but not where
+    // converting K and V is what takes the time: the product would wait for the next K,
+    // and the next V's stage for the product (32 trees over 4096 tokens 150 us ahead, 140
+    // behind; 8 trees of 4, 8 and 64 nodes, 64 heads on 8, 110, 117 and 432 ahead, 104, 125 and
+    // 491 behind).
+    static constexpr bool kAhead = !KV8 || RT > 32;
     // What an item costs beside its tiles, in tiles: with 0, 1 and 2, 32 trees over 4096
     // tokens took 202, 191 and 191 us (32 nodes, RT 32), 227, 209 and 204 (64), 155,
     // 145 and 137 (64 nodes, 32 heads on 8, RT 128; 136 with 3).
@@ -105,7 +114,8 @@ template <int RT, bool KV8> struct Shape {
     static constexpr uint32_t kOffTab = kOffP + kPBytes;            // cp.async: row offsets of 2 tiles
     static constexpr uint32_t kOffSee = kOffTab + 2u * kTok * 8u;   // who sees each node, two trees
     static constexpr uint32_t kOffRow = kOffSee + 2u * SGMV_TREE_MAX_NODES * kWords * 4u;  // rows' places
-    static constexpr uint32_t kBytes = kOffRow + kSegs * RT * 8u + 1024u;  // + alignment
+    static constexpr uint32_t kOffScale = kOffRow + kSegs * RT * 8u;  // their scores' factors
+    static constexpr uint32_t kBytes = kOffScale + (KV8 ? kSegs * RT * 4u : 0u) + 1024u;  // + alignment
 };
 
 struct MmaParams {
@@ -248,6 +258,15 @@ __device__ __forceinline__ void fma_pair(float &x, float &y, float c, float a, f
     asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(v) : "l"(k), "l"(w));
     asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
 }
+// ... with a factor each (as bits).
+__device__ __forceinline__ void fma_pair(float &x, float &y, uint32_t c, uint32_t d, float a, float b) {
+    uint64_t v, w, k;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(k) : "r"(c), "r"(d));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(w) : "f"(a), "f"(b));
+    asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(v) : "l"(k), "l"(w));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
 __device__ __forceinline__ void add_pair(float &x, float &y, float a, float b) {
     uint64_t v, w;
     asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
@@ -343,42 +362,14 @@ template <typename T> __device__ __forceinline__ bool bad16(uint32_t h) {
     return (h & e) == e;
 }
 
-// Four e4m3 values as 16-bit ones, exactly.  f16: the conversion instruction (its pipe takes
-// a quarter of the lanes in a cycle, but all of a tile's conversions hide behind the
-// rest: 32 trees over 4096 tokens 151 us, 148 with none at all, 200 with the integer form).
-// bf16 has no such instruction: sign, exponent and mantissa are put in their
-// places, and a product, which is exact, makes up for the other bias, subnormal values
-// too.  That takes NaN (all ones but for the sign) for 480: put_nan.
-template <typename T> __device__ __forceinline__ void widen4(uint32_t u, uint32_t &a, uint32_t &b) {
-    if constexpr (std::is_same<T, __half>::value) {
-        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-            "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}\n"
-            : "=r"(a), "=r"(b)
-            : "r"(u));
-    } else {
-        const uint32_t x = __byte_perm(u, 0, 0x1404), y = __byte_perm(u, 0, 0x3424);  // to the upper bytes
-        a = (x & 0x80008000u) | (x & 0x7fff7fffu) >> 4;
-        b = (y & 0x80008000u) | (y & 0x7fff7fffu) >> 4;
-        asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(0x7B807B80u));  // 2^120
-        asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(b) : "r"(0x7B807B80u));
-    }
-}
-template <typename T> __device__ __forceinline__ void widen16(const uint4 &v, uint4 &lo, uint4 &hi) {
-    widen4<T>(v.x, lo.x, lo.y);
-    widen4<T>(v.y, lo.z, lo.w);
-    widen4<T>(v.z, hi.x, hi.y);
-    widen4<T>(v.w, hi.z, hi.w);
-}
-__device__ __forceinline__ uint32_t e4m3_nan(uint32_t u) {  // the bytes that are no numbers: their top bits
-    return ((u & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-}
-__device__ __forceinline__ uint32_t e4m3_nan(const uint4 &v) {
-    return e4m3_nan(v.x) | e4m3_nan(v.y) | e4m3_nan(v.z) | e4m3_nan(v.w);
-}
-__device__ __forceinline__ void put_nan(uint32_t u, uint32_t &a, uint32_t &b) {
-    const uint32_t n = e4m3_nan(u);
-    a |= ((n >> 7 & 1u) | (n >> 15 & 1u) << 16) * 0x7fffu;
-    b |= ((n >> 23 & 1u) | (n >> 31) << 16) * 0x7fffu;
+// Four e4m3 values as f16, exactly (NaN stays NaN).  The conversion's pipe takes a quarter of the
+// lanes in a cycle, but all of a tile's hide behind the rest: 32 trees over 4096 tokens
+// took 151 us, 148 with no conversions at all, 200 with bits moved by integer instructions.
+__device__ __forceinline__ void widen4(uint32_t u, uint32_t &a, uint32_t &b) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}\n"
+        : "=r"(a), "=r"(b)
+        : "r"(u));
 }
 
 // Row r of an item's row tile: its token (~token for a padding row) and query head.
@@ -397,7 +388,9 @@ template <typename T, int RT, bool KV8>
 __global__ void __launch_bounds__(Shape<RT, KV8>::kThreads, Shape<RT, KV8>::kPerSm)
     sgmv_tree_mma_kernel(const __grid_constant__ MmaParams P) {
     using S = Shape<RT, KV8>;
-    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    using M = std::conditional_t<KV8, __half, T>;  // of the products' operands
+    constexpr bool kBf16 = std::is_same<M, __nv_bfloat16>::value;
+    constexpr bool kTurnQ = !std::is_same<M, T>::value;  // q is converted as well
     const sgmv_tree_attention_args &a = P.a;
     extern __shared__ __align__(128) uint8_t dsm[];
     __shared__ __align__(8) uint64_t full[S::kStages], empty[S::kStages], q_full[S::kQ], q_empty[S::kQ];
@@ -421,7 +414,7 @@ __global__ void __launch_bounds__(Shape<RT, KV8>::kThreads, Shape<RT, KV8>::kPer
         if (lane == 0) {
             for (int i = 0; i < S::kStages; ++i)
                 mbar_init(&full[i], KV8 ? S::kConverters / 32 : P.box ? kLoaders / 32 : kLoaders), mbar_init(&empty[i], 1);
-            for (int i = 0; i < S::kQ; ++i) mbar_init(&q_full[i], P.q_box ? 1 : 32), mbar_init(&q_empty[i], 1);
+            for (int i = 0; i < S::kQ; ++i) mbar_init(&q_full[i], !kTurnQ && P.q_box ? 1 : 32), mbar_init(&q_empty[i], 1);
             for (int i = 0; i < kSegs; ++i) {
                 mbar_init(&seg_full[i], 1);
                 mbar_init(&seg_empty[i], 2 + (kLoaders + S::kConverters) / 32);  // MMA, softmax, loaders, converters
@@ -452,7 +445,7 @@ __global__ void __launch_bounds__(Shape<RT, KV8>::kThreads, Shape<RT, KV8>::kPer
     if (KV8 ? P.tok < kTok || a.D % 64 != 0 : P.tok < kTok)
         for (uint32_t i = tid * 16u; i < S::kOffQ; i += S::kThreads * 16u)
             sts128(sm + i, make_uint4(0, 0, 0, 0));
-    if (a.D % 64 != 0 && !(P.box && P.q_box))
+    if (a.D % 64 != 0 && (kTurnQ || !(P.box && P.q_box)))
         for (uint32_t i = (KV8 || P.box ? S::kOffQ : 0u) + tid * 16u; i < S::kOffP; i += S::kThreads * 16u)
             sts128(sm + i, make_uint4(0, 0, 0, 0));
     fence_proxy_async();
@@ -601,6 +594,54 @@ __global__ void __launch_bounds__(Shape<RT, KV8>::kThreads, Shape<RT, KV8>::kPer
             uint8_t *const qs = sm + S::kOffQ + (uint32_t)qb * S::kQBytes;
             int2 *const place = reinterpret_cast<int2 *>(sm + S::kOffRow) + (i % kSegs) * RT;
             auto bring_q = [&]() {
+                if constexpr (kTurnQ) {
+                    // two rows at a time, 16 lanes each, eight such steps' loads under way
+                    float *const factor = reinterpret_cast<float *>(sm + S::kOffScale) + (i % kSegs) * RT;
+                    const float c = P.c * s_seg[i % kSegs].k_scale;
+                    const int col = lane & 15;
+                    constexpr int kSteps = RT / 2 < 8 ? RT / 2 : 8;
+#pragma unroll 1
+                    for (int m0 = 0; m0 < RT; m0 += 2 * kSteps) {
+                        uint4 u[kSteps];
+#pragma unroll
+                        for (int e = 0; e < kSteps; ++e) {
+                            const int2 at = place[min(m0 + 2 * e + (lane >> 4), R - 1)];
+                            u[e] = *reinterpret_cast<const uint4 *>(
+                                static_cast<const T *>(a.q) + (int64_t)(at.x < 0 ? ~at.x : at.x) * a.q_token +
+                                (int64_t)at.y * a.q_head + min(col, cpr - 1) * 8);
+                        }
+#pragma unroll
+                        for (int e = 0; e < kSteps; ++e) {
+                            const int m = m0 + 2 * e + (lane >> 4);
+                            uint32_t *const w = reinterpret_cast<uint32_t *>(&u[e]);
+                            uint32_t top = 0;  // the largest finite magnitude's bits
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const uint32_t lo = w[q] & 0x7fffu, hi = w[q] >> 16 & 0x7fffu;
+                                top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+                            }
+#pragma unroll
+                            for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                            // times 2^(14 - its exponent): below 2^15
+                            const int up = min(max(268 - (int)(top >> 7), 1), 253);
+                            const float f = __int_as_float(up << 23);
+                            uint32_t h[4];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                float x, y;
+                                unpack2<T>(w[q], x, y);
+                                h[q] = m < R ? pack2<M>(x * f, y * f) : 0u;
+                            }
+                            if (col < cpr)
+                                sts128(qs + (col >> 3) * (S::kN * 128u) + sw128_offset(m, col & 7),
+                                       make_uint4(h[0], h[1], h[2], h[3]));
+                            if (col == 0) factor[m] = c * __int_as_float((254 - up) << 23);
+                        }
+                    }
+                    fence_proxy_async();
+                    mbar_arrive(&q_full[qb]);
+                    return;
+                }
                 if (P.q_box) {
                     // (rows past R are the next sequence's or zeros: finite or not,
                     // they end in columns of the products that nobody reads)
@@ -627,12 +668,12 @@ __global__ void __launch_bounds__(Shape<RT, KV8>::kThreads, Shape<RT, KV8>::kPer
                 }
                 cp_async_arrive(&q_full[qb]);
             };
-            if (i < S::kQ && P.q_box) bring_q();
-            else if (P.q_box && lane < halves)  // its buffer is in use: as far as L2
+            if (!kTurnQ && i < S::kQ && P.q_box) bring_q();
+            else if (!kTurnQ && P.q_box && lane < halves)  // its buffer is in use: as far as L2
                 tma_prefetch_3d(&P.map_q, lane * 64, h * group, q.t0 + rt * RT / group);
             for (int r = lane; r < R; r += 32) place[r] = row_place(P, q.t0, h, rt * RT + r);
             __syncwarp();
-            if (i < S::kQ && !P.q_box) bring_q();
+            if (i < S::kQ && (kTurnQ || !P.q_box)) bring_q();
             if (build) {
                 // see[j]: the rows that see tree node j.  Every node of this row
                 // tile marks itself and its ancestors with its rows' bits.
@@ -675,15 +716,27 @@ __global__ void __launch_bounds__(Shape<RT, KV8>::kThreads, Shape<RT, KV8>::kPer
         if constexpr (KV8) {
             const int cw = warp - kWalkWarp - kLoaders / 32 - 1, pieces = D / 16;
             constexpr int kChunks = 8;  // 16-byte chunks per lane and operand, at most
-            // a warp has 32 tokens of every tile, which lie D bytes apart; where a lane's
-            // chunks go: the second half's in the other order, so that eight lanes write
-            // to eight different groups of banks
-            const uint32_t from = S::kOffRaw + (uint32_t)(cw * 32 * pieces + lane) * 16u;
+            // A warp has 32 tokens of every tile, which lie D bytes apart.  Which chunks are a
+            // lane's: eight lanes are to touch eight different groups of banks when they read, and
+            // when they write.  kCross: they have the first half of an even row and the second
+            // of the next, or the other halves of the two (with 128 columns).  Else they have a
+            // row, and those with the second half write their two pieces in the other order.
+            // (32 and 64 rows: 8 trees of 4 and 8 nodes, 64 heads on 8, 101 and 117 us crossed, 104 and 131 in
+            // rows; 16 and 128 rows, where registers are short: 159 and 451 crossed, 150 and
+            // 430 in rows, on 32 trees over 4096 tokens and 8 trees of 64 nodes.)
+            constexpr bool kCross = RT == 32 || RT == 64;
+            const bool cross = kCross && pieces == kChunks;
+            const int pair = lane >> 2 & 1, other = (lane >> 3 & 1) ^ pair;
+            const uint32_t from = S::kOffRaw + (uint32_t)cw * 32u * (uint32_t)D +
+                                  (cross ? (uint32_t)((2 * (lane >> 4) + pair) * 128 + other * 64 + (lane & 3) * 16)
+                                         : (uint32_t)lane * 16u);
             uint32_t to[kChunks];
 #pragma unroll
             for (int i = 0; i < kChunks; ++i) {
-                const int e = lane + 32 * i, m = e / pieces, c = e - m * pieces, odd = c >> 2;
-                to[i] = (uint32_t)odd * kHalf + sw128_offset(cw * 32 + m, (2 * c + odd) & 7);
+                const int e = lane + 32 * i;
+                const int m = cross ? 4 * i + 2 * (lane >> 4) + pair : e / pieces;
+                const int c = cross ? other * 4 + (lane & 3) : e - m * pieces, odd = kCross ? 0 : c >> 2;
+                to[i] = (uint32_t)(c >> 2) * kHalf + sw128_offset(cw * 32 + m, (2 * c + odd) & 7);
             }
             int n = 0, st = 0, slot = 0;
             uint32_t ph = 1, raw_ph = 0;
@@ -701,7 +754,6 @@ __global__ void __launch_bounds__(Shape<RT, KV8>::kThreads, Shape<RT, KV8>::kPer
                     const uint8_t *const src = sm + from + (uint32_t)slot * (kStage / 2);
                     uint8_t *const dst = sm + (uint32_t)st * kStage;
                     uint4 v[kChunks];
-                    uint32_t nan = 0;
 #pragma unroll
                     for (int e = 0; e < kChunks; ++e)
                         if (e < pieces) v[e] = lds128(src + e * 512);
@@ -709,31 +761,14 @@ __global__ void __launch_bounds__(Shape<RT, KV8>::kThreads, Shape<RT, KV8>::kPer
                     for (int e = 0; e < kChunks; ++e)
                         if (e < pieces) {
                             uint4 lo, hi;
-                            widen16<T>(v[e], lo, hi);
-                            if (!std::is_same<T, __half>::value) nan |= e4m3_nan(v[e]);
-                            const bool odd = to[e] >= kHalf;
+                            widen4(v[e].x, lo.x, lo.y);
+                            widen4(v[e].y, lo.z, lo.w);
+                            widen4(v[e].z, hi.x, hi.y);
+                            widen4(v[e].w, hi.z, hi.w);
+                            const bool odd = !kCross && to[e] >= kHalf;
                             sts128(dst + to[e], odd ? hi : lo);
                             sts128(dst + (to[e] ^ 16u), odd ? lo : hi);
                         }
-                    // (once per operand: a branch per chunk cost 64 heads over 32768
-                    // tokens 150 of 580 us)
-                    if (nan) {
-#pragma unroll 1
-                        for (int e = 0; e < pieces; ++e) {
-                            const uint4 u = lds128(src + e * 512);
-                            if (!e4m3_nan(u)) continue;
-                            uint4 lo, hi;
-                            widen16<T>(u, lo, hi);
-                            put_nan(u.x, lo.x, lo.y);
-                            put_nan(u.y, lo.z, lo.w);
-                            put_nan(u.z, hi.x, hi.y);
-                            put_nan(u.w, hi.z, hi.w);
-                            const int k = lane + 32 * e, m = k / pieces, c = k - m * pieces;
-                            uint8_t *const half = dst + (uint32_t)(c >> 2) * kHalf;
-                            sts128(half + sw128_offset(cw * 32 + m, (2 * c) & 7), lo);
-                            sts128(half + sw128_offset(cw * 32 + m, (2 * c + 1) & 7), hi);
-                        }
-                    }
                     fence_proxy_async();
                     __syncwarp();
                     if (lane == 0) {
@@ -939,7 +974,7 @@ __global__ void __launch_bounds__(Shape<RT, KV8>::kThreads, Shape<RT, KV8>::kPer
             }
             --left;
             // cp.async (generic proxy) data -> tensor core (async proxy)
-            if ((first && !P.q_box) || (!KV8 && !P.box)) fence_proxy_async();
+            if ((first && (kTurnQ || !P.q_box)) || (!KV8 && !P.box)) fence_proxy_async();
             tc_fence_after();
             const uint64_t kd = k_desc + (uint32_t)k_st * (kStage >> 4);
             const uint64_t qd = q_desc + (uint32_t)qb * (S::kQBytes >> 4);
@@ -967,7 +1002,7 @@ __global__ void __launch_bounds__(Shape<RT, KV8>::kThreads, Shape<RT, KV8>::kPer
             for (int t = 0; t < tiles; ++t, ++g) {
                 // A tile ahead; but with one Q buffer the next segment's first scores
                 // wait for its Q, and must not hold up this segment's last product.
-                if (S::kQ > 1 || t + 1 < tiles) scores(g + 1);  // nothing at the end
+                if (S::kAhead && (S::kQ > 1 || t + 1 < tiles)) scores(g + 1);  // nothing at the end
                 if (stop || !await(&full[v_st], v_ph, lost) || !await(&p_full, (uint32_t)g & 1, lost)) {
                     stop = true;
                     break;
@@ -981,7 +1016,7 @@ __global__ void __launch_bounds__(Shape<RT, KV8>::kThreads, Shape<RT, KV8>::kPer
                 commit_on(on, &empty[v_st]);
                 commit_on(on, &pv_done);
                 skip(v_st, v_ph);
-                if (S::kQ == 1 && t + 1 == tiles) scores(g + 1);
+                if (!S::kAhead || (S::kQ == 1 && t + 1 == tiles)) scores(g + 1);
             }
             if (lane == 0 && !stop) mbar_arrive(&seg_empty[i % kSegs]);
             __syncwarp();
@@ -1034,6 +1069,7 @@ __global__ void __launch_bounds__(Shape<RT, KV8>::kThreads, Shape<RT, KV8>::kPer
             if (end == 0) break;
             const int R = min(RT, cur.n * group - cur.rt * RT);  // rows in use
             const float c = KV8 ? P.c * cur.k_scale : P.c;
+            const float *const row_c = reinterpret_cast<const float *>(sm + S::kOffScale) + (seg % kSegs) * RT + r0;
             const uint32_t *const see = reinterpret_cast<const uint32_t *>(sm + S::kOffSee) +
                                         cur.see * SGMV_TREE_MAX_NODES * S::kWords + wg;
             bool aux = false;  // the walk's tables for this segment are known to be there
@@ -1063,8 +1099,8 @@ __global__ void __launch_bounds__(Shape<RT, KV8>::kThreads, Shape<RT, KV8>::kPer
                         bool any = false;
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            if (bad16<T>(x[q])) any = true, x[q] &= 0xffff0000u;
-                            if (bad16<T>(x[q] >> 16)) any = true, x[q] &= 0xffffu;
+                            if (bad16<M>(x[q])) any = true, x[q] &= 0xffff0000u;
+                            if (bad16<M>(x[q] >> 16)) any = true, x[q] &= 0xffffu;
                         }
                         if (any) {
                             s_poison = seg;
@@ -1091,8 +1127,14 @@ __global__ void __launch_bounds__(Shape<RT, KV8>::kThreads, Shape<RT, KV8>::kPer
 #pragma unroll
                     for (int i = 0; i < S::kRows; i += 4) {
                         const uint4 u = lds128(&s_ref[r0 + i]);
-                        fma_pair(s[i], s[i + 1], c, __uint_as_float(u.x), __uint_as_float(u.y));
-                        fma_pair(s[i + 2], s[i + 3], c, __uint_as_float(u.z), __uint_as_float(u.w));
+                        if constexpr (kTurnQ) {
+                            const uint4 f = lds128(row_c + i);
+                            fma_pair(s[i], s[i + 1], f.x, f.y, __uint_as_float(u.x), __uint_as_float(u.y));
+                            fma_pair(s[i + 2], s[i + 3], f.z, f.w, __uint_as_float(u.z), __uint_as_float(u.w));
+                        } else {
+                            fma_pair(s[i], s[i + 1], c, __uint_as_float(u.x), __uint_as_float(u.y));
+                            fma_pair(s[i + 2], s[i + 3], c, __uint_as_float(u.z), __uint_as_float(u.w));
+                        }
                     }
                     if (edge) {
 #pragma unroll
@@ -1116,7 +1158,7 @@ __global__ void __launch_bounds__(Shape<RT, KV8>::kThreads, Shape<RT, KV8>::kPer
                     // new references: the larger of the old and this tile's maximum
                     tmem_load(ts, s);
 #pragma unroll
-                    for (int i = 0; i < S::kRows; ++i) s[i] = !edge || (vis >> i & 1u) ? s[i] * c : -INFINITY;
+                    for (int i = 0; i < S::kRows; ++i) s[i] = !edge || (vis >> i & 1u) ? s[i] * (kTurnQ ? ldsf(row_c + i) : c) : -INFINITY;
                     const int row = warp_rows<true>(s, lane);
                     s_red[warp & 3][r0 + row] = s[0];
                     group_bar(wg);
@@ -1149,7 +1191,7 @@ __global__ void __launch_bounds__(Shape<RT, KV8>::kThreads, Shape<RT, KV8>::kPer
 #pragma unroll
                 for (int i = 0; i < S::kRows; i += 2) {
                     add_pair(l[i], l[i + 1], s[i], s[i + 1]);
-                    p[i / 2] = pack2<T>(s[i], s[i + 1]);
+                    p[i / 2] = pack2<M>(s[i], s[i + 1]);
                 }
                 // the previous tile's P has been read
                 if (g > 0) pv_finished(g - 1);
@@ -1264,7 +1306,7 @@ __global__ void __launch_bounds__(Shape<RT, KV8>::kThreads, Shape<RT, KV8>::kPer
         for (int r = tid; r < 2 * RT; r += S::kThreads)
             *reinterpret_cast<float2 *>(P.ml + ((int64_t)blockIdx.x * 2 * RT + r) * 2) = make_float2(kUnset, -1.f);
         // copies under way land while this shared memory is the CTA's
-        if (P.q_box && warp == kWalkWarp)
+        if (!kTurnQ && P.q_box && warp == kWalkWarp)
             for (int i = max(0, issued - S::kQ); i < issued; ++i)
                 if (!mbar_wait(&q_full[i % S::kQ], (uint32_t)(i / S::kQ) & 1)) break;
         constexpr int kRing = KV8 ? S::kRaw : S::kStages;
@@ -1352,7 +1394,9 @@ __global__ void __launch_bounds__(kJoinThreads, 4) sgmv_tree_join_kernel(const _
 template <typename T, int RT, bool KV8>
 int launch(const MmaParams &p, int ctas, cudaStream_t stream) {
     using S = Shape<RT, KV8>;
-    static_assert((S::kBytes + 4096) * S::kPerSm <= 227 * 1024, "shared memory");
+    // (3 KB of static shared memory, 6 with one CTA, and the 1 KB that each CTA takes besides)
+    static_assert(S::kPerSm > 1 ? (S::kBytes + 4096) * S::kPerSm <= 228 * 1024 : S::kBytes + 7168 <= 228 * 1024,
+                  "shared memory");
     const cudaError_t e = cudaFuncSetAttribute(sgmv_tree_mma_kernel<T, RT, KV8>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)S::kBytes);
