@@ -11,10 +11,15 @@ moves the accepted tokens' keys and values to their places:
     sgmv_rope                    rotary positions, k and v appended to the paged cache
     sgmv_tree_attention          every row over its context and its ancestors
     sgmv_apply                   the adapter of o
+    sgmv_sample                  the target distributions, filtered
     sgmv_tree_verify             which drafted tokens are accepted
     sgmv_cache_commit            their keys and values, all layers at once
 
-    python examples/speculative_decode.py [tokens]
+With Model(head_norms=True) q and k are normalised per head (sgmv_norm_rope in
+place of sgmv_rope), with Model(e4m3=True) the cache holds 8-bit values
+(sgmv_quant_attention in place of sgmv_tree_attention).
+
+    python examples/speculative_decode.py [tokens [8bit]]
 """
 import os
 import sys
@@ -41,6 +46,12 @@ class Model:
     adapters: int = 4
     seed: int = 0
     dtype: torch.dtype = torch.float16
+    head_norms: bool = False
+    e4m3: bool = False
+    temperature: float = 1.0
+    top_k: int = 0
+    top_p: float = 1.0
+    min_p: float = 0.0
     w: dict = field(default_factory=dict)
 
     def __post_init__(self):
@@ -55,7 +66,12 @@ class Model:
         self.base = [[rand(H, H, std=H ** -0.5) for _ in range(4)] for _ in range(self.layers)]
         self.A = [[rand(L, H, r, std=H ** -0.5) for _ in range(4)] for _ in range(self.layers)]
         self.B = [[rand(L, r, H, std=r ** -0.5) for _ in range(4)] for _ in range(self.layers)]
-        self.inv_freq = sgmv.sgmv_rope_frequencies(H // self.heads // 2)
+        D = H // self.heads
+        self.inv_freq = sgmv.sgmv_rope_frequencies(D // 2)
+        self.norms = [[(1 + rand(D, std=0.2)).to(self.dtype) for _ in range(2)] if self.head_norms else [None, None]
+                      for _ in range(self.layers)]
+        # what the cache's values are multiples of: some six deviations of k and v reach the largest
+        self.scale = torch.full((self.heads,), 6 / 448, device="cuda") if self.e4m3 else None
 
 
 class Requests:
@@ -68,7 +84,7 @@ class Requests:
         self.bs = block_size
         self.table = torch.randperm(batch * pages, generator=g).to(torch.int32).view(batch, pages).cuda()
         shape = (model.layers, batch * pages, block_size, model.heads, D)
-        self.k = torch.empty(shape, dtype=model.dtype, device="cuda")
+        self.k = torch.empty(shape, dtype=torch.float8_e4m3fn if model.e4m3 else model.dtype, device="cuda")
         self.v = torch.empty_like(self.k)
         self.lens = torch.zeros(batch, dtype=torch.int32, device="cuda")
         self.last = torch.randint(0, model.vocab, (batch,), generator=g).to(torch.int32).cuda()
@@ -110,9 +126,18 @@ def step(model, req, parents=PARENTS, depth=DEPTH, tokens=None, greedy=False):
         qkv = [h @ W[i] for i in range(3)]
         sgmv.sgmv_apply_multi(qkv, [h] * 3, A[:3], Bm[:3], seg_ptr, idx, 0.5, perm=perm)
         q, k, v = (t.view(T, heads, D) for t in qkv)
-        sgmv.sgmv_rope(q, k, positions, model.inv_freq, v=v, k_cache=req.k[layer], v_cache=req.v[layer], slots=slots)
+        cache = dict(v=v, k_cache=req.k[layer], v_cache=req.v[layer], slots=slots)
+        if model.head_norms or model.e4m3:
+            sgmv.sgmv_norm_rope(q, k, positions, model.inv_freq, *model.norms[layer], k_scale=model.scale,
+                                v_scale=model.scale, **cache)
+        else:
+            sgmv.sgmv_rope(q, k, positions, model.inv_freq, **cache)
         attn = torch.empty_like(q)
-        sgmv.sgmv_tree_attention(attn, q, req.k[layer], req.v[layer], req.table, req.lens, tree_ptr, par)
+        if model.e4m3:
+            sgmv.sgmv_quant_attention(attn, q, req.k[layer], req.v[layer], model.scale, model.scale, req.table,
+                                      req.lens, tree_ptr, par)
+        else:
+            sgmv.sgmv_tree_attention(attn, q, req.k[layer], req.v[layer], req.table, req.lens, tree_ptr, par)
         attn = attn.view(T, H)
         y = attn @ W[3]
         sgmv.sgmv_apply(y, attn, A[3], Bm[3], seg_ptr, idx, 0.5, perm=perm)
@@ -121,7 +146,8 @@ def step(model, req, parents=PARENTS, depth=DEPTH, tokens=None, greedy=False):
     if greedy:
         target = torch.zeros_like(logits).scatter_(1, logits.argmax(-1, keepdim=True), 1.0)
     else:
-        target = torch.softmax(logits, -1)
+        target = torch.empty_like(logits)
+        sgmv.sgmv_sample(logits, None, model.temperature, model.top_k, model.top_p, model.min_p, probs=target)
     u = torch.rand(T + B, generator=req.random, device="cuda")
     count, path, token = sgmv.sgmv_tree_verify(target, None, tokens.view(-1), par, tree_ptr, u[:T], u[T:], n)
     sgmv.sgmv_cache_commit(req.k, req.v, req.table, req.lens, path, count)
@@ -147,7 +173,8 @@ def generate(model, req, length, parents=PARENTS, depth=DEPTH, greedy=False, tok
 
 def main():
     steps = int(sys.argv[1]) if len(sys.argv) > 1 else 32
-    model = Model()
+    eight = "8bit" in sys.argv[2:]
+    model = Model(head_norms=eight, e4m3=eight)
     # a step adds up to three tokens to a request, and one at least to the slowest
     req = Requests(model, batch=8, longest=max(1024, (max(DEPTH) + 1) * steps + len(PARENTS)))
     out, took = generate(model, req, steps)

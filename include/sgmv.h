@@ -571,7 +571,7 @@ int sgmv_cache_commit(const sgmv_cache_commit_args *args, void *stream);
  * with v beside it: to q's type if k_scale and v_scale are NULL, else to e4m3.
  * `rope` is as for sgmv_rope, with inverse = 0; its caches are of the type just
  * said.  Squares are summed in fp32, and so must not pass its range (3.4e38).  eps > 0.
- * T * (Hq + 2 Hk) below 2^31 (SGMV_ERR_UNSUPPORTED).
+ * T * (Hq + 2 Hk) up to 2^30 (SGMV_ERR_UNSUPPORTED beyond).
  */
 typedef struct {
     sgmv_rope_args rope;
@@ -589,7 +589,7 @@ int sgmv_norm_rope(const sgmv_norm_rope_args *args, void *stream);
  *   dx = r (h - r^2 x mean(h * x)),   dw = sum over rows and heads of g * r x
  * (dx = g for a tensor without a weight).  q, k, dq_out, dk_out, dq, dk [T][heads][D]
  * of any token and head strides, dq and dk apart from the inputs; q or k may be
- * left out (Hq or Hk = 0), and is not read without its weight.  dq_weight, dk_weight fp32 [D], written
+ * left out (Hq or Hk = 0), and is not read without its weight; T * (Hq + Hk) up to 2^30.  dq_weight, dk_weight fp32 [D], written
  * (not added to); given exactly where the weight is.  Sums are fp32, joined in fp64 in a fixed order:
  * the same result in every run.
  *   workspace: sgmv_norm_rope_grad_workspace_bytes(D) bytes, 16-byte aligned; what it
@@ -620,10 +620,11 @@ int sgmv_norm_rope_grad(const sgmv_norm_rope_grad_args *args, void *stream);
 
 /*
  * sgmv_tree_attention over an e4m3 cache: out = v_scale[h] softmax(scale *
- * k_scale[h] * q K^T) V, with K and V as stored (they are converted to q's type,
- * exactly, for the products).  `attention` is as there, its caches of e4m3; D a
- * multiple of 16, at most 128 (SGMV_ERR_UNSUPPORTED beyond).  Masks, padding, lse and
- * values that are no numbers as there.
+ * k_scale[h] * q K^T) V, with K and V as stored.  `attention` is as there, its caches
+ * of e4m3; D a multiple of 16, at most 128 (SGMV_ERR_UNSUPPORTED beyond).  Masks, padding,
+ * lse and values that are no numbers as there.  The products' operands are f16: K and V
+ * exactly; queries of bf16 too, a row at a time by a power of two (a value loses 2^-39 of its
+ * row's largest at most); the weights rounded to f16, the output to q's type.
  */
 typedef struct {
     sgmv_tree_attention_args attention;
@@ -654,7 +655,7 @@ int sgmv_quant_attention(const sgmv_quant_attention_args *args, void *stream);
  *     temperature_all, ... hold for every row
  *   u fp32 [T], token int32 [T]: both or neither; probs fp32 [T][V], or NULL
  *   logits_row, probs_row: elements between rows; logits aligned to its type
- * V up to 2^24 (SGMV_ERR_UNSUPPORTED beyond).
+ * probs must not overlap logits.  V up to 2^24, T to 2^27 (SGMV_ERR_UNSUPPORTED beyond).
  */
 typedef struct {
     const void *logits;
@@ -698,7 +699,7 @@ int sgmv_read_floor(const void *src, size_t bytes, int32_t T, int32_t L, int32_t
  * the device error word, the chunk is then awaited with the full limit (so
  * the kernel still ends normally, with every copy landed) and the thread
  * writes no y.  Launches of the tree attention for heads of up to 128 columns
- * take theirs in one role of each CTA, given by the value: 1 the walk along
+ * (and of sgmv_quant_attention) take theirs in one role of each CTA, given by the value: 1 the walk along
  * the work, 2 the loading of K and V, 3 the matrix products, 4 the softmax;
  * the status is the same, and the call writes no output.  Other kernels are
  * unaffected.  Returns SGMV_OK.

@@ -40,11 +40,13 @@ struct NormParams {
     sgmv_norm_rope_args a;
     uint64_t turns[kRopeMaxPairs];
     int32_t rot, uph;  // lanes of a group whose columns turn, lanes with columns
+    float inv_d;
 };
 struct GradParams {
     sgmv_norm_rope_grad_args a;
     uint64_t turns[kRopeMaxPairs];
     int32_t rot, uph;
+    float inv_d;
     int32_t ctas_q;  // CTAs with rows of q; the others have rows of k
     float *part;     // [CTA][D]
 };
@@ -59,6 +61,14 @@ template <int MODE> struct Columns {
         c = MODE == kInterleaved ? w * 16 : MODE == kHalves && !turns ? (w - rot) * 8 + 2 * pairs : w * 8;
         d = MODE == kInterleaved ? c + 8 : c + pairs;
         second = here && (MODE == kInterleaved ? d < D : MODE == kHalves && turns);
+    }
+    // What was read as the second vector: zeros, if an interleaved lane has none.
+    __device__ __forceinline__ uint4 rest(const uint4 &v) const {
+        return MODE == kInterleaved && !second ? make_uint4(0, 0, 0, 0) : v;
+    }
+    // The sum of the lane's own columns, from those of x and y (see Lane).
+    __device__ __forceinline__ float own(float2 x, float2 y) const {
+        return !here ? 0.f : MODE == kInterleaved || second ? (x.x + x.y) + (y.x + y.y) : x.x + x.y;
     }
 };
 
@@ -87,65 +97,127 @@ template <int G> __device__ __forceinline__ float group_sum(float v) {
     return v;
 }
 
-// Angles (cosine, sine times scale) of tokens t0 ... of one chunk.
-__device__ __forceinline__ void chunk_angles(float2 (*s_angle)[kRopeMaxPairs], const int32_t *positions,
-                                             const uint64_t *turns, int64_t t0, int n, int pairs, float scale) {
+// Two fp32 operations in one instruction, each rounded as alone: these kernels are bound by
+// their instructions as much as by memory.
+__device__ __forceinline__ uint64_t bits2(float2 a) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a.x), "f"(a.y));
+    return v;
+}
+__device__ __forceinline__ float2 floats2(uint64_t v) {
+    float2 a;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(v));
+    return a;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t v;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(bits2(a)), "l"(bits2(b)));
+    return floats2(v);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t v;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+    return floats2(v);
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+__device__ __forceinline__ float2 minus(float2 a) { return make_float2(-a.x, -a.y); }
+
+// A lane's columns in fp32: x and y are partners.  kHalves: its two vectors; kInterleaved: the
+// first and the second columns of its eight pairs; kGather: its vector, and the partners.
+struct Lane {
+    float2 x[4], y[4];
+};
+template <typename T, int MODE> __device__ __forceinline__ void spread(const uint4 &u, const uint4 &v, Lane &l) {
+    const uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (MODE == kInterleaved) {
+            unpack2<T>(w[2 * i], l.x[i].x, l.y[i].x);
+            unpack2<T>(w[2 * i + 1], l.x[i].y, l.y[i].y);
+        } else {
+            unpack2<T>(w[i], l.x[i].x, l.x[i].y);
+            unpack2<T>(w[4 + i], l.y[i].x, l.y[i].y);
+        }
+    }
+}
+// Values j of the two vectors, in the columns' order.
+template <int MODE> __device__ __forceinline__ float2 two_of(const Lane &l, int j) {
+    if (MODE != kInterleaved) return j < 4 ? l.x[j] : l.y[j - 4];
+    return j & 1 ? make_float2(l.x[j / 2].y, l.y[j / 2].y) : make_float2(l.x[j / 2].x, l.y[j / 2].x);
+}
+template <typename T, int MODE> __device__ __forceinline__ uint4 vector_of(const Lane &l, int which) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 v = two_of<MODE>(l, 4 * which + j);
+        w[j] = pack2<T>(v.x, v.y);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// Eight values of e4m3: beyond 448 the largest, NaN as NaN.
+template <int MODE> __device__ __forceinline__ uint2 bytes_of(const Lane &l, int which) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = __nv_cvt_float2_to_fp8x2(two_of<MODE>(l, 4 * which + j), __NV_SATFINITE, __NV_E4M3);
+    return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+}
+
+// The angles of kChunk tokens, scale included.
+struct Angles {
+    float c[kChunk][kRopeMaxPairs], s[kChunk][kRopeMaxPairs];
+};
+__device__ __forceinline__ void chunk_angles(Angles &to, const int32_t *positions, const uint64_t *turns, int64_t t0,
+                                             int n, int pairs, float scale) {
     for (int e = threadIdx.x; e < n * pairs; e += kNormThreads) {
         const int k = e / pairs, i = e - k * pairs;
         const float2 cs = rotary_angle(turns[i], positions[t0 + k]);
-        s_angle[k][i] = make_float2(cs.x * scale, cs.y * scale);
+        to.c[k][i] = cs.x * scale;
+        to.s[k][i] = cs.y * scale;
     }
 }
 
-// Turns the lane's columns x (and y, kHalves) by the angles of its token, or back.
-// partner: of kGather, the columns' partners.
+// Turns the lane's columns by the angles of its token, or back.
 template <int MODE, bool BACK>
-__device__ __forceinline__ void turn(const Columns<MODE> &col, const float2 *angle, int pairs, float (&x)[8],
-                                     float (&y)[8]) {
-    if (MODE == kHalves) {
-        if (!col.turns) return;
-        const float4 *const at = reinterpret_cast<const float4 *>(angle + col.c);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float4 u = at[i];
-            const float c0 = u.x, s0 = BACK ? -u.y : u.y, c1 = u.z, s1 = BACK ? -u.w : u.w;
-            const float a = x[2 * i], b = x[2 * i + 1];
-            x[2 * i] = a * c0 - y[2 * i] * s0;
-            y[2 * i] = a * s0 + y[2 * i] * c0;
-            x[2 * i + 1] = b * c1 - y[2 * i + 1] * s1;
-            y[2 * i + 1] = b * s1 + y[2 * i + 1] * c1;
-        }
-    } else if (MODE == kInterleaved) {
-        const float4 *const at = reinterpret_cast<const float4 *>(angle + col.c / 2);
-        auto two = [](float4 u, float (&z)[8], int i, bool last) {
-            const float s0 = BACK ? -u.y : u.y, s1 = BACK ? -u.w : u.w;
-            const float a = z[4 * i], b = z[4 * i + 2];
-            z[4 * i] = a * u.x - z[4 * i + 1] * s0;
-            z[4 * i + 1] = a * s0 + z[4 * i + 1] * u.x;
-            if (last) return;
-            z[4 * i + 2] = b * u.z - z[4 * i + 3] * s1;
-            z[4 * i + 3] = b * s1 + z[4 * i + 3] * u.z;
-        };
-        if (col.c / 2 + 8 <= pairs) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) two(at[i], x, i, false), two(at[2 + i], y, i, false);
-        } else {  // columns behind the last pair stay
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int left = pairs - (col.c / 2 + 2 * i);
-                if (left > 0) two(at[i], x, i, left == 1);
-                if (left > 4) two(at[2 + i], y, i, left == 5);
-            }
-        }
-    } else {  // y: the partners
+__device__ __forceinline__ void turn(const Columns<MODE> &col, const Angles &angles, int token, int pairs, Lane &l) {
+    const float *const c = angles.c[token], *const s = angles.s[token];
+    if (MODE == kGather) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int j = col.c + i;
             if (j >= 2 * pairs) break;
             const bool second = j >= pairs;
-            const float2 u = angle[second ? j - pairs : j];
-            const float s = BACK != second ? u.y : -u.y;
-            x[i] = x[i] * u.x + y[i] * s;
+            const int k = second ? j - pairs : j;
+            float &x = i & 1 ? l.x[i / 2].y : l.x[i / 2].x;
+            const float y = i & 1 ? l.y[i / 2].y : l.y[i / 2].x;
+            x = x * c[k] + y * (BACK != second ? s[k] : -s[k]);
+        }
+        return;
+    }
+    const int first = MODE == kInterleaved ? col.c / 2 : col.c;  // of the lane's pairs
+    if (MODE == kHalves ? !col.turns : first + 8 > pairs) {
+        // (columns behind the last pair stay: the angle zero would make NaN of an infinity's partner)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (MODE == kInterleaved && first + i < pairs) {
+                float &x = i & 1 ? l.x[i / 2].y : l.x[i / 2].x, &y = i & 1 ? l.y[i / 2].y : l.y[i / 2].x;
+                const float cc = c[first + i], ss = BACK ? -s[first + i] : s[first + i], a = x;
+                x = a * cc - y * ss;
+                y = a * ss + y * cc;
+            }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float4 cc = *reinterpret_cast<const float4 *>(c + first + 4 * i);
+        const float4 ss = *reinterpret_cast<const float4 *>(s + first + 4 * i);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float2 c2 = e ? make_float2(cc.z, cc.w) : make_float2(cc.x, cc.y);
+            const float2 s0 = e ? make_float2(ss.z, ss.w) : make_float2(ss.x, ss.y);
+            const float2 s2 = BACK ? minus(s0) : s0;
+            const float2 a = l.x[2 * i + e], b = l.y[2 * i + e];
+            l.x[2 * i + e] = fma2(a, c2, minus(mul2(b, s2)));
+            l.y[2 * i + e] = fma2(a, s2, mul2(b, c2));
         }
     }
 }
@@ -154,22 +226,13 @@ __device__ __forceinline__ int partner_of(int j, int pairs) {
     return j < pairs ? j + pairs : j < 2 * pairs ? j - pairs : j;
 }
 
-// Eight fp32 values as 8 bytes of e4m3: beyond 448 the largest value, NaN as NaN.
-__device__ __forceinline__ uint2 pack_e4m3(const float (&v)[8], float f) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i] * f, v[2 * i + 1] * f), __NV_SATFINITE, __NV_E4M3);
-    return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
-}
-
 template <typename T, int MODE, int G, bool Q8>
 __global__ void __launch_bounds__(kNormThreads, kNormCtas)
     sgmv_norm_rope_kernel(const __grid_constant__ NormParams P, int *err) {
     const sgmv_rope_args &a = P.a.rope;
     constexpr int kGroups = kNormThreads / G;
     constexpr bool kTwo = MODE != kGather;
-    __shared__ __align__(16) float2 s_angles[2][kChunk][kRopeMaxPairs];
+    __shared__ __align__(16) Angles s_angles[2];
     const int g = threadIdx.x / G, pairs = a.pairs;
     const Columns<MODE> col(threadIdx.x % G, P.rot, P.uph, pairs, a.D);
     const bool append = a.k_cache != nullptr;
@@ -209,7 +272,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormCtas)
         m.slot = slots[m.t];
     };
     // the weights of this lane's columns
-    uint4 wq[2], wk[2];
+    uint4 wq[2] = {}, wk[2] = {};
     auto weights = [&](const void *w, uint4 (&to)[2]) {
         if (!w || !col.here) return;
         const T *const src = static_cast<const T *>(w);
@@ -240,40 +303,32 @@ __global__ void __launch_bounds__(kNormThreads, kNormCtas)
             fetch(after < c1 ? after : c1 + g, next);
             if (!__any_sync(0xffffffffu, mine)) continue;
             const bool is_v = mine && m.h >= a.Hq + a.Hk, is_k = mine && m.h >= a.Hq && !is_v;
-            float x[8], y[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = y[e] = 0.f;
-            if (mine && col.here) {
-                unpack8<T>(m.x, x);
-                if (col.second || (MODE == kGather && !is_v)) unpack8<T>(m.y, y);
-            }
+            Lane l;
+            spread<T, MODE>(m.x, col.rest(m.y), l);
             const bool normed = mine && !is_v && (is_k ? P.a.k_weight : P.a.q_weight) != nullptr;
-            float ss = 0.f;
+            float2 s2 = both(0.f), t2 = both(0.f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                ss = fmaf(x[e], x[e], ss);
-                if (kTwo) ss = fmaf(y[e], y[e], ss);
+            for (int e = 0; e < 4; ++e) {
+                s2 = fma2(l.x[e], l.x[e], s2);
+                if (kTwo) t2 = fma2(l.y[e], l.y[e], t2);
             }
-            ss = group_sum<G>(ss);
+            const float ss = group_sum<G>(col.own(s2, t2));
             if (MODE == kGather) __syncwarp();  // in place: partners are read before any is written
             if (!mine || !col.here) continue;
             if (normed) {
-                const float r = rsqrtf(ss / (float)a.D + P.a.eps);
-                float w[8];
-                unpack8<T>(is_k ? wk[0] : wq[0], w);
+                const float2 r = both(rsqrtf(ss * P.inv_d + P.a.eps));
+                Lane w;
+                spread<T, MODE>(is_k ? wk[0] : wq[0], is_k ? wk[1] : wq[1], w);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] *= r * w[e];
-                if (col.second || MODE == kGather) {
-                    unpack8<T>(is_k ? wk[1] : wq[1], w);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] *= r * w[e];
+                for (int e = 0; e < 4; ++e) {
+                    l.x[e] = mul2(l.x[e], mul2(r, w.x[e]));
+                    l.y[e] = mul2(l.y[e], mul2(r, w.y[e]));
                 }
             }
-            if (!is_v) turn<MODE, false>(col, s_angles[buf][m.t - t0], pairs, x, y);
-            const bool second = col.second;
+            if (!is_v) turn<MODE, false>(col, s_angles[buf], (int)(m.t - t0), pairs, l);
             auto put16 = [&](T *dst) {
-                store8<T>(dst + col.c, x);
-                if (second) store8<T>(dst + col.d, y);
+                *reinterpret_cast<uint4 *>(dst + col.c) = vector_of<T, MODE>(l, 0);
+                if (col.second) *reinterpret_cast<uint4 *>(dst + col.d) = vector_of<T, MODE>(l, 1);
             };
             if (!is_k && !is_v) {
                 put16(static_cast<T *>(a.q_out) + m.t * a.q_out_token + m.h * a.q_out_head);
@@ -290,9 +345,11 @@ __global__ void __launch_bounds__(kNormThreads, kNormCtas)
                                 (int64_t)(m.slot % a.block_size) * a.cache_token + h * a.cache_head;
             if (Q8) {
                 uint8_t *const dst = static_cast<uint8_t *>(is_v ? a.v_cache : a.k_cache) + off;
-                const float f = 1.f / (is_v ? P.a.v_scale : P.a.k_scale)[h];
-                *reinterpret_cast<uint2 *>(dst + col.c) = pack_e4m3(x, f);
-                if (second) *reinterpret_cast<uint2 *>(dst + col.d) = pack_e4m3(y, f);
+                const float2 f = both(1.f / (is_v ? P.a.v_scale : P.a.k_scale)[h]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) l.x[e] = mul2(l.x[e], f), l.y[e] = mul2(l.y[e], f);
+                *reinterpret_cast<uint2 *>(dst + col.c) = bytes_of<MODE>(l, 0);
+                if (col.second) *reinterpret_cast<uint2 *>(dst + col.d) = bytes_of<MODE>(l, 1);
             } else {
                 put16(static_cast<T *>(is_v ? a.v_cache : a.k_cache) + off);
             }
@@ -307,7 +364,7 @@ __global__ void __launch_bounds__(kNormThreads, kGradCtas)
     const sgmv_norm_rope_grad_args &a = P.a;
     constexpr int kGroups = kNormThreads / G;
     constexpr bool kTwo = MODE != kGather;
-    __shared__ __align__(16) float2 s_angles[2][kChunk][kRopeMaxPairs];
+    __shared__ __align__(16) Angles s_angles[2];
     __shared__ float s_dw[kGroups > 8 ? 8 : kGroups][kSpecMaxD];
     const int g = threadIdx.x / G, pairs = a.pairs;
     const Columns<MODE> col(threadIdx.x % G, P.rot, P.uph, pairs, a.D);
@@ -351,13 +408,11 @@ __global__ void __launch_bounds__(kNormThreads, kGradCtas)
             m.gy = make_uint4(p[0] | p[1] << 16, p[2] | p[3] << 16, p[4] | p[5] << 16, p[6] | p[7] << 16);
         }
     };
-    float w[8], v[8], dw[8], dv[8];  // weights of the lane's columns, and their gradients
+    Lane w, dw;  // weights of the lane's columns, and their gradients
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = v[e] = 1.f, dw[e] = dv[e] = 0.f;
-    if (W && col.here) {
-        load8<T>(W + col.c, w);
-        if (col.second) load8<T>(W + col.d, v);
-    }
+    for (int e = 0; e < 4; ++e) w.x[e] = w.y[e] = both(1.f), dw.x[e] = dw.y[e] = both(0.f);
+    if (W)
+        spread<T, MODE>(*reinterpret_cast<const uint4 *>(W + c_at), *reinterpret_cast<const uint4 *>(W + d_at), w);
     Item next = {};
     if (i0 < i1) fetch(i0 + g, next);
     int buf = 0;
@@ -374,69 +429,65 @@ __global__ void __launch_bounds__(kNormThreads, kGradCtas)
             fetch(i + kGroups < c1 ? i + kGroups : c1 + g, next);
             if (!__any_sync(0xffffffffu, mine)) continue;
             const bool on = mine && col.here, second = col.second;
-            float gx[8], gy[8], x[8], y[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) gx[e] = gy[e] = x[e] = y[e] = 0.f;
+            Lane g, x;
+            spread<T, MODE>(m.gx, col.rest(m.gy), g);
+            spread<T, MODE>(m.x, col.rest(m.y), x);
             const int64_t t = mine ? m.t : t0, h = mine ? m.h : 0;
-            if (on) {
-                unpack8<T>(m.gx, gx);
-                if (second || MODE == kGather) unpack8<T>(m.gy, gy);
-                if (W) unpack8<T>(m.x, x);
-                if (W && second) unpack8<T>(m.y, y);
-                turn<MODE, true>(col, s_angles[buf][t - t0], pairs, gx, gy);
-            }
+            if (on) turn<MODE, true>(col, s_angles[buf], (int)(t - t0), pairs, g);
             if (W) {
                 // sum x^2, and sum of w g x: then mean(h * xh) = r / D times it
-                float ss = 0.f, dot = 0.f;
+                float2 s2 = both(0.f), d2 = both(0.f), t2 = both(0.f), e2 = both(0.f);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    ss = fmaf(x[e], x[e], ss);
-                    dot = fmaf(w[e] * gx[e], x[e], dot);
+                for (int e = 0; e < 4; ++e) {
+                    s2 = fma2(x.x[e], x.x[e], s2);
+                    d2 = fma2(mul2(w.x[e], g.x[e]), x.x[e], d2);
                     if (kTwo) {
-                        ss = fmaf(y[e], y[e], ss);
-                        dot = fmaf(v[e] * gy[e], y[e], dot);
+                        t2 = fma2(x.y[e], x.y[e], t2);
+                        e2 = fma2(mul2(w.y[e], g.y[e]), x.y[e], e2);
                     }
                 }
-                ss = group_sum<G>(ss);
-                dot = group_sum<G>(dot);
-                const float r = rsqrtf(ss / (float)a.D + a.eps), f = dot * r / (float)a.D * r;
+                const float ss = group_sum<G>(col.own(s2, t2)), dot = group_sum<G>(col.own(d2, e2));
+                const float r = rsqrtf(ss * P.inv_d + a.eps), f = dot * r * P.inv_d * r;
                 if (on) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        dw[e] = fmaf(gx[e], x[e] * r, dw[e]);
-                        gx[e] = r * (w[e] * gx[e] - f * x[e]);
+                    for (int e = 0; e < 4; ++e) {
+                        dw.x[e] = fma2(g.x[e], mul2(x.x[e], both(r)), dw.x[e]);
+                        g.x[e] = mul2(both(r), fma2(x.x[e], both(-f), mul2(w.x[e], g.x[e])));
                         if (kTwo) {
-                            dv[e] = fmaf(gy[e], y[e] * r, dv[e]);
-                            gy[e] = r * (v[e] * gy[e] - f * y[e]);
+                            dw.y[e] = fma2(g.y[e], mul2(x.y[e], both(r)), dw.y[e]);
+                            g.y[e] = mul2(both(r), fma2(x.y[e], both(-f), mul2(w.y[e], g.y[e])));
                         }
                     }
                 }
             }
             if (on) {
                 T *const dx = DX + t * dx_token + h * dx_head;
-                store8<T>(dx + col.c, gx);
-                if (second) store8<T>(dx + col.d, gy);
+                *reinterpret_cast<uint4 *>(dx + col.c) = vector_of<T, MODE>(g, 0);
+                if (second) *reinterpret_cast<uint4 *>(dx + col.d) = vector_of<T, MODE>(g, 1);
             }
         }
         c0 = c1;
     }
     if (!W) return;
     // the groups' sums, in order: over the warp, then over the eight warps
-    constexpr int kWarpGroups = 32 / G;
+    float sums[16];
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
+    for (int j = 0; j < 8; ++j) {
+        const float2 v = two_of<MODE>(dw, j);
+        sums[2 * j] = v.x;
+        sums[2 * j + 1] = v.y;
+    }
 #pragma unroll
-        for (int o = G; o < 32; o <<= 1) {
-            dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], o);
-            if (kTwo) dv[e] += __shfl_xor_sync(0xffffffffu, dv[e], o);
-        }
+    for (int e = 0; e < (kTwo ? 16 : 8); ++e)
+#pragma unroll
+        for (int o = G; o < 32; o <<= 1) sums[e] += __shfl_xor_sync(0xffffffffu, sums[e], o);
     const int warp = threadIdx.x / 32;
-    static_assert(kNormThreads / 32 <= 8 && (kGroups >= 8 || kWarpGroups == 1), "a row of sums per warp");
+    static_assert(kNormThreads / 32 <= 8 && kGroups >= 8, "a row of sums per warp");
     if ((threadIdx.x & 31) < G && col.here) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            s_dw[warp][col.c + e] = dw[e];
-            if (col.second) s_dw[warp][col.d + e] = dv[e];
+            s_dw[warp][col.c + e] = sums[e];
+            if (col.second) s_dw[warp][col.d + e] = sums[8 + e];
         }
     }
     __syncthreads();
@@ -545,6 +596,7 @@ template <typename T> int launch_grad_mode(const GradParams &p, int mode, int ns
 int norm_rope_launch(const sgmv_norm_rope_args &a, const uint64_t *turns, int nsm, int *err, cudaStream_t stream) {
     NormParams p;
     p.a = a;
+    p.inv_d = 1.f / (float)a.rope.D;
     for (int i = 0; i < a.rope.pairs; ++i) p.turns[i] = turns[i];
     const int mode = mode_of(a.rope.interleaved, a.rope.pairs);
     places(mode, a.rope.D, a.rope.pairs, &p.rot, &p.uph);
@@ -558,6 +610,7 @@ int norm_rope_grad_launch(const sgmv_norm_rope_grad_args &a, const uint64_t *tur
     GradParams p;
     p.a = a;
     p.part = static_cast<float *>(a.workspace);
+    p.inv_d = 1.f / (float)a.D;
     for (int i = 0; i < a.pairs; ++i) p.turns[i] = turns[i];
     const int mode = mode_of(a.interleaved, a.pairs);
     places(mode, a.D, a.pairs, &p.rot, &p.uph);

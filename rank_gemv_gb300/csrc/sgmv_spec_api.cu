@@ -28,6 +28,7 @@ void settle(int64_t &stride, int32_t entries, int32_t D) {
 }
 
 constexpr int32_t kMaxVocabulary = 1 << 24;
+constexpr double kMaxRows = 1 << 30;  // heads of all tokens, which the norm kernels count in 32 bits
 
 int check_head(int32_t D) {
     if (D < 1) return SGMV_ERR_INVALID_ARG;
@@ -270,7 +271,7 @@ int sgmv_norm_rope(const sgmv_norm_rope_args *args, void *stream) {
     int st = check_rope(a, e4m3 ? 16 : 8, &none);
     if (st != SGMV_OK) return st;
     if (!aligned16(n.q_weight) || !aligned16(n.k_weight)) return SGMV_ERR_ALIGNMENT;
-    if ((double)a.T * ((double)a.Hq + 2.0 * a.Hk) >= 2147483648.0) return SGMV_ERR_UNSUPPORTED;
+    if ((double)a.T * ((double)a.Hq + 2.0 * a.Hk) > kMaxRows) return SGMV_ERR_UNSUPPORTED;
     if (none) return SGMV_OK;
     uint64_t turns[kRopeMaxPairs];
     if ((st = turns_of(a.inv_freq, a.pairs, turns)) != SGMV_OK) return st;
@@ -296,7 +297,7 @@ int sgmv_norm_rope_grad(const sgmv_norm_rope_grad_args *args, void *stream) {
     if (!a.q_weight != !a.dq_weight || !a.k_weight != !a.dk_weight || (a.Hq == 0 && a.q_weight) ||
         (a.Hk == 0 && a.k_weight))
         return SGMV_ERR_INVALID_ARG;
-    if ((double)a.T * ((double)a.Hq + a.Hk) >= 2147483648.0) return SGMV_ERR_UNSUPPORTED;
+    if ((double)a.T * ((double)a.Hq + a.Hk) > kMaxRows) return SGMV_ERR_UNSUPPORTED;
     if (a.T == 0 && !a.dq_weight && !a.dk_weight) return SGMV_OK;
     if (a.Hq == 0 && a.Hk == 0) return SGMV_OK;
     if (a.T > 0) {

@@ -14,7 +14,7 @@ EPS = 1e-5
 # T, Hq, Hk, D, pairs: lanes of 4 to 32 per head, idle lanes, pairs of any number, few and many rows
 SHAPES = [(1, 32, 8, 128, 64), (7, 8, 2, 128, 32), (33, 3, 1, 80, 16), (5, 4, 4, 64, 5), (3, 1, 1, 16, 8),
           (4, 2, 2, 256, 128), (2, 5, 5, 96, 0), (300, 2, 1, 64, 13), (1000, 40, 8, 32, 16), (9, 1, 7, 48, 24),
-          (40, 1, 1, 240, 8), (65, 7, 3, 112, 55)]
+          (40, 1, 1, 240, 8), (65, 7, 3, 112, 55), (6, 2, 1, 8, 4), (11, 3, 2, 24, 8)]
 
 
 @pytest.fixture(scope="module")
