@@ -84,6 +84,7 @@ struct SampleParams {
     int32_t share;   // entries of a warp's range
     int32_t staged;  // the ranges are in shared memory
     int32_t noted;   // a thread's entries of a range have a bit each
+    int32_t sorted;  // slow rows first
 };
 
 // One zero; finite logits and +inf within +-2^126, so that differences are finite; NaN as -inf.
@@ -141,9 +142,31 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
     __shared__ SampleShared s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cl = (int)cluster_size(), rank = (int)cluster_rank(), share = P.share;
-    const int64_t t = (int64_t)(blockIdx.x / (unsigned)cl);
+    int64_t t = (int64_t)(blockIdx.x / (unsigned)cl);
     pdl_wait();
     pdl_trigger();
+    if (P.sorted) {
+        // More rows than run at once: those whose filters may have to look at many tokens, which
+        // take several times as long, come first (128 rows of 100277 with mixed settings: 63 us,
+        // 77 as they come; 512 rows of 32000 with probabilities: 113, 144).
+        bool slow = false;
+        if (tid < a.T) {
+            const int k = a.top_k ? a.top_k[tid] : a.top_k_all;
+            const float p = a.top_p ? a.top_p[tid] : a.top_p_all, tau = a.temperature ? a.temperature[tid] : a.temperature_all;
+            slow = tau > 0.f && (k <= 0 || k > kFew) && (p < 1.f || k > kFew) && p > 0.f;
+        }
+        const unsigned who = __ballot_sync(0xffffffffu, slow);
+        if (lane == 0) s.scan_n[warp] = (uint32_t)__popc(who);
+        __syncthreads();
+        int before = __popc(who & ((1u << lane) - 1)), all = 0;  // slow rows
+        for (int e = 0; e < kWarps; ++e) {
+            if (e < warp) before += (int)s.scan_n[e];
+            all += (int)s.scan_n[e];
+        }
+        if (tid < a.T && (slow ? before : all + tid - before) == (int)t) s.found = tid;
+        __syncthreads();
+        t = s.found;
+    }
     const T *const row = static_cast<const T *>(a.logits) + t * a.logits_row;
     // Entries u = token + skew: vectors at whole multiples are aligned in memory.
     constexpr int kVec = 16 / (int)sizeof(T);
@@ -377,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
     // The sum of all entries' kept weights, with take(logit) for those that are not deep.
     // Deep ones, mostly the most, are done at once; the others, whose weights take ten times the
     // instructions, wait in a queue of the warp's until all of its lanes have one.
-    auto sum_weights = [&](auto take) {
+    auto sum_weights = [&](auto take, int64_t &deep_sum) {
         const bool all = cut_l == -INFINITY;
         float *const queue = reinterpret_cast<float *>(s.list) + warp * 64;
         int64_t sum = 0;
@@ -409,12 +432,12 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
                     __syncwarp();
                 }
             }
-            sum += w;
+            deep_sum += w;
         }
         __syncwarp();
         if (lane < waiting) weigh_one(queue[lane]);
         __syncwarp();
-        return sum;
+        return sum + deep_sum;
     };
     // Counts what the pass counts; the whole cluster's counts in n2, those before them in n_before.
     auto count_bins = [&](auto pass) {
@@ -575,7 +598,9 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
     int64_t target = 0;  // top-p's part of the weights
     // Bounds of the running weight at the ends of this thread's bins, over `above`; then the
     // first bin that can reach the target, and the first that must, to bin0 and bin1.
-    auto bound_bins = [&](int64_t above) {
+    // mass: what the counted tokens weigh in all, if known (else 0): then what lies behind a bin
+    // bounds it too, which is what finds a cut near the end.
+    auto bound_bins = [&](int64_t above, int64_t mass) {
         float wl[2], wh[2], sl = 0.f, sh = 0.f;
         auto edge = [&](int b) {
             return first ? b * (-kOctaves / kBins) : (hi - (hi - lo) * ((float)b / (kBins - 1)) - m) * weigh.ch;
@@ -594,12 +619,21 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
         if (tid == 0) s.bin0 = s.bin1 = kBins - 1;
         __syncthreads();
         sl -= own_l, sh -= own_h;
-        for (int e = 0; e < warp; ++e) sl += s.scan_lo[e], sh += s.scan_hi[e];
-        const float need = (float)(target - above);
+        float all_l = 0.f, all_h = 0.f;
+        for (int e = 0; e < kWarps; ++e) {
+            if (e < warp) sl += s.scan_lo[e], sh += s.scan_hi[e];
+            all_l += s.scan_lo[e], all_h += s.scan_hi[e];
+        }
+        const float need = (float)(target - above), m0 = (float)mass, slack = all_h * kSlack;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            if ((sh + wh[e]) * (1.f + kSlack) >= need) atomicMin(&s.bin0, 2 * tid + e);
-            if ((sl + wl[e]) * (1.f - kSlack) >= need) atomicMin(&s.bin1, 2 * tid + e);
+            float most = (sh + wh[e]) * (1.f + kSlack), least = (sl + wl[e]) * (1.f - kSlack);
+            if (mass > 0) {
+                most = fminf(most, m0 - (all_l - (sl + wl[e])) + slack);
+                least = fmaxf(least, m0 - (all_h - (sh + wh[e])) - slack);
+            }
+            if (most >= need) atomicMin(&s.bin0, 2 * tid + e);
+            if (least >= need) atomicMin(&s.bin1, 2 * tid + e);
         }
         __syncthreads();
     };
@@ -617,7 +651,8 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
         }
         __syncthreads();
     };
-    int64_t total = 0;  // of the tokens that top-k keeps
+    int64_t total = 0;    // of the tokens that top-k keeps
+    int64_t counted = 0;  // and of those in the first bins
     bool cut_k = false;
     // Notes this thread's tokens in bins up to `last`.
     auto note = [&](int last) {
@@ -652,10 +687,10 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
             clear_bins();
         }
         if (!by_note || few > kFew) {
-            int64_t v[1] = {0};
+            int64_t v[2] = {0, 0};  // the weights, and those of deep ones that are not counted
             const bool sums = by_p && !by_k;
             count_bins([&]() {
-                if (sums && P.noted) v[0] = sum_weights(count);  // (deep ones are not counted)
+                if (sums && P.noted) v[0] = sum_weights(count, v[1]);
                 else each([&](float l, int) {
                     count(l);
                     if (sums) v[0] += weigh(l);
@@ -673,13 +708,15 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
                     join(v, plus);
                     total = v[0];
                     target = part(total, part_p);
-                    bound_bins(0);
+                    counted = total - v[1];
+                    bound_bins(0, counted);
                     last = s.bin1;
                     if (sums && P.noted && last >= (int)(kDeep * (kBins / kOctaves)) - 1) {
                         // the cut may be among the deep ones: with them
                         clear_bins();
                         count_bins(count_kept);
-                        bound_bins(0);
+                        counted = total;
+                        bound_bins(0, counted);
                         last = s.bin1;
                         few = n_all;
                     }
@@ -780,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
                 if (kept(l, i)) v[0] += weigh(l);
             });
             join(v, plus);
-            total = v[0];
+            counted = total = v[0];
             target = part(total, part_p);
         }
     }
@@ -788,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
         // ---- where the running weight reaches p of the total ------------------------------
         int64_t above = 0;
         for (;;) {
-            bound_bins(above);
+            bound_bins(above, first ? counted : 0);
             int b0 = s.bin0, b1 = s.bin1;
             Span e = span(b0, b1, true);
             if (!first && e.count > kFew && e.lo < e.hi && e.lo == lo && e.hi == hi) {
@@ -833,9 +870,9 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
         const int64_t w = weigh(l);
         return w >= least ? w : 0;
     };
-    int64_t v[1] = {0};
+    int64_t v[1] = {0}, deep = 0;
     if (by_note || !P.noted || least > 0) each([&](float l, int i) { v[0] += final_weight(l, i); });
-    else v[0] = sum_weights([](float) {});
+    else v[0] = sum_weights([](float) {}, deep);
     join(v, plus);
     if (a.token) {
         int64_t u = (int64_t)(a.u[t] * 0x1p24f);
@@ -873,6 +910,7 @@ int sample_launch(const sgmv_sample_args &a, int nsm, cudaStream_t stream) {
     const size_t bytes = (size_t)p.share * kWarps * 4;
     p.staged = bytes <= 200 * 1024;
     p.noted = p.staged && p.share <= 64 / 4 * 128;
+    p.sorted = (a.top_k || a.top_p) && a.T <= kThreads && (int64_t)a.T * cl > 2 * std::max(1, nsm);
     const size_t smem = p.staged ? bytes : 0;
     switch (a.dtype) {
         case SGMV_F16: return launch<__half>(p, cl, smem, stream);
