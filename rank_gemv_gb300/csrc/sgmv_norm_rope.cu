@@ -8,13 +8,20 @@
 // over the group by shuffles, turned in registers and written once to each of its
 // places.  Items of q, k and v lie on one line, t * (Hq + 2 Hk) + head, of which
 // every CTA takes an equal contiguous part; the angles of kChunk tokens at a time
-// are computed into shared memory and used by all their heads.  Bounded by memory.
+// are computed into shared memory and used by all their heads.  8192 rows of 32 + 8 heads of 128 to an
+// e4m3 cache: 47 us, 184 MB at 3.9 TB/s; bounded by the instructions (some 370 per warp and
+// 512 columns, the issue slots 68 % busy) in front of the memory: a plain copy of as many
+// bytes takes 35 us.  (Loads under a condition, one vector per lane: 69 us; fp32 operations
+// one at a time: 50.)
 //
 // Gradient: with g = scale R^T dy, xh = r x, h = w * g,
 //   dx = r (h - xh mean(h * xh)),   dw = sum over rows of g * xh.
 // A lane adds up its columns of dw in registers over all its items, a CTA then its
 // groups' in shared memory, in order; a second kernel adds the CTAs' sums, in order
-// too, so the result is the same in every run.  A CTA has rows of q or of k only.
+// too, so the result is the same in every run.  A CTA has rows of q or of k only.  8192
+// rows of 32 + 8 heads of 128: 72 us, 252 MB at 3.5 TB/s (a plain copy: 45); bounded by
+// latency, as the sums' registers leave room for 512 threads on an SM, with 32 KB of rows
+// under way.
 #include <cuda_fp8.h>
 
 #include <algorithm>

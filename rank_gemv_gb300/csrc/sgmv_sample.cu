@@ -16,6 +16,13 @@
 // and only those are looked at again: the bins around the cut are divided finer, until
 // few tokens are left, or one value, whose tokens are counted off by index; the sums
 // above the cut are exact at every step.
+//
+// 128 rows of 100277 fp32 logits, all filters, no two rows alike: 63 us (51 MB at 0.8 TB/s; a
+// plain copy of them takes 16).  Bounded by the rows that have many candidates: one row
+// takes 10 us greedy, 12 to 25 with a top-k of up to 256, 30 to 40 of 1000, and 35 to 59 with
+// top-p alone, most of that weighing, some 40 instructions for a weight that is not
+// deep.  All 128 run at once.  One row of 32000, top-p: 10 us, of which the host
+// needs most.
 #include <algorithm>
 
 #include "sgmv_device.cuh"
