@@ -17,12 +17,15 @@
 // few tokens are left, or one value, whose tokens are counted off by index; the sums
 // above the cut are exact at every step.
 //
-// 128 rows of 100277 fp32 logits, all filters, no two rows alike: 63 us (51 MB at 0.8 TB/s; a
-// plain copy of them takes 16).  Bounded by the rows that have many candidates: one row
-// takes 10 us greedy, 12 to 25 with a top-k of up to 256, 30 to 40 of 1000, and 35 to 59 with
-// top-p alone, most of that weighing, some 40 instructions for a weight that is not
-// deep.  All 128 run at once.  One row of 32000, top-p: 10 us, of which the host
-// needs most.
+// 128 rows of 100277 fp32 logits, all filters, no two rows alike: 63 to 82 us for eight sets of
+// rows and settings (51 MB at 0.6 to 0.8 TB/s; a plain copy of them takes 16; without filters
+// 62).  Bounded by the rows that have many candidates: one row takes 10 us greedy, 12 to 25
+// with a top-k of up to 256, 30 to 40 of 1000, and 35 to 60 with top-p alone, most of that
+// weighing, some 40 instructions for a weight that is not deep.  Each token is weighed once
+// for the total and once above the cut, at most: what a thread has weighed above is its part
+// of the kept weights too, where min-p drops nothing (a third time: 64 to 94 us, top-p alone
+// 133 against 107).  One row of 32000, top-p: 12 to 30 us by the number of candidates, a
+// chain of passes with a cluster barrier after each; the host needs 9.
 #include <algorithm>
 
 #include "sgmv_device.cuh"
@@ -404,11 +407,11 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
         const int b = bin_of(l);
         if (b >= 0 && b < kBins) atomicAdd(&s.hist[b], 1u);
     };
-    // The sum of all entries' kept weights, with take(logit) for those that are not deep.
+    // The sum of the weights of entries with on(logit, token, bit), with take(logit) for those
+    // that are not deep.
     // Deep ones, mostly the most, are done at once; the others, whose weights take ten times the
     // instructions, wait in a queue of the warp's until all of its lanes have one.
-    auto sum_weights = [&](auto take, int64_t &deep_sum) {
-        const bool all = cut_l == -INFINITY;
+    auto sum_weights = [&](auto on, auto take, int64_t &deep_sum) {
         float *const queue = reinterpret_cast<float *>(s.list) + warp * 64;
         int64_t sum = 0;
         int waiting = 0;
@@ -424,8 +427,8 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float up = weigh.raised(x[e]);
-                const bool on = all || kept(x[e], u0 + i + e - skew), full = on && up >= 38.f - kDeep;
-                if (on && !full) w += Weigh::deep(up);
+                const bool yes = on(x[e], u0 + i + e - skew, 4 * j + e), full = yes && up >= 38.f - kDeep;
+                if (yes && !full) w += Weigh::deep(up);
                 const unsigned who = __ballot_sync(0xffffffffu, full);
                 if (full) queue[waiting + __popc(who & ((1u << lane) - 1))] = x[e];
                 waiting += __popc(who);
@@ -575,22 +578,31 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
         int64_t above, count;
         float lo, hi;
     };
+    int64_t own_above = 0;  // this thread's part of the last span's weights
     auto span = [&](int b0, int b1, bool weights) {
         int64_t v[4] = {0, 0, 0, 0};
         float small = INFINITY, large = -INFINITY;
         inside = 0;
-        each([&](float l, int i) {
+        // whether a token is in a bin before b0; those in the bins are counted
+        auto before = [&](float l, int i, uint64_t bit) {
             const int b = bin_of(l);
-            if (b < 0 || b > b1 || !kept(l, i)) return;
-            if (b >= b0) {
-                ++v[1];
-                inside |= at_bit;
-                small = fminf(small, l);
-                large = fmaxf(large, l);
-            } else if (weights) {
-                v[0] += weigh(l);
-            }
-        });
+            if (b < 0 || b > b1 || !kept(l, i)) return false;
+            if (b < b0) return true;
+            ++v[1];
+            inside |= bit;
+            small = fminf(small, l);
+            large = fmaxf(large, l);
+            return false;
+        };
+        if (P.noted && !by_note) {
+            int64_t deep = 0;
+            v[0] = sum_weights([&](float l, int i, int bit) { return before(l, i, 1ull << bit) && weights; }, [](float) {}, deep);
+        } else {
+            each([&](float l, int i) {
+                if (before(l, i, at_bit) && weights) v[0] += weigh(l);
+            });
+        }
+        own_above = v[0];
         // (floats in the order of whole numbers)
         auto key = [](float x) { return (int64_t)(__float_as_int(x) ^ (__float_as_int(x) < 0 ? 0x7fffffff : 0)); };
         auto back = [](int64_t x) { return __int_as_float((int)x ^ ((int)x < 0 ? 0x7fffffff : 0)); };
@@ -660,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
     };
     int64_t total = 0;    // of the tokens that top-k keeps
     int64_t counted = 0;  // and of those in the first bins
-    bool cut_k = false;
+    bool cut_k = false, bounds = false;  // bounds: bin0 and bin1 are those of the first bins
     // Notes this thread's tokens in bins up to `last`.
     auto note = [&](int last) {
         noted = 0;
@@ -697,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
             int64_t v[2] = {0, 0};  // the weights, and those of deep ones that are not counted
             const bool sums = by_p && !by_k;
             count_bins([&]() {
-                if (sums && P.noted) v[0] = sum_weights(count, v[1]);
+                if (sums && P.noted) v[0] = sum_weights([](float, int, int) { return true; }, count, v[1]);
                 else each([&](float l, int) {
                     count(l);
                     if (sums) v[0] += weigh(l);
@@ -727,6 +739,7 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
                         last = s.bin1;
                         few = n_all;
                     }
+                    bounds = true;
                     if (tid == last / 2) s.count = n_before + n2[0] + (last & 1 ? n2[1] : 0);
                     __syncthreads();
                     few = s.count;
@@ -785,9 +798,12 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
             }
             return;
         }
+        // (half of the row: 128 rows with top-k and top-p took 76 us with a sixteenth, 65 so;
+        // without, the first span looks at every token, in vectors)
         if (P.noted && few <= (uint32_t)a.V / 2) note(last);
     }
     const uint64_t candidates = noted;
+    const bool some = by_note;
     if (cut_k) {
         // ---- the k-th token ---------------------------------------------------------
         const uint32_t n2_0 = n2[0], n2_1 = n2[1], n_before_0 = n_before;
@@ -809,12 +825,14 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
             hi = e.hi;
             lo = e.lo;
             noted = inside;  // only these are looked at from here on
+            by_note = P.noted;
             clear_bins();
             count_bins(count_kept);
         }
         // the first bins' counts of what is left
         first = true;
         noted = candidates;
+        by_note = some;
         const uint32_t room = (uint32_t)k > n_before_0 ? (uint32_t)k - n_before_0 : 0;
         n2[0] = min(n2_0, room);
         n2[1] = min(n2_1, room - n2[0]);
@@ -828,11 +846,13 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
             target = part(total, part_p);
         }
     }
+    int64_t own_kept = 0;  // what this thread has weighed above the cut
     if (by_p) {
         // ---- where the running weight reaches p of the total ------------------------------
         int64_t above = 0;
         for (;;) {
-            bound_bins(above, first ? counted : 0);
+            if (!bounds) bound_bins(above, first ? counted : 0);
+            bounds = false;
             int b0 = s.bin0, b1 = s.bin1;
             Span e = span(b0, b1, true);
             if (!first && e.count > kFew && e.lo < e.hi && e.lo == lo && e.hi == hi) {
@@ -847,6 +867,9 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
                 }
             }
             above += e.above;
+            own_kept += own_above;
+            noted = inside;  // only these are looked at from here on
+            by_note = P.noted;
             if (e.count <= kFew) {
                 collect(b0, b1);
                 rank_list([&](const Entry &x, bool last) {
@@ -862,13 +885,11 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
             first = false;
             hi = e.hi;
             lo = e.lo;
-            noted = inside;  // only these are looked at from here on
             clear_bins();
             count_bins(count_kept);
         }
     }
 
-    noted = candidates;
     // ---- the token ---------------------------------------------------------------------
     // (a logit whose weight cannot reach min_p's needs no weight)
     const float floor_l = least > 0 ? log2f((float)least) - 38.01f : -INFINITY;
@@ -878,8 +899,19 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
         return w >= least ? w : 0;
     };
     int64_t v[1] = {0}, deep = 0;
-    if (by_note || !P.noted || least > 0) each([&](float l, int i) { v[0] += final_weight(l, i); });
-    else v[0] = sum_weights([](float) {}, deep);
+    if (by_p && P.noted && weigh(cut_l) >= least) {
+        // min-p drops nothing that is left: the tokens above have been weighed, those around the
+        // cut are noted
+        v[0] = own_kept;
+        each([&](float l, int i) {
+            if (kept(l, i)) v[0] += weigh(l);
+        });
+    } else {
+        noted = candidates;
+        by_note = some;
+        if (by_note || !P.noted || least > 0) each([&](float l, int i) { v[0] += final_weight(l, i); });
+        else v[0] = sum_weights([&](float l, int i, int) { return kept(l, i); }, [](float) {}, deep);
+    }
     join(v, plus);
     if (a.token) {
         int64_t u = (int64_t)(a.u[t] * 0x1p24f);
