@@ -588,7 +588,8 @@ int sgmv_norm_rope(const sgmv_norm_rope_args *args, void *stream);
  * g = scale R^T dy, r = 1 / sqrt(mean(x^2) + eps), h = w * g,
  *   dx = r (h - r^2 x mean(h * x)),   dw = sum over rows and heads of g * r x
  * (dx = g for a tensor without a weight).  q, k, dq_out, dk_out, dq, dk [T][heads][D]
- * of any token and head strides, dq and dk apart from the inputs; q or k may be
+ * of any token and head strides, dq and dk apart from the inputs (SGMV_ERR_INVALID_ARG
+ * for the same address); q or k may be
  * left out (Hq or Hk = 0), and is not read without its weight; T * (Hq + Hk) up to 2^30.  dq_weight, dk_weight fp32 [D], written
  * (not added to); given exactly where the weight is.  Sums are fp32, joined in fp64 in a fixed order:
  * the same result in every run.
@@ -655,7 +656,7 @@ int sgmv_quant_attention(const sgmv_quant_attention_args *args, void *stream);
  *     temperature_all, ... hold for every row
  *   u fp32 [T], token int32 [T]: both or neither; probs fp32 [T][V], or NULL
  *   logits_row, probs_row: elements between rows; logits aligned to its type
- * probs must not overlap logits.  V up to 2^24, T to 2^27 (SGMV_ERR_UNSUPPORTED beyond).
+ * probs must not overlap logits (SGMV_ERR_INVALID_ARG for the same address).  V up to 2^24, T to 2^27 (SGMV_ERR_UNSUPPORTED beyond).
  */
 typedef struct {
     const void *logits;

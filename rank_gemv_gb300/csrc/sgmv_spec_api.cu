@@ -322,6 +322,10 @@ int sgmv_norm_rope_grad(const sgmv_norm_rope_grad_args *args, void *stream) {
         st = check_workspace(a.workspace, a.workspace_bytes, norm_rope_grad_workspace(a.D), 16);
         if (st != SGMV_OK) return st;
     }
+    // not in place
+    if (a.T > 0 && ((a.Hq > 0 && (a.dq == a.dq_out || (a.q_weight && a.dq == a.q))) ||
+                    (a.Hk > 0 && (a.dk == a.dk_out || (a.k_weight && a.dk == a.k)))))
+        return SGMV_ERR_INVALID_ARG;
     uint64_t turns[kRopeMaxPairs];
     if ((st = turns_of(a.inv_freq, a.pairs, turns)) != SGMV_OK) return st;
     if (!device_error_word()) return SGMV_ERR_CUDA;
@@ -341,6 +345,7 @@ int sgmv_sample(const sgmv_sample_args *args, void *stream) {
     if (!a.logits) return SGMV_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(a.logits) % (a.dtype == SGMV_F32 ? 4 : 2) != 0 || !aligned4(a.probs))
         return SGMV_ERR_ALIGNMENT;
+    if (a.probs == a.logits) return SGMV_ERR_INVALID_ARG;  // not in place
     return finish("sampling kernel", sample_launch(a, device_sms(), static_cast<cudaStream_t>(stream)), 1);
 }
 

@@ -135,6 +135,21 @@ def test_sample_refusals(sgmv):
     assert sgmv.load_library().sgmv_sample(None, None) == INVALID
 
 
+def test_gradient_and_sampling_are_not_in_place(sgmv, freq):
+    size = sgmv.sgmv_norm_rope_grad_workspace_bytes(64)
+    apart = dict(zip(("dq", "dk", "dq_out", "dk_out", "q", "k"), range(A16, A16 + 6 * 4096, 4096)))
+    base = dict({f: 64 for f in GRAD if f.endswith(("_token", "_head"))}, **apart, q_weight=A16, k_weight=A16,
+                dq_weight=A16, dk_weight=A16, positions=A16, inv_freq=freq.data_ptr(), workspace=A16,
+                workspace_bytes=size, T=4, Hq=2, Hk=2, D=64, pairs=32, scale=1.0, eps=1e-6)
+    call = caller(sgmv, "sgmv_norm_rope_grad", sgmv._NORM_GRAD_ARGS, GRAD, base)
+    for side in "qk":
+        for other in (f"d{side}_out", side):
+            assert call(**{f"d{side}": base[other]}) == INVALID, other
+    base = dict(logits=A16, u=A16, token=A16, probs=A16, logits_row=50, probs_row=50, T=4, V=50, dtype=2,
+                temperature_all=1.0, top_p_all=1.0)
+    assert caller(sgmv, "sgmv_sample", sgmv._SAMPLE_ARGS, SAMPLE, base)() == INVALID
+
+
 def i32(*x):
     return torch.tensor(x, dtype=I)
 
