@@ -153,6 +153,7 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cl = (int)cluster_size(), rank = (int)cluster_rank(), share = P.share;
     int64_t t = (int64_t)(blockIdx.x / (unsigned)cl);
+    if (cl > 1) cluster_arrive_relaxed();  // waited on just before the first peer access
     pdl_wait();
     pdl_trigger();
     if (P.sorted) {
@@ -345,6 +346,7 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
         // (floats in the order of whole numbers)
         auto key = [](float x) { return (int64_t)(__float_as_int(x) ^ (__float_as_int(x) < 0 ? 0x7fffffff : 0)); };
         int64_t v[1] = {key(m)};
+        if (cl > 1) cluster_wait();  // every CTA of the cluster has started
         join(v, [](int, int64_t x, int64_t y) { return x > y ? x : y; });
         m = __int_as_float((int)v[0] ^ ((int)v[0] < 0 ? 0x7fffffff : 0));
     }
