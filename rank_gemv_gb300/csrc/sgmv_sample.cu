@@ -549,12 +549,12 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
         }
         return x;
     };
-    // Ranks the list; where yes(entry, last), the cut is.
+    // Ranks the list; where yes(entry), the cut is.
     auto rank_list = [&](auto yes) {
         if (rank == 0) {
             const int n = min((int)s.listed, kFew);
             const Entry x = entry(n);
-            if (tid < n && yes(x, x.place == n - 1))
+            if (tid < n && yes(x))
                 for (int r = 0; r < cl; ++r) {
                     st_peer(peer_addr(&s.cut_l, (uint32_t)r), x.l);
                     st_peer32(peer_addr(&s.cut_v, (uint32_t)r), (uint32_t)x.v);
@@ -620,7 +620,10 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
     // Bounds of the running weight at the ends of this thread's bins, over `above`; then the
     // first bin that can reach the target, and the first that must, to bin0 and bin1.
     // mass: what the counted tokens weigh in all, if known (else 0): then what lies behind a bin
-    // bounds it too, which is what finds a cut near the end.
+    // bounds it too, which is what finds a cut near the end.  A weight is rounded down to a whole
+    // number: at the lower edge it is above 2^x - 2, not 2^x, which counts where the cut is among
+    // weights of some thousand units or less.  (What fp32 makes of an edge, x and the weights
+    // themselves is 1.5e-5 of a weight at most: kSlack.)
     auto bound_bins = [&](int64_t above, int64_t mass) {
         float wl[2], wh[2], sl = 0.f, sh = 0.f;
         auto edge = [&](int b) {
@@ -629,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             wh[e] = sh += (float)n2[e] * exp2f(edge(2 * tid + e) + 38.f);
-            wl[e] = sl += (float)n2[e] * exp2f(edge(2 * tid + e + 1) + 38.f);
+            wl[e] = sl += (float)n2[e] * fmaxf(exp2f(edge(2 * tid + e + 1) + 38.f) - 2.f, 0.f);
         }
         const float own_l = sl, own_h = sh;
         for (int o = 1; o < 32; o <<= 1) {
@@ -815,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
             want = s.rank;
             if (s.count <= kFew) {
                 collect(b, b);
-                rank_list([&](const Entry &x, bool) { return x.place == (int)want - 1; });
+                rank_list([&](const Entry &x) { return x.place == (int)want - 1; });
                 break;
             }
             const Span e = span(b, b, false);
@@ -874,8 +877,8 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
             by_note = P.noted;
             if (e.count <= kFew) {
                 collect(b0, b1);
-                rank_list([&](const Entry &x, bool last) {
-                    return above + x.before < target && (above + x.before + x.w >= target || last);
+                rank_list([&](const Entry &x) {
+                    return above + x.before < target && above + x.before + x.w >= target;
                 });
                 break;
             }
