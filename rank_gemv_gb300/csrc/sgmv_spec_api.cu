@@ -13,7 +13,8 @@ namespace {
 using namespace sgmv;
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+// of every array of 32-bit words (those that are not given pass)
+template <typename... P> bool aligned4(const P *...p) { return ((reinterpret_cast<uintptr_t>(p) | ... | 0) & 3u) == 0; }
 bool half_type(int dt) { return dt == SGMV_F16 || dt == SGMV_BF16; }
 
 // 16-bit data read and written in 16-byte pieces
@@ -68,7 +69,7 @@ int check_rope(sgmv_rope_args &a, int width, bool *none) {
     if (append && (!vectors(a.v, a.v_token, a.v_head) || !vectors(a.k_cache, a.cache_block, a.cache_token, width) ||
                    !vectors(a.v_cache, a.cache_head, 0, width) || a.D % width != 0))
         return SGMV_ERR_ALIGNMENT;
-    return SGMV_OK;
+    return aligned4(a.positions, a.slots) ? SGMV_OK : SGMV_ERR_ALIGNMENT;
 }
 
 // Turns per position, modulo one turn, as a fraction of 2^64.
@@ -112,7 +113,7 @@ int check_attention(sgmv_tree_attention_args &a, int width, bool *none) {
         !vectors(a.k_cache, a.cache_block, a.cache_token, width) || !vectors(a.v_cache, a.cache_head, 0, width) ||
         a.D % width != 0)
         return SGMV_ERR_ALIGNMENT;
-    return SGMV_OK;
+    return aligned4(a.lse, a.block_table, a.prefix_lens, a.tree_ptr, a.parents) ? SGMV_OK : SGMV_ERR_ALIGNMENT;
 }
 int check_workspace(const void *workspace, uint64_t bytes, size_t need, size_t align) {
     if (bytes < need || !workspace) return SGMV_ERR_WORKSPACE;
@@ -201,6 +202,7 @@ int sgmv_quant_attention(const sgmv_quant_attention_args *args, void *stream) {
     if (a.D > kMmaMaxD) return SGMV_ERR_UNSUPPORTED;
     if (none) return SGMV_OK;
     if (!q.k_scale || !q.v_scale) return SGMV_ERR_INVALID_ARG;
+    if (!aligned4(q.k_scale, q.v_scale)) return SGMV_ERR_ALIGNMENT;
     st = check_workspace(a.workspace, a.workspace_bytes,
                          sgmv_quant_attention_workspace_bytes(a.T, a.B, a.Hq, a.Hkv, a.D), 256);
     if (st != SGMV_OK) return st;
@@ -219,7 +221,8 @@ int sgmv_tree_verify(const sgmv_tree_verify_args *args, void *stream) {
     if (a.B == 0) return SGMV_OK;
     if (!a.tree_ptr || !a.count || !a.path || !a.token || !a.u_sample) return SGMV_ERR_INVALID_ARG;
     if (a.T > 0 && (!a.target || !a.tokens || !a.u_accept)) return SGMV_ERR_INVALID_ARG;
-    if (!aligned4(a.target) || !aligned4(a.draft)) return SGMV_ERR_ALIGNMENT;
+    if (!aligned4(a.target, a.draft, a.tokens, a.parents, a.tree_ptr, a.u_accept, a.u_sample, a.count, a.path, a.token))
+        return SGMV_ERR_ALIGNMENT;
     int *err = device_error_word();
     if (!err) return SGMV_ERR_CUDA;
     return finish("verification kernel",
@@ -247,7 +250,8 @@ int sgmv_cache_commit(const sgmv_cache_commit_args *args, void *stream) {
     settle(a.cache_head, a.Hkv, a.D);
     const int width = e4m3 ? 16 : 8;
     if (!vectors(a.k_cache, a.cache_block, a.cache_token, width) ||
-        !vectors(a.v_cache, a.cache_head, a.cache_layer, width) || a.D % width != 0)
+        !vectors(a.v_cache, a.cache_head, a.cache_layer, width) || a.D % width != 0 ||
+        !aligned4(a.block_table, a.prefix_lens, a.path, a.count))
         return SGMV_ERR_ALIGNMENT;
     if (e4m3) {  // the same bytes as half as many 16-bit values
         for (int64_t *s : {&a.cache_layer, &a.cache_block, &a.cache_token, &a.cache_head}) *s /= 2;
@@ -270,7 +274,7 @@ int sgmv_norm_rope(const sgmv_norm_rope_args *args, void *stream) {
     bool none;
     int st = check_rope(a, e4m3 ? 16 : 8, &none);
     if (st != SGMV_OK) return st;
-    if (!aligned16(n.q_weight) || !aligned16(n.k_weight)) return SGMV_ERR_ALIGNMENT;
+    if (!aligned16(n.q_weight) || !aligned16(n.k_weight) || !aligned4(n.k_scale, n.v_scale)) return SGMV_ERR_ALIGNMENT;
     if ((double)a.T * ((double)a.Hq + 2.0 * a.Hk) > kMaxRows) return SGMV_ERR_UNSUPPORTED;
     if (none) return SGMV_OK;
     uint64_t turns[kRopeMaxPairs];
@@ -315,7 +319,7 @@ int sgmv_norm_rope_grad(const sgmv_norm_rope_grad_args *args, void *stream) {
                          (a.k_weight && !vectors(a.k, a.k_token, a.k_head))))
             return SGMV_ERR_ALIGNMENT;
     }
-    if (!aligned16(a.q_weight) || !aligned16(a.k_weight) || !aligned4(a.dq_weight) || !aligned4(a.dk_weight))
+    if (!aligned16(a.q_weight) || !aligned16(a.k_weight) || !aligned4(a.dq_weight, a.dk_weight, a.positions))
         return SGMV_ERR_ALIGNMENT;
     const bool sums = a.dq_weight || a.dk_weight;
     if (sums) {
@@ -343,7 +347,8 @@ int sgmv_sample(const sgmv_sample_args *args, void *stream) {
     if (!a.token != !a.u) return SGMV_ERR_INVALID_ARG;
     if (a.T == 0 || (!a.token && !a.probs)) return SGMV_OK;
     if (!a.logits) return SGMV_ERR_INVALID_ARG;
-    if (reinterpret_cast<uintptr_t>(a.logits) % (a.dtype == SGMV_F32 ? 4 : 2) != 0 || !aligned4(a.probs))
+    if (reinterpret_cast<uintptr_t>(a.logits) % (a.dtype == SGMV_F32 ? 4 : 2) != 0 ||
+        !aligned4(a.u, a.temperature, a.top_k, a.top_p, a.min_p, a.token, a.probs))
         return SGMV_ERR_ALIGNMENT;
     if (a.probs == a.logits) return SGMV_ERR_INVALID_ARG;  // not in place
     return finish("sampling kernel", sample_launch(a, device_sms(), static_cast<cudaStream_t>(stream)), 1);
