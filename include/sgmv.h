@@ -588,11 +588,11 @@ int sgmv_norm_rope(const sgmv_norm_rope_args *args, void *stream);
  * g = scale R^T dy, r = 1 / sqrt(mean(x^2) + eps), h = w * g,
  *   dx = r (h - r^2 x mean(h * x)),   dw = sum over rows and heads of g * r x
  * (dx = g for a tensor without a weight).  q, k, dq_out, dk_out, dq, dk [T][heads][D]
- * of any token and head strides, dq and dk apart from the inputs (SGMV_ERR_INVALID_ARG
- * for the same address); q or k may be
- * left out (Hq or Hk = 0), and is not read without its weight; T * (Hq + Hk) up to 2^30.  dq_weight, dk_weight fp32 [D], written
- * (not added to); given exactly where the weight is.  Sums are fp32, joined in fp64 in a fixed order:
- * the same result in every run.
+ * of any token and head strides, dq and dk apart from all inputs and from each other
+ * (SGMV_ERR_INVALID_ARG for the same address); q or k may be left out (Hq or Hk = 0), and
+ * is not read without its weight; T * (Hq + Hk) up to 2^30.  dq_weight, dk_weight fp32 [D],
+ * written (not added to); given exactly where the weight is.  Sums are fp32, joined in fp64
+ * in a fixed order: the same result in every run.
  *   workspace: sgmv_norm_rope_grad_workspace_bytes(D) bytes, 16-byte aligned; what it
  *     holds does not matter.  Calls that run at the same time need separate ones.
  */

@@ -326,10 +326,15 @@ int sgmv_norm_rope_grad(const sgmv_norm_rope_grad_args *args, void *stream) {
         st = check_workspace(a.workspace, a.workspace_bytes, norm_rope_grad_workspace(a.D), 16);
         if (st != SGMV_OK) return st;
     }
-    // not in place
-    if (a.T > 0 && ((a.Hq > 0 && (a.dq == a.dq_out || (a.q_weight && a.dq == a.q))) ||
-                    (a.Hk > 0 && (a.dk == a.dk_out || (a.k_weight && a.dk == a.k)))))
-        return SGMV_ERR_INVALID_ARG;
+    // not in place, nor over what the other side reads or writes
+    if (a.T > 0) {
+        const void *const in[] = {a.Hq > 0 ? a.dq_out : nullptr, a.Hk > 0 ? a.dk_out : nullptr,
+                                  a.q_weight ? a.q : nullptr, a.k_weight ? a.k : nullptr};
+        for (const void *x : in)
+            if (x && ((a.Hq > 0 && x == a.dq) || (a.Hk > 0 && x == a.dk))) return SGMV_ERR_INVALID_ARG;
+        if (a.Hq > 0 && a.Hk > 0 && a.dq == a.dk) return SGMV_ERR_INVALID_ARG;
+    }
+    if (a.dq_weight && a.dq_weight == a.dk_weight) return SGMV_ERR_INVALID_ARG;
     uint64_t turns[kRopeMaxPairs];
     if ((st = turns_of(a.inv_freq, a.pairs, turns)) != SGMV_OK) return st;
     if (!device_error_word()) return SGMV_ERR_CUDA;
