@@ -527,8 +527,9 @@ int sgmv_tree_verify(const sgmv_tree_verify_args *args, void *stream);
 
 /*
  * Moves the accepted nodes' k and v to their final places in the cache (f16,
- * bf16, or e4m3 with D and the strides multiples of 16), in place: position prefix_lens[b] + d takes what position prefix_lens[b] +
- * path[b][d] held, for d < count[b].  path rows ascend (as
+ * bf16, or e4m3 with D and the strides multiples of 16), in place: position
+ * prefix_lens[b] + d takes what position prefix_lens[b] + path[b][d] held, for
+ * d < count[b].  path rows ascend (as
  * sgmv_tree_verify writes them).  Afterwards the sequence's context is
  * prefix_lens[b] + count[b] long.  layers > 1 moves the same tokens in that
  * many caches, cache_layer elements apart.
@@ -560,6 +561,8 @@ int sgmv_cache_commit(const sgmv_cache_commit_args *args, void *stream);
  * k_scale, v_scale [Hk].  Written, a value is divided by its scale (as a product
  * with the fp32 reciprocal), limited to +-448 and rounded to nearest even, once; NaN
  * stays NaN.  D and the cache's strides are multiples of 16 (SGMV_ERR_ALIGNMENT).
+ * Heads of up to 256 columns are written and moved (sgmv_norm_rope,
+ * sgmv_cache_commit), of up to 128 read (sgmv_quant_attention).
  */
 
 /*

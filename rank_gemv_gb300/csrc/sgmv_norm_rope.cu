@@ -21,7 +21,8 @@
 // too, so the result is the same in every run.  A CTA has rows of q or of k only.  8192
 // rows of 32 + 8 heads of 128: 72 us, 252 MB at 3.5 TB/s (a plain copy: 45); bounded by
 // latency, as the sums' registers leave room for 512 threads on an SM, with 32 KB of rows
-// under way.
+// under way.  With few KV heads k's CTAs set the time, whose chunks of 8 tokens leave groups
+// idle: 32 + 2 heads 120 us, 32 + 1 heads 209.
 #include <cuda_fp8.h>
 
 #include <algorithm>

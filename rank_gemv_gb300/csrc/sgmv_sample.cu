@@ -26,6 +26,11 @@
 // of the kept weights too, where min-p drops nothing (a third time: 64 to 94 us, top-p alone
 // 133 against 107).  One row of 32000, top-p: 12 to 30 us by the number of candidates, a
 // chain of passes with a cluster barrier after each; the host needs 9.
+//
+// Slower: a cut among weights of a few units, where the bounds are wide and each pass narrows
+// less (one large logit over 128255 others 24 nats below, top_p 1 - 2^-20: 128 rows 583 us, 75
+// with 0.9999); and vocabularies from 262138 tokens on, whose ranges are too long for a bit per
+// entry of a thread (128 rows, top-p alone: of 250000 tokens 404 us, of 262144 963).
 #include <algorithm>
 
 #include "sgmv_device.cuh"
@@ -158,8 +163,9 @@ __global__ void __launch_bounds__(kThreads, 2) sgmv_sample_kernel(const __grid_c
     pdl_trigger();
     if (P.sorted) {
         // More rows than run at once: those whose filters may have to look at many tokens, which
-        // take several times as long, come first (128 rows of 100277 with mixed settings: 63 us,
-        // 77 as they come; 512 rows of 32000 with probabilities: 113, 144).
+        // take several times as long, come first (128 rows of 100277, one of the sets of mixed
+        // settings: 63 us, 77 as they come; 512 rows of 32000 with probabilities, when they were
+        // weighed three times: 113, 144).  A thread looks at each row: up to 512 of them.
         bool slow = false;
         if (tid < a.T) {
             const int k = a.top_k ? a.top_k[tid] : a.top_k_all;
